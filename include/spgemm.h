@@ -231,6 +231,77 @@ const char* gemm_status_string(gemm_status s);
  * of the failing call), or "" if none.  Valid until the thread's next library call. */
 const char* gemm_last_hip_error(void);
 
+/* ---------------------------------------------------------------------------------
+ * Feed-forward operators: the gated projection with its backward pass, and products of
+ * 8-bit integers.  The conventions above hold: dense row-major matrices, device pointers
+ * owned by the caller, any element alignment (16-byte aligned rows and pointers are
+ * faster), status codes, checks before any HIP call, asynchronous on `stream`, no
+ * allocation and no synchronization, so every call may be captured into a HIP graph.
+ * Outputs must not overlap inputs (not checked).
+ *
+ * Workspaces.  Where the reduction is split over workgroups, and in the backward pass, a
+ * call needs scratch memory: gemm_*_workspace() bytes, 16-byte aligned, contents
+ * irrelevant before and undefined after.  One workspace serves every call of its plan as
+ * long as the calls follow each other on one stream; calls in flight on several streams
+ * need one each.  A NULL or too small workspace is INVALID_ARG where it is needed. */
+typedef enum {
+    GEMM_ACT_NONE = 0,       /* quantized products only: no gate, one B */
+    GEMM_ACT_SILU = 1,       /* x / (1 + exp(-x)) */
+    GEMM_ACT_GELU_TANH = 2,  /* the tanh approximation above */
+    GEMM_ACT_RELU = 3        /* max(x, 0) */
+} gemm_activation;
+
+typedef struct gemm_gated_plan* gemm_gated_handle;
+typedef struct gemm_quantized_plan* gemm_quantized_handle;
+
+/* Plan of the gated projection of a feed-forward block,
+ *     G = X Wg,  U = X Wu,  H = act(G) * U
+ * X [M,K], Wg and Wu [N,K] (GEMM_B_NK) or [K,N] (GEMM_B_KN), all fp16 or all bf16; sums
+ * and the activation in fp32, each output rounded once.  M, N, K >= 0.
+ * Errors: INVALID_ARG (out NULL, negative size, fp32 or unknown dtype, unknown layout, act
+ * NONE or unknown), UNSUPPORTED (a size above 2^30). */
+gemm_status gemm_gated_create(gemm_gated_handle* out, int64_t M, int64_t N, int64_t K, gemm_dtype dtype,
+                              gemm_b_layout layout, gemm_activation act);
+/* Bytes of workspace that gemm_gated_run and gemm_gated_backward need (-1: NULL handle). */
+int64_t gemm_gated_workspace(gemm_gated_handle h);
+/* H [M,N]; G and U [M,N] receive the pre-activations that the backward pass reads, rounded
+ * to the plan's type; both NULL (serving) or both given (training). */
+gemm_status gemm_gated_run(gemm_gated_handle h, const void* X, const void* Wg, const void* Wu, void* H, void* G,
+                           void* U, void* workspace, int64_t workspace_bytes, hipStream_t stream);
+/* From dH [M,N] and the forward pass's operands, G and U:
+ *     dU = dH * act(G), dG = dH * U * act'(G)      (act'(0) = 0 for ReLU)
+ *     dX = dG Wg^T + dU Wu^T, dWg = X^T dG, dWu = X^T dU   (stored as X, Wg and Wu are)
+ * dG and dU are rounded to the plan's type; the sums are fp32, each gradient rounded once;
+ * results do not vary from run to run.  Sums over nothing (M = 0: the weights' gradients,
+ * N = 0: dX) write zeros. */
+gemm_status gemm_gated_backward(gemm_gated_handle h, const void* dH, const void* X, const void* Wg, const void* Wu,
+                                const void* G, const void* U, void* dX, void* dWg, void* dWu, void* workspace,
+                                int64_t workspace_bytes, hipStream_t stream);
+gemm_status gemm_gated_destroy(gemm_gated_handle h);
+
+/* Plan of a product of 8-bit integers,
+ *     C[m,n] = (sum_k A[m,k] B[n,k]) * scale_a[m] * scale_b[n]
+ * A [M,K] with a scale per row (token), B [N,K] with a scale per row (output channel),
+ * exact int32 sums, C [M,N] fp16, bf16 or fp32, rounded once.  With an activation:
+ * C = act(C1) * C2, C1 from (B, scale_b) and C2 from (B2, scale_b2).
+ * Errors: INVALID_ARG, UNSUPPORTED (K > 131071, where the sums could overflow). */
+gemm_status gemm_quantized_create(gemm_quantized_handle* out, int64_t M, int64_t N, int64_t K, gemm_dtype out_dtype,
+                                  gemm_activation act);
+int64_t gemm_quantized_workspace(gemm_quantized_handle h);
+/* B2 and scale_b2 are NULL when the plan has no activation. */
+gemm_status gemm_quantized_run(gemm_quantized_handle h, const int8_t* A, const float* scale_a, const int8_t* B,
+                               const float* scale_b, const int8_t* B2, const float* scale_b2, void* C,
+                               void* workspace, int64_t workspace_bytes, hipStream_t stream);
+gemm_status gemm_quantized_destroy(gemm_quantized_handle h);
+
+/* Each row of X [rows,K] (fp16, bf16 or fp32) brought to 8 bits:
+ *     scale[m] = max_k |X[m,k]| / 127,  A[m,k] = round(127 X[m,k] / max_k |X[m,k]|)
+ * rounded to nearest, ties to even, exactly.  A row of zeros (or K = 0) gives zeros and
+ * scale 0; a row with an infinity or a NaN gives zeros and an infinite or NaN scale, so
+ * that its products are NaN. */
+gemm_status gemm_quantize_rows(const void* X, gemm_dtype dtype, int64_t rows, int64_t K, int8_t* A, float* scale,
+                               hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,5 +1,5 @@
-"""Python binding of the MI355X software-pipelined tiled GEMM (C ABI in include/spgemm.h)
-and of the standalone elementwise GELU (include/spgelu.h).
+"""Python binding of the MI355X software-pipelined tiled GEMM and the feed-forward operators
+(C ABI in include/spgemm.h) and of the standalone elementwise GELU (include/spgelu.h).
 
 Argument marshalling only: every step of C = epi(A . B) runs in the HIP
 kernels of ``libspgemm.so``.  PyTorch is used by callers for device memory and
@@ -29,6 +29,7 @@ STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "out of memory",
 DTYPES = {"f16": 0, "bf16": 1, "f32": 2}
 B_LAYOUTS = {"kn": 0, "nk": 1}
 EPILOGUES = {"none": 0, "gelu_tanh": 1, "relu": 2}
+ACTIVATIONS = {"none": 0, "silu": 1, "gelu_tanh": 2, "relu": 3}
 STAGING = {0: "direct", 1: "vgpr", 2: "direct-spread", 3: "producer-wave", 4: "direct-a-deep",
            5: "direct-late-release", 6: "direct-b-deep", 7: "vgpr-any-alignment"}
 
@@ -77,7 +78,10 @@ class TileConfig(ctypes.Structure):
 EXPORTED = ("gemm_create", "gemm_run", "gemm_destroy", "gemm_get_config", "gemm_launch_config",
             "gemm_autotune",
             "gemm_num_configs", "gemm_list_config", "gemm_lds_bytes", "gemm_status_string",
-            "gemm_last_hip_error", "gemm_wait_timeouts", "gelu_run")
+            "gemm_last_hip_error", "gemm_wait_timeouts", "gelu_run",
+            "gemm_gated_create", "gemm_gated_workspace", "gemm_gated_run", "gemm_gated_backward",
+            "gemm_gated_destroy", "gemm_quantized_create", "gemm_quantized_workspace",
+            "gemm_quantized_run", "gemm_quantized_destroy", "gemm_quantize_rows")
 
 _lib = None
 _poison_lib = None
@@ -138,6 +142,20 @@ def _load(path):
     L.gemm_wait_timeouts.argtypes = [ctypes.POINTER(ctypes.c_uint32), i32]
     L.gelu_run.restype = ctypes.c_int
     L.gelu_run.argtypes = [vp, vp, i64, ctypes.c_int, vp]
+    en = ctypes.c_int
+    for name, res, args in (
+            ("gemm_gated_create", en, [ctypes.POINTER(vp), i64, i64, i64, en, en, en]),
+            ("gemm_gated_workspace", i64, [vp]),
+            ("gemm_gated_run", en, [vp] * 8 + [i64, vp]),
+            ("gemm_gated_backward", en, [vp] * 11 + [i64, vp]),
+            ("gemm_gated_destroy", en, [vp]),
+            ("gemm_quantized_create", en, [ctypes.POINTER(vp), i64, i64, i64, en, en]),
+            ("gemm_quantized_workspace", i64, [vp]),
+            ("gemm_quantized_run", en, [vp] * 9 + [i64, vp]),
+            ("gemm_quantized_destroy", en, [vp]),
+            ("gemm_quantize_rows", en, [vp, en, i64, i64, vp, vp, vp])):
+        f = getattr(L, name)
+        f.restype, f.argtypes = res, args
     return L
 
 
@@ -244,6 +262,225 @@ def gelu_run(x, y, n: int, dtype: str = "bf16", stream=None) -> None:
     """y[i] = gelu(x[i]) for n contiguous elements of dtype (include/spgelu.h)."""
     st = lib().gelu_run(_ptr(x), _ptr(y), n, DTYPES[dtype], _stream(stream, x, y))
     _check(st, "gelu_run")
+
+
+# ---- the feed-forward operators --------------------------------------------------------
+
+def gemm_gated_create(M: int, N: int, K: int, dtype: str = "bf16", layout: str = "nk",
+                      act: str = "silu") -> int:
+    h = ctypes.c_void_p()
+    st = lib().gemm_gated_create(ctypes.byref(h), M, N, K, DTYPES[dtype], B_LAYOUTS[layout],
+                                 ACTIVATIONS[act])
+    _check(st, "gemm_gated_create")
+    return int(h.value)
+
+
+def gemm_gated_workspace(handle: int) -> int:
+    return int(lib().gemm_gated_workspace(handle))
+
+
+def gemm_gated_run(handle: int, X, Wg, Wu, H, G=None, U=None, workspace=None,
+                   workspace_bytes: Optional[int] = None, stream=None) -> None:
+    st = lib().gemm_gated_run(handle, _ptr(X), _ptr(Wg), _ptr(Wu), _ptr(H), _ptr(G), _ptr(U),
+                              _ptr(workspace), _nbytes(workspace, workspace_bytes),
+                              _stream(stream, X, H))
+    _check(st, "gemm_gated_run")
+
+
+def gemm_gated_backward(handle: int, dH, X, Wg, Wu, G, U, dX, dWg, dWu, workspace=None,
+                        workspace_bytes: Optional[int] = None, stream=None) -> None:
+    st = lib().gemm_gated_backward(handle, _ptr(dH), _ptr(X), _ptr(Wg), _ptr(Wu), _ptr(G), _ptr(U),
+                                   _ptr(dX), _ptr(dWg), _ptr(dWu), _ptr(workspace),
+                                   _nbytes(workspace, workspace_bytes), _stream(stream, dH, X, dX))
+    _check(st, "gemm_gated_backward")
+
+
+def gemm_gated_destroy(handle: Optional[int]) -> None:
+    _check(lib().gemm_gated_destroy(handle), "gemm_gated_destroy")
+
+
+def gemm_quantized_create(M: int, N: int, K: int, out_dtype: str = "bf16", act: str = "none") -> int:
+    h = ctypes.c_void_p()
+    st = lib().gemm_quantized_create(ctypes.byref(h), M, N, K, DTYPES[out_dtype], ACTIVATIONS[act])
+    _check(st, "gemm_quantized_create")
+    return int(h.value)
+
+
+def gemm_quantized_workspace(handle: int) -> int:
+    return int(lib().gemm_quantized_workspace(handle))
+
+
+def gemm_quantized_run(handle: int, A, scale_a, B, scale_b, C, B2=None, scale_b2=None, workspace=None,
+                       workspace_bytes: Optional[int] = None, stream=None) -> None:
+    st = lib().gemm_quantized_run(handle, _ptr(A), _ptr(scale_a), _ptr(B), _ptr(scale_b), _ptr(B2),
+                                  _ptr(scale_b2), _ptr(C), _ptr(workspace),
+                                  _nbytes(workspace, workspace_bytes), _stream(stream, A, C))
+    _check(st, "gemm_quantized_run")
+
+
+def gemm_quantized_destroy(handle: Optional[int]) -> None:
+    _check(lib().gemm_quantized_destroy(handle), "gemm_quantized_destroy")
+
+
+def gemm_quantize_rows(X, A, scale, stream=None, dtype: Optional[str] = None,
+                       shape: Optional[tuple] = None) -> None:
+    """Quantise the rows of X into A (int8) and scale (fp32).  For tensors the type and the
+    [rows, K] shape are X's; with raw device pointers they are given."""
+    if dtype is None or shape is None:
+        t = _torch_names()
+        dtype = t[X.dtype] if dtype is None else dtype
+        if shape is None:
+            if X.dim() < 1:
+                raise GemmError(1, "gemm_quantize_rows: X needs at least one dimension")
+            K = X.shape[-1]
+            shape = (X.numel() // K if K else _rows_of_empty(X.shape), K)
+        _expect("gemm_quantize_rows", X=(X, dtype, tuple(X.shape)), A=(A, "i8", tuple(X.shape)),
+                scale=(scale, "f32", tuple(X.shape[:-1])))
+    st = lib().gemm_quantize_rows(_ptr(X), DTYPES[dtype], shape[0], shape[1], _ptr(A), _ptr(scale),
+                                  _stream(stream, X, A))
+    _check(st, "gemm_quantize_rows")
+
+
+def _rows_of_empty(shape) -> int:
+    n = 1
+    for d in shape[:-1]:
+        n *= d
+    return n
+
+
+def _nbytes(workspace, given: Optional[int]) -> int:
+    if given is not None:
+        return given
+    if workspace is None or isinstance(workspace, int):
+        return 0
+    return workspace.numel() * workspace.element_size()
+
+
+_names = None
+
+
+def _torch_names():
+    """torch dtype -> this library's name."""
+    global _names
+    if _names is None:
+        import torch
+        _names = {torch.float16: "f16", torch.bfloat16: "bf16", torch.float32: "f32", torch.int8: "i8"}
+    return _names
+
+
+def _expect(what: str, **tensors) -> None:
+    """Check tensors (raw pointers and None pass) against (tensor, dtype, shape): the kernels
+    read dense memory of exactly that shape, so anything else is refused here."""
+    names = _torch_names()
+    device = None
+    for name, (t, dtype, shape) in tensors.items():
+        if t is None or isinstance(t, int):
+            continue
+        if t.shape != shape:
+            raise GemmError(1, f"{what}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+        if names.get(t.dtype) != dtype:
+            raise GemmError(1, f"{what}: {name} is {t.dtype}, not {dtype}")
+        if not t.is_contiguous():
+            raise GemmError(1, f"{what}: {name} is not contiguous")
+        if not t.is_cuda:
+            raise GemmError(1, f"{what}: {name} is not on a GPU")
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            raise GemmError(1, f"{what}: {name} is on another device")
+
+
+class Gated:
+    """The gated projection H = act(X Wg) * (X Wu) of a feed-forward block, and its backward
+    pass (gemm_gated_* in include/spgemm.h).
+
+    X [M,K]; Wg, Wu [N,K] ("nk") or [K,N] ("kn"); H, G, U [M,N].  Pass G and U to keep the
+    pre-activations for ``backward``.  ``workspace`` is a uint8 tensor of at least
+    ``workspace_bytes()``; calls in flight on different streams need one each."""
+
+    def __init__(self, M, N, K, dtype="bf16", layout="nk", act="silu"):
+        self.handle = 0
+        self.M, self.N, self.K = M, N, K
+        self.dtype, self.layout, self.act = dtype, layout, act
+        self.handle = gemm_gated_create(M, N, K, dtype, layout, act)
+        self._x, self._h = (M, K), (M, N)
+        self._w = (N, K) if layout == "nk" else (K, N)
+
+    def workspace_bytes(self) -> int:
+        return gemm_gated_workspace(self.handle)
+
+    def __call__(self, X, Wg, Wu, H, G=None, U=None, workspace=None, stream=None):
+        d = self.dtype
+        _expect("Gated", X=(X, d, self._x), Wg=(Wg, d, self._w), Wu=(Wu, d, self._w),
+                H=(H, d, self._h), G=(G, d, self._h), U=(U, d, self._h))
+        gemm_gated_run(self.handle, X, Wg, Wu, H, G, U, workspace, stream=stream)
+        return H
+
+    def backward(self, dH, X, Wg, Wu, G, U, dX, dWg, dWu, workspace=None, stream=None):
+        d = self.dtype
+        _expect("Gated.backward", dH=(dH, d, self._h), X=(X, d, self._x), Wg=(Wg, d, self._w),
+                Wu=(Wu, d, self._w), G=(G, d, self._h), U=(U, d, self._h), dX=(dX, d, self._x),
+                dWg=(dWg, d, self._w), dWu=(dWu, d, self._w))
+        gemm_gated_backward(self.handle, dH, X, Wg, Wu, G, U, dX, dWg, dWu, workspace, stream=stream)
+        return dX, dWg, dWu
+
+    def close(self):
+        if self.handle:
+            gemm_gated_destroy(self.handle)
+            self.handle = 0
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class QuantizedGemm:
+    """C = (A B^T) scaled by row and by column, int8 operands (gemm_quantized_* in
+    include/spgemm.h); with an activation C = act(C1) * C2 from B and B2.
+
+    A [M,K] int8 with scale_a [M]; B, B2 [N,K] int8 with scale_b, scale_b2 [N]; C [M,N]."""
+
+    def __init__(self, M, N, K, out_dtype="bf16", act="none"):
+        self.handle = 0
+        self.M, self.N, self.K = M, N, K
+        self.out_dtype, self.act = out_dtype, act
+        self.handle = gemm_quantized_create(M, N, K, out_dtype, act)
+
+    def workspace_bytes(self) -> int:
+        return gemm_quantized_workspace(self.handle)
+
+    def __call__(self, A, scale_a, B, scale_b, C, B2=None, scale_b2=None, workspace=None, stream=None):
+        M, N, K = self.M, self.N, self.K
+        _expect("QuantizedGemm", A=(A, "i8", (M, K)), scale_a=(scale_a, "f32", (M,)),
+                B=(B, "i8", (N, K)), scale_b=(scale_b, "f32", (N,)), C=(C, self.out_dtype, (M, N)),
+                B2=(B2, "i8", (N, K)), scale_b2=(scale_b2, "f32", (N,)))
+        gemm_quantized_run(self.handle, A, scale_a, B, scale_b, C, B2, scale_b2, workspace, stream=stream)
+        return C
+
+    def close(self):
+        if self.handle:
+            gemm_quantized_destroy(self.handle)
+            self.handle = 0
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
 
 
 class Gemm:

@@ -4,7 +4,9 @@ The kernel instantiations listed in csrc/variants.inc are spread over translatio
 units by the first field of each line: csrc/gemm_unit.hip is compiled once per unit
 number (with -DSPG_UNIT_IS_<n>=~,1 selecting that unit's lines), so the units compile
 in parallel.  csrc/gemm.hip holds the GEMM's host side (C ABI, variant table) and
-csrc/gelu.hip the standalone elementwise GELU (include/spgelu.h).
+csrc/gelu.hip the standalone elementwise GELU (include/spgelu.h).  The feed-forward
+operators are csrc/product.hip (host side) and csrc/product_unit.hip, compiled once per
+element type, product and copy mode.
 """
 
 from __future__ import annotations
@@ -49,6 +51,14 @@ def units() -> list:
     return sorted(found)
 
 
+def product_units() -> list:
+    """(element type, product, copy mode) of every product_unit.hip object: the enums of
+    csrc/product_kernels.hpp and csrc/product_launch.hpp (products 0-4 in fp16 and bf16,
+    5 and 6 in int8; each with direct copies and register-staged)."""
+    pairs = [(et, p) for p in range(5) for et in (0, 1)] + [(2, 5), (2, 6)]
+    return [(et, p, reg) for et, p in pairs for reg in (0, 1)]
+
+
 def build(out: str = OUT, extra=(), poison: bool = False) -> str:
     """Compile the library; poison=True builds the poison library from POISON_UNITS."""
     unit_src = os.path.join(CSRC, "gemm_unit.hip")
@@ -57,7 +67,11 @@ def build(out: str = OUT, extra=(), poison: bool = False) -> str:
     pdef = ["-DSPG_POISON"] if poison else []
     # (source, object name, defines): the host side, the GELU, and one object per unit
     jobs = [(os.path.join(CSRC, "gemm.hip"), "gemm.o", pdef + keep),
-            (os.path.join(CSRC, "gelu.hip"), "gelu.o", [])]
+            (os.path.join(CSRC, "gelu.hip"), "gelu.o", []),
+            (os.path.join(CSRC, "product.hip"), "product.o", pdef)]
+    jobs += [(os.path.join(CSRC, "product_unit.hip"), f"product_unit_{et}_{p}_{reg}.o",
+              pdef + [f"-DSPG_ET={et}", f"-DSPG_PRODUCT={p}", f"-DSPG_REG={reg}"])
+             for et, p, reg in product_units()]
     jobs += [(unit_src, f"gemm_unit{u}.o", pdef + [f"-DSPG_UNIT_IS_{u}=~,1"]) for u in us]
     inc = ["-I", os.path.join(ROOT, "include"), "-I", CSRC]
     with tempfile.TemporaryDirectory(prefix="spgemm_build_") as tmp:

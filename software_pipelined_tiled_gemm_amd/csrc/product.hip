@@ -1,0 +1,453 @@
+// C ABI of the feed-forward operators (declared in include/spgemm.h): the gated projection
+// and its backward pass, products of int8 operands, quantisation of rows.
+//
+// Host side: argument validation (before any HIP call), the choice of kernel, tile and
+// parts of the reduction from the shape, the workspace layout and the launches.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <new>
+
+#include "errors.hpp"
+#include "product_launch.hpp"
+#include "spgemm.h"
+
+using spg::ProductArgs;
+
+namespace {
+
+constexpr int64_t kAlign = 256;   // sections of a workspace
+int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+bool is16(const void* p) { return (uintptr_t)p % 16 == 0; }
+
+gemm_status launched() {
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? GEMM_OK : spg::hip_fail(e);
+}
+
+// One product of a plan: tile class and parts of the reduction.
+struct Shape {
+    int64_t M, N;      // of one result
+    int64_t kt;        // k-tiles of the whole sum
+    int zm, zn;        // results stacked along rows / columns
+    int mats;          // B matrices side by side in a tile (2: gated)
+    double bytes;      // operands and results, read or written once
+};
+struct Tiling {
+    int tile, split;
+    int64_t kt_part;
+};
+
+// Estimated microseconds of a tile class and a number of parts: rounds of the 256 CUs
+// (each tile class fills a CU's LDS, so one workgroup at a time) times the k-tiles of a
+// part, against the time memory needs; parts add their sums' traffic and a launch.
+Tiling choose(const Shape& s, bool reg) {
+    const double kt_us[spg::kTiles] = {1.40, 0.45, 0.30};
+    const double fixed_us[spg::kTiles] = {9.0, 5.0, 4.0};
+    Tiling best{spg::kTileSmall, 1, s.kt};
+    double best_t = -1.0;
+    for (int t = 0; t < spg::kTiles; ++t) {
+        if (reg && t == spg::kTileBig) continue;   // register staging: no 256x256 tile
+        const int64_t tiles = ceil_div(s.M, spg::kTileM[t]) * s.zm * ceil_div(s.N, spg::kTileN[t] / s.mats) * s.zn;
+        for (int64_t split = 1; split <= 64 && split <= s.kt; ++split) {
+            const int64_t part = ceil_div(s.kt, split);
+            if (split > 1 && (part < 4 || ceil_div(s.kt, part) != split)) continue;
+            const double rounds = (double)ceil_div(tiles * split, 256);
+            double us = rounds * (kt_us[t] * (reg ? 1.3 : 1.0) * (double)part + fixed_us[t]);
+            us = std::max(us, s.bytes / 5.0e6);
+            if (split > 1) us += 3.0 + 2.0 * 4.0 * (double)split * s.M * s.zm * s.N * s.zn * s.mats / 4.0e6;
+            if (best_t < 0 || us < best_t) {
+                best_t = us;
+                best = Tiling{t, (int)split, part};
+            }
+        }
+    }
+    return best;
+}
+
+int64_t part_ld(const Shape& s) { return up(s.N, 4) * s.mats * s.zn; }
+int64_t part_bytes(const Shape& s, const Tiling& t) {
+    return t.split > 1 ? up((int64_t)t.split * s.M * s.zm * part_ld(s) * 4, kAlign) : 0;
+}
+
+template <int P, bool REG>
+void launch_type(int et, int tile, const ProductArgs& a, dim3 grid, hipStream_t st) {
+    if constexpr (P == spg::kInt8 || P == spg::kInt8Gated) spg::launch_product<spg::kElI8, P, REG>(tile, a, grid, st);
+    else if (et == spg::kElBF16) spg::launch_product<spg::kElBF16, P, REG>(tile, a, grid, st);
+    else spg::launch_product<spg::kElF16, P, REG>(tile, a, grid, st);
+}
+
+template <int P>
+void launch_mode(int et, bool reg, int tile, const ProductArgs& a, dim3 grid, hipStream_t st) {
+    if (reg) launch_type<P, true>(et, tile, a, grid, st);
+    else launch_type<P, false>(et, tile, a, grid, st);
+}
+
+void launch_tiled(int product, int et, bool reg, int tile, const ProductArgs& a, dim3 grid, hipStream_t st) {
+    switch (product) {
+        case spg::kGatedNK: return launch_mode<spg::kGatedNK>(et, reg, tile, a, grid, st);
+        case spg::kGatedKN: return launch_mode<spg::kGatedKN>(et, reg, tile, a, grid, st);
+        case spg::kGradXNK: return launch_mode<spg::kGradXNK>(et, reg, tile, a, grid, st);
+        case spg::kGradXKN: return launch_mode<spg::kGradXKN>(et, reg, tile, a, grid, st);
+        case spg::kGradW: return launch_mode<spg::kGradW>(et, reg, tile, a, grid, st);
+        case spg::kInt8: return launch_mode<spg::kInt8>(et, reg, tile, a, grid, st);
+        default: return launch_mode<spg::kInt8Gated>(et, reg, tile, a, grid, st);
+    }
+}
+
+// The tiled product and, for a split reduction, the sum of its parts.
+gemm_status run_tiled(int product, int et, bool reg, const Shape& s, const Tiling& t, ProductArgs a, void* parts,
+                      hipStream_t st) {
+    a.zm = s.zm;
+    a.zn = s.zn;
+    a.tiles_m = (int32_t)ceil_div(s.M, spg::kTileM[t.tile]);
+    a.tiles_n = (int32_t)ceil_div(s.N, spg::kTileN[t.tile] / s.mats);
+    a.group_m = 4;
+    a.split = t.split;
+    a.kt_part = (int32_t)t.kt_part;
+    a.part = t.split > 1 ? (float*)parts : nullptr;
+    a.ldp = part_ld(s);
+    const int64_t wgs = (int64_t)a.tiles_m * a.zm * a.tiles_n * a.zn * t.split;
+    launch_tiled(product, et, reg, t.tile, a, dim3((unsigned)wgs), st);
+    gemm_status e = launched();
+    if (e != GEMM_OK || t.split == 1) return e;
+    const int64_t quads = s.M * s.zm * (up(s.N, 4) / 4) * s.zn;
+    const dim3 grid((unsigned)ceil_div(quads, 256));
+    const bool dual = s.mats == 2;
+    if (et == spg::kElI8) {
+        if (dual) hipLaunchKernelGGL((spg::sum_parts<spg::kElI8, true>), grid, dim3(256), 0, st, a);
+        else hipLaunchKernelGGL((spg::sum_parts<spg::kElI8, false>), grid, dim3(256), 0, st, a);
+    } else if (et == spg::kElBF16) {
+        if (dual) hipLaunchKernelGGL((spg::sum_parts<spg::kElBF16, true>), grid, dim3(256), 0, st, a);
+        else hipLaunchKernelGGL((spg::sum_parts<spg::kElBF16, false>), grid, dim3(256), 0, st, a);
+    } else {
+        if (dual) hipLaunchKernelGGL((spg::sum_parts<spg::kElF16, true>), grid, dim3(256), 0, st, a);
+        else hipLaunchKernelGGL((spg::sum_parts<spg::kElF16, false>), grid, dim3(256), 0, st, a);
+    }
+    return launched();
+}
+
+template <int ET, bool DUAL>
+void stream_rows(const ProductArgs& a, hipStream_t st) {
+    const dim3 grid((unsigned)ceil_div(a.N, 16));
+    if (a.M <= 16) hipLaunchKernelGGL((spg::stream_kernel<ET, DUAL, 1, 1, 8, 8>), grid, dim3(512), 0, st, a);
+    else if (a.M <= 32) hipLaunchKernelGGL((spg::stream_kernel<ET, DUAL, 2, 1, 8, 4>), grid, dim3(512), 0, st, a);
+    else hipLaunchKernelGGL((spg::stream_kernel<ET, DUAL, 4, 1, 8, 4>), grid, dim3(512), 0, st, a);
+}
+
+template <int ET, bool DUAL>
+gemm_status run_simple(const spg::SimpleArgs& a, hipStream_t st) {
+    const int64_t n = std::min<int64_t>(ceil_div((int64_t)a.p.M * a.p.N, 256), 1 << 16);
+    hipLaunchKernelGGL((spg::simple_product<ET, DUAL>), dim3((unsigned)n), dim3(256), 0, st, a);
+    return launched();
+}
+
+constexpr int64_t kStreamRows = 64;
+// Rows of operands are addressed by 32-bit offsets below 2^31: 256 of them fit up to here.
+constexpr int64_t kMaxRowBytes = ((int64_t)1 << 23) - 128;
+
+}  // namespace
+
+struct gemm_gated_plan {
+    int64_t M, N, K;
+    int et;
+    bool nk;
+    int act;
+    bool simple, simple_back;
+    int64_t np;              // columns of dG and of dU in the workspace
+    Shape fwd, dx, dw;
+    Tiling t_fwd[2], t_dx[2], t_dw[2];   // [register-staged]
+    int64_t ws_fwd, ws_back, off_part;
+};
+
+struct gemm_quantized_plan {
+    int64_t M, N, K;
+    int out, act;
+    bool simple;
+    Shape s;
+    Tiling t[2];
+    int64_t ws;
+};
+
+extern "C" {
+
+gemm_status gemm_gated_create(gemm_gated_handle* out, int64_t M, int64_t N, int64_t K, gemm_dtype dtype,
+                              gemm_b_layout layout, gemm_activation act) {
+    if (!out) return GEMM_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (M < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_ARG;
+    if (dtype != GEMM_F16 && dtype != GEMM_BF16) return GEMM_ERR_INVALID_ARG;
+    if (layout != GEMM_B_KN && layout != GEMM_B_NK) return GEMM_ERR_INVALID_ARG;
+    if (act != GEMM_ACT_SILU && act != GEMM_ACT_GELU_TANH && act != GEMM_ACT_RELU) return GEMM_ERR_INVALID_ARG;
+    const int64_t lim = INT32_MAX / 2 - 512;
+    if (M > lim || N > lim || K > lim) return GEMM_ERR_UNSUPPORTED;
+    gemm_gated_plan* p = new (std::nothrow) gemm_gated_plan;
+    if (!p) return GEMM_ERR_OUT_OF_MEMORY;
+    p->M = M;
+    p->N = N;
+    p->K = K;
+    p->et = dtype == GEMM_BF16 ? spg::kElBF16 : spg::kElF16;
+    p->nk = layout == GEMM_B_NK;
+    p->act = (int)act;
+    const double m = (double)M, n = (double)N, k = (double)K;
+    const bool empty = M == 0 || N == 0;
+    // the tiled kernel needs 16 bytes of every row it copies, and 32-bit offsets
+    p->simple = empty || K < 8 || (!p->nk && N < 8) || K * 2 > kMaxRowBytes || (!p->nk && N * 2 > kMaxRowBytes);
+    p->np = up(N, 64);
+    p->simple_back = p->simple || p->np * 4 > kMaxRowBytes || K == 0;
+    p->fwd = Shape{M, N, ceil_div(K, 64), 1, 1, 2, 2 * (m * k + 2 * n * k + m * n)};
+    p->dx = Shape{M, K, 2 * ceil_div(N, 64), 1, 1, 1, 2 * (2 * m * n + 2 * n * k + m * k)};
+    p->dw = p->nk ? Shape{N, K, ceil_div(M, 64), 2, 1, 1, 2 * (2 * m * n + 2 * n * k + m * k)}
+                  : Shape{K, N, ceil_div(M, 64), 1, 2, 1, 2 * (2 * m * n + 2 * n * k + m * k)};
+    p->ws_fwd = 0;
+    int64_t parts = 0;
+    for (int r = 0; r < 2; ++r) {
+        if (!p->simple) {
+            p->t_fwd[r] = choose(p->fwd, r == 1);
+            p->ws_fwd = std::max(p->ws_fwd, part_bytes(p->fwd, p->t_fwd[r]));
+        }
+        if (!p->simple_back) {
+            p->t_dx[r] = choose(p->dx, r == 1);
+            p->t_dw[r] = choose(p->dw, r == 1);
+            parts = std::max(parts, std::max(part_bytes(p->dx, p->t_dx[r]), part_bytes(p->dw, p->t_dw[r])));
+        }
+    }
+    p->off_part = up(M * p->np * 4, kAlign);
+    p->ws_back = p->off_part + parts;
+    *out = p;
+    return GEMM_OK;
+}
+
+int64_t gemm_gated_workspace(gemm_gated_handle h) { return h ? std::max(h->ws_fwd, h->ws_back) : -1; }
+
+gemm_status gemm_gated_run(gemm_gated_handle h, const void* X, const void* Wg, const void* Wu, void* H, void* G,
+                           void* U, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+    if (!h || (G == nullptr) != (U == nullptr)) return GEMM_ERR_INVALID_ARG;
+    if (h->M == 0 || h->N == 0) return GEMM_OK;
+    if (!H || (h->K > 0 && (!X || !Wg || !Wu))) return GEMM_ERR_INVALID_ARG;
+    ProductArgs a{};
+    a.A[0] = (const char*)X;
+    a.B[0] = (const char*)Wg;
+    a.B[1] = (const char*)Wu;
+    a.C[0] = H;
+    a.G = G;
+    a.U = U;
+    a.M = (int32_t)h->M;
+    a.N = (int32_t)h->N;
+    a.K = (int32_t)h->K;
+    a.lda = h->K * 2;
+    a.ldb = (h->nk ? h->K : h->N) * 2;
+    a.b_cols = (int32_t)h->N;
+    a.segments = 1;
+    a.act = h->act;
+    if (h->simple) {
+        spg::SimpleArgs s{a, h->K, 1, h->nk ? h->K : 1, h->nk ? 1 : h->N, 0};
+        return h->et == spg::kElBF16 ? run_simple<spg::kElBF16, true>(s, stream) : run_simple<spg::kElF16, true>(s, stream);
+    }
+    if (h->nk && h->M <= kStreamRows) {
+        if (h->et == spg::kElBF16) stream_rows<spg::kElBF16, true>(a, stream);
+        else stream_rows<spg::kElF16, true>(a, stream);
+        return launched();
+    }
+    const bool reg = a.lda % 16 != 0 || a.ldb % 16 != 0 || !is16(X) || !is16(Wg) || !is16(Wu);
+    const Tiling& t = h->t_fwd[reg];
+    if (t.split > 1 && (!workspace || (uintptr_t)workspace % 16 != 0 || workspace_bytes < part_bytes(h->fwd, t)))
+        return GEMM_ERR_INVALID_ARG;
+    return run_tiled(h->nk ? spg::kGatedNK : spg::kGatedKN, h->et, reg, h->fwd, t, a, workspace, stream);
+}
+
+gemm_status gemm_gated_backward(gemm_gated_handle h, const void* dH, const void* X, const void* Wg, const void* Wu,
+                                const void* G, const void* U, void* dX, void* dWg, void* dWu, void* workspace,
+                                int64_t workspace_bytes, hipStream_t stream) {
+    if (!h) return GEMM_ERR_INVALID_ARG;
+    const int64_t M = h->M, N = h->N, K = h->K;
+    if (K == 0 || (M == 0 && N == 0)) return GEMM_OK;      // every gradient is empty
+    if ((M > 0 && !dX) || (N > 0 && (!dWg || !dWu))) return GEMM_ERR_INVALID_ARG;
+    if (M > 0 && N > 0) {
+        if (!dH || !X || !Wg || !Wu || !G || !U) return GEMM_ERR_INVALID_ARG;
+        if (!workspace || (uintptr_t)workspace % 16 != 0 || workspace_bytes < h->ws_back) return GEMM_ERR_INVALID_ARG;
+    }
+    const bool bf = h->et == spg::kElBF16;
+    uint16_t* D = (uint16_t*)workspace;
+    void* parts = (char*)workspace + h->off_part;
+    if (M > 0 && N > 0) {
+        const int64_t items = M * (h->np / 8);
+        const dim3 grid((unsigned)ceil_div(items, 256));
+        if (bf) hipLaunchKernelGGL((spg::gated_slopes<true>), grid, dim3(256), 0, stream, (const uint16_t*)dH,
+                                   (const uint16_t*)G, (const uint16_t*)U, D, (int)M, (int)N, (int)h->np, h->act);
+        else hipLaunchKernelGGL((spg::gated_slopes<false>), grid, dim3(256), 0, stream, (const uint16_t*)dH,
+                                (const uint16_t*)G, (const uint16_t*)U, D, (int)M, (int)N, (int)h->np, h->act);
+        const gemm_status e = launched();
+        if (e != GEMM_OK) return e;
+    }
+    // dX = [dG dU] . [Wg; Wu]: one sum over both segments
+    if (M > 0) {
+        ProductArgs a{};
+        a.A[0] = (const char*)D;
+        a.B[0] = (const char*)Wg;
+        a.B[1] = (const char*)Wu;
+        a.C[0] = dX;
+        a.M = (int32_t)M;
+        a.N = (int32_t)K;
+        a.K = (int32_t)N;
+        a.lda = h->np * 4;
+        a.ldb = (h->nk ? K : N) * 2;
+        a.b_cols = (int32_t)K;
+        a.segments = 2;
+        gemm_status e;
+        if (h->simple_back) {
+            spg::SimpleArgs s{a, 2 * h->np, 1, h->nk ? 1 : N, h->nk ? K : 1, h->np};
+            e = bf ? run_simple<spg::kElBF16, false>(s, stream) : run_simple<spg::kElF16, false>(s, stream);
+        } else {
+            const bool reg = a.ldb % 16 != 0 || !is16(Wg) || !is16(Wu);
+            e = run_tiled(h->nk ? spg::kGradXNK : spg::kGradXKN, h->et, reg, h->dx, h->t_dx[reg], a, parts, stream);
+        }
+        if (e != GEMM_OK) return e;
+    }
+    // dWg, dWu: [N,K] weights dG^T X and dU^T X, [K,N] weights X^T dG and X^T dU
+    if (N > 0) {
+        const char* D0 = (const char*)D;
+        const char* D1 = (const char*)(D + h->np);
+        ProductArgs a{};
+        a.A[0] = h->nk ? D0 : (const char*)X;
+        a.A[1] = h->nk ? D1 : (const char*)X;
+        a.B[0] = h->nk ? (const char*)X : D0;
+        a.B[1] = h->nk ? (const char*)X : D1;
+        a.C[0] = dWg;
+        a.C[1] = dWu;
+        a.M = (int32_t)(h->nk ? N : K);
+        a.N = (int32_t)(h->nk ? K : N);
+        a.K = (int32_t)M;
+        a.lda = h->nk ? h->np * 4 : K * 2;
+        a.ldb = h->nk ? K * 2 : h->np * 4;
+        a.a_cols = (int32_t)(h->nk ? h->np : K);
+        a.b_cols = (int32_t)(h->nk ? K : h->np);
+        a.segments = 1;
+        if (h->simple_back) {
+            for (int z = 0; z < 2; ++z) {
+                ProductArgs b = a;
+                b.A[0] = a.A[z];
+                b.B[0] = a.B[z];
+                b.C[0] = a.C[z];
+                spg::SimpleArgs s{b, 1, a.lda / 2, 1, a.ldb / 2, 0};
+                const gemm_status e = bf ? run_simple<spg::kElBF16, false>(s, stream) : run_simple<spg::kElF16, false>(s, stream);
+                if (e != GEMM_OK) return e;
+            }
+            return GEMM_OK;
+        }
+        const bool reg = K % 8 != 0 || !is16(X);
+        return run_tiled(spg::kGradW, h->et, reg, h->dw, h->t_dw[reg], a, parts, stream);
+    }
+    return GEMM_OK;
+}
+
+gemm_status gemm_gated_destroy(gemm_gated_handle h) {
+    delete h;
+    return GEMM_OK;
+}
+
+gemm_status gemm_quantized_create(gemm_quantized_handle* out, int64_t M, int64_t N, int64_t K, gemm_dtype out_dtype,
+                                  gemm_activation act) {
+    if (!out) return GEMM_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (M < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_ARG;
+    if (out_dtype != GEMM_F16 && out_dtype != GEMM_BF16 && out_dtype != GEMM_F32) return GEMM_ERR_INVALID_ARG;
+    if (act != GEMM_ACT_NONE && act != GEMM_ACT_SILU && act != GEMM_ACT_GELU_TANH && act != GEMM_ACT_RELU)
+        return GEMM_ERR_INVALID_ARG;
+    const int64_t lim = INT32_MAX / 2 - 512;
+    // 128 * 128 * K stays below 2^31 up to here: the int32 sums cannot overflow
+    if (M > lim || N > lim || K > 131071) return GEMM_ERR_UNSUPPORTED;
+    gemm_quantized_plan* p = new (std::nothrow) gemm_quantized_plan;
+    if (!p) return GEMM_ERR_OUT_OF_MEMORY;
+    p->M = M;
+    p->N = N;
+    p->K = K;
+    p->out = (int)out_dtype;
+    p->act = (int)act;
+    p->simple = M == 0 || N == 0 || K < 16;
+    const double m = (double)M, n = (double)N, k = (double)K;
+    const int mats = act == GEMM_ACT_NONE ? 1 : 2;
+    p->s = Shape{M, N, ceil_div(K, 128), 1, 1, mats, m * k + mats * n * k + m * n * (out_dtype == GEMM_F32 ? 4 : 2)};
+    p->ws = 0;
+    if (!p->simple)
+        for (int r = 0; r < 2; ++r) {
+            p->t[r] = choose(p->s, r == 1);
+            p->ws = std::max(p->ws, part_bytes(p->s, p->t[r]));
+        }
+    *out = p;
+    return GEMM_OK;
+}
+
+int64_t gemm_quantized_workspace(gemm_quantized_handle h) { return h ? h->ws : -1; }
+
+gemm_status gemm_quantized_run(gemm_quantized_handle h, const int8_t* A, const float* scale_a, const int8_t* B,
+                               const float* scale_b, const int8_t* B2, const float* scale_b2, void* C,
+                               void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+    if (!h) return GEMM_ERR_INVALID_ARG;
+    const bool dual = h->act != GEMM_ACT_NONE;
+    if (!dual && (B2 || scale_b2)) return GEMM_ERR_INVALID_ARG;
+    if (h->M == 0 || h->N == 0) return GEMM_OK;
+    if (!C || !scale_a || !scale_b || (dual && !scale_b2)) return GEMM_ERR_INVALID_ARG;
+    if (h->K > 0 && (!A || !B || (dual && !B2))) return GEMM_ERR_INVALID_ARG;
+    ProductArgs a{};
+    a.A[0] = (const char*)A;
+    a.B[0] = (const char*)B;
+    a.B[1] = (const char*)B2;
+    a.C[0] = C;
+    a.sa = scale_a;
+    a.sb[0] = scale_b;
+    a.sb[1] = scale_b2;
+    a.M = (int32_t)h->M;
+    a.N = (int32_t)h->N;
+    a.K = (int32_t)h->K;
+    a.lda = a.ldb = h->K;
+    a.segments = 1;
+    a.out_dtype = h->out;
+    a.act = h->act;
+    if (h->simple) {
+        spg::SimpleArgs s{a, h->K, 1, h->K, 1, 0};
+        return dual ? run_simple<spg::kElI8, true>(s, stream) : run_simple<spg::kElI8, false>(s, stream);
+    }
+    if (h->M <= kStreamRows) {
+        if (dual) stream_rows<spg::kElI8, true>(a, stream);
+        else stream_rows<spg::kElI8, false>(a, stream);
+        return launched();
+    }
+    const bool reg = h->K % 16 != 0 || !is16(A) || !is16(B) || (dual && !is16(B2));
+    const Tiling& t = h->t[reg];
+    if (t.split > 1 && (!workspace || (uintptr_t)workspace % 16 != 0 || workspace_bytes < part_bytes(h->s, t)))
+        return GEMM_ERR_INVALID_ARG;
+    return run_tiled(dual ? spg::kInt8Gated : spg::kInt8, spg::kElI8, reg, h->s, t, a, workspace, stream);
+}
+
+gemm_status gemm_quantized_destroy(gemm_quantized_handle h) {
+    delete h;
+    return GEMM_OK;
+}
+
+gemm_status gemm_quantize_rows(const void* X, gemm_dtype dtype, int64_t rows, int64_t K, int8_t* A, float* scale,
+                               hipStream_t stream) {
+    if (rows < 0 || K < 0) return GEMM_ERR_INVALID_ARG;
+    if (dtype != GEMM_F16 && dtype != GEMM_BF16 && dtype != GEMM_F32) return GEMM_ERR_INVALID_ARG;
+    if (rows == 0) return GEMM_OK;
+    if (!scale || (K > 0 && (!X || !A))) return GEMM_ERR_INVALID_ARG;
+    if (rows > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)rows), wg(256);
+    auto go = [&](auto dt) {
+        constexpr int D = decltype(dt)::value;
+        const int64_t per = ceil_div(K, 256 * spg::RowVec<D>::E);   // vectors of a thread
+        const char* x = (const char*)X;
+        if (per <= 2) hipLaunchKernelGGL((spg::quantize_rows<D, 2>), grid, wg, 0, stream, x, A, scale, K);
+        else if (per <= 8) hipLaunchKernelGGL((spg::quantize_rows<D, 8>), grid, wg, 0, stream, x, A, scale, K);
+        else hipLaunchKernelGGL((spg::quantize_rows<D, 0>), grid, wg, 0, stream, x, A, scale, K);
+    };
+    if (dtype == GEMM_F16) go(std::integral_constant<int, spg::kOutF16>{});
+    else if (dtype == GEMM_BF16) go(std::integral_constant<int, spg::kOutBF16>{});
+    else go(std::integral_constant<int, spg::kOutF32>{});
+    return launched();
+}
+
+}  // extern "C"

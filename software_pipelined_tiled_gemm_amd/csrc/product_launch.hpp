@@ -1,0 +1,62 @@
+// Launchers of the feed-forward operators' kernels: declared for the host unit, defined and
+// explicitly instantiated by product_unit.hip, which is compiled once per (element type,
+// product, copy mode) so that the units build in parallel.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "product_kernels.hpp"
+
+namespace spg {
+
+// The products, by how their operands are stored.
+enum {
+    kGatedNK = 0,     // X [M,K] with two weights [N,K]
+    kGatedKN = 1,     // X [M,K] with two weights [K,N]
+    kGradXNK = 2,     // [dG dU] with weights [N,K]: B is stored reduction-major
+    kGradXKN = 3,     // [dG dU] with weights [K,N]
+    kGradW = 4,       // both operands reduction-major
+    kInt8 = 5,        // int8, one B
+    kInt8Gated = 6,   // int8, two B
+    kProducts = 7
+};
+
+// Tile classes: rows x columns of a workgroup's tile (DUAL: columns of both matrices)
+enum { kTileBig = 0, kTileMid = 1, kTileSmall = 2, kTiles = 3 };
+constexpr int kTileM[kTiles] = {256, 128, 64};
+constexpr int kTileN[kTiles] = {256, 128, 128};
+
+template <int ET, int P, bool REG>
+void launch_product(int tile, const ProductArgs& a, dim3 grid, hipStream_t st);
+
+#ifdef SPG_DEFINE_PRODUCT
+template <int ET, int P, bool REG, int BM, int BN, int WM, int WN, int S, bool DEEP>
+void launch_tile(const ProductArgs& a, dim3 grid, hipStream_t st) {
+    constexpr bool AT = P == kGradW, BNC = P == kGatedKN || P == kGradXNK || P == kGradW;
+    constexpr bool DUAL = P == kGatedNK || P == kGatedKN || P == kInt8Gated;
+    constexpr bool SEG = P == kGradXNK || P == kGradXKN;
+    hipLaunchKernelGGL((product_kernel<ET, AT, BNC, DUAL, SEG, REG, BM, BN, WM, WN, S, DEEP>), grid,
+                       dim3(ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP>::NT), 0, st, a);
+}
+
+template <int ET, int P, bool REG>
+void launch_product(int tile, const ProductArgs& a, dim3 grid, hipStream_t st) {
+    constexpr bool DUAL = P == kGatedNK || P == kGatedKN || P == kInt8Gated;
+    if constexpr (!REG) {
+        if (tile == kTileBig) {
+            // DUAL: 64 x 128 per wave, so that a wave's output rows are whole 128-byte lines
+            if constexpr (DUAL) launch_tile<ET, P, REG, 256, 256, 64, 128, 2, false>(a, grid, st);
+            else launch_tile<ET, P, REG, 256, 256, 128, 64, 2, false>(a, grid, st);
+        } else if (tile == kTileMid) {
+            launch_tile<ET, P, REG, 128, 128, 32, 64, 4, false>(a, grid, st);
+        } else {
+            launch_tile<ET, P, REG, 64, 128, 32, 64, 6, false>(a, grid, st);
+        }
+    } else {
+        if (tile == kTileMid) launch_tile<ET, P, REG, 128, 128, 32, 64, 2, false>(a, grid, st);
+        else launch_tile<ET, P, REG, 64, 128, 32, 64, 2, false>(a, grid, st);
+    }
+}
+#endif
+
+}  // namespace spg

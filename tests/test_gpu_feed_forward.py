@@ -1,0 +1,468 @@
+"""GPU tests of the feed-forward operators (gated projection, its backward pass, int8
+products, quantisation of rows) against plain formulas in 64 bits.
+
+Tolerances, derived from the arithmetic and applied to every element.  With e the output
+type's epsilon, an output y rounded once is off by e/2 |y|.  A sum of K products in fp32 in
+any order is off by at most K 2^-24 S, S the sum of the products' magnitudes.  The
+activations and their slopes are evaluated in fp32 from a sigmoid with relative error below
+2^-20: act is off by 2^-20 |g|, act' by 2^-19 (1 + |g|); |act'| < 1.13 for all three.
+fp16 results below 2^-14 are rounded to multiples of 2^-24: half of that is added.  In the
+backward pass dG and dU are rounded to the operands' type before the products.
+"""
+
+import pytest
+
+import software_pipelined_tiled_gemm_amd as spg
+from tests import gpu_util
+
+pytestmark = pytest.mark.gpu
+
+U32 = 2.0 ** -24
+SLOPE = 1.13
+
+
+def _t():
+    import torch
+    return torch
+
+
+def _dt(name):
+    torch = _t()
+    return {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}[name]
+
+
+def _half_ulp(name):
+    return _t().finfo(_dt(name)).eps / 2
+
+
+def _tiny(name):
+    return 2.0 ** -25 if name == "f16" else 2.0 ** -134
+
+
+class Buf:
+    """A tensor inside a larger allocation, `off` elements past a 16-byte boundary, with
+    guard elements on both sides that must stay untouched."""
+
+    def __init__(self, shape, dtype, off=0, value=None):
+        torch = _t()
+        n = 1
+        for d in shape:
+            n *= d
+        self.n, self.lo = n, 64 + off
+        raw = {1: torch.int8, 2: torch.int16, 4: torch.int32}[torch.empty(0, dtype=dtype).element_size()]
+        self.raw = torch.full((n + 128 + off,), 0x5A, dtype=raw, device=gpu_util.torch_dev())
+        self.t = self.raw.view(dtype)[self.lo:self.lo + n].view(shape)
+        if value is not None:
+            self.t.copy_(value)
+
+    def intact(self):
+        return bool((self.raw[:self.lo] == 0x5A).all()) and bool((self.raw[self.lo + self.n:] == 0x5A).all())
+
+
+def _normal(gen, shape, std):
+    torch = _t()
+    return torch.empty(shape, dtype=torch.float32, device="cuda").normal_(0.0, std, generator=gen)
+
+
+def _gen(seed):
+    g = _t().Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _act(g, act):
+    torch = _t()
+    if act == "relu":
+        return g.clamp(min=0)
+    z = g if act == "silu" else 2 * 0.7978845608 * (g + 0.044715 * g ** 3)
+    return g * torch.sigmoid(z)
+
+
+def _slope(g, act):
+    torch = _t()
+    if act == "relu":
+        return (g > 0).double()
+    if act == "silu":
+        z, dz = g, 1.0
+    else:
+        z, dz = 2 * 0.7978845608 * (g + 0.044715 * g ** 3), 2 * 0.7978845608 * (1 + 3 * 0.044715 * g * g)
+    s = torch.sigmoid(z)
+    return s + g * s * (1 - s) * dz
+
+
+def _within(got, want, tol, what):
+    torch = _t()
+    err = (got.double() - want).abs()
+    bad = ~(err <= tol)
+    if bool(bad.any()):
+        i = int(bad.flatten().nonzero()[0])
+        raise AssertionError(f"{what}: {int(bad.sum())} of {bad.numel()} outside, first at flat index {i}: "
+                             f"got {got.flatten()[i].item()}, want {want.flatten()[i].item()}, "
+                             f"tol {tol.flatten()[i].item()}")
+    return float((err / tol.clamp(min=1e-300)).max()) if err.numel() else 0.0
+
+
+# (M, N, K): few rows (1, 16, 17, 33, 64), tiles cut on every side, odd rows, one k-tile,
+# more parts of the reduction than one, grids of the 256-wide tile
+SIZES = [(1, 48, 40), (1, 4096, 1001), (3, 130, 64), (16, 72, 200), (17, 96, 136), (33, 40, 8), (48, 56, 777),
+         (64, 264, 512), (65, 100, 64), (129, 257, 320), (200, 64, 2048), (300, 2731, 1001), (511, 520, 500),
+         (70, 33, 9), (96, 1536, 4096), (1280, 2304, 192)]
+
+
+def _gated_case(M, N, K, dtype, layout, seed, off=0):
+    gen = _gen(seed)
+    dt = _dt(dtype)
+    w = (N, K) if layout == "nk" else (K, N)
+    x = Buf((M, K), dt, off, _normal(gen, (M, K), 1.0).to(dt))
+    wg = Buf(w, dt, off, _normal(gen, w, K ** -0.5).to(dt))
+    wu = Buf(w, dt, off, _normal(gen, w, K ** -0.5).to(dt))
+    return x, wg, wu
+
+
+def _as_kn(w, layout):
+    d = w.double()
+    return d.t().contiguous() if layout == "nk" else d
+
+
+def _check_forward(x, wg, wu, h, g, u, dtype, layout, act):
+    K = x.shape[1]
+    xd, gd, ud = x.double(), _as_kn(wg, layout), _as_kn(wu, layout)
+    G, U = xd @ gd, xd @ ud
+    sg, su = K * U32 * (xd.abs() @ gd.abs()), K * U32 * (xd.abs() @ ud.abs())
+    e, tiny = _half_ulp(dtype), _tiny(dtype)
+    A = _act(G, act)
+    want = A * U
+    tol = e * want.abs() + SLOPE * sg * (U.abs() + su) + A.abs() * su + 2.0 ** -20 * G.abs() * U.abs() + tiny
+    r = _within(h, want, tol, "H")
+    if g is not None:
+        _within(g, G, e * G.abs() + 1.01 * sg + tiny, "G")
+        _within(u, U, e * U.abs() + 1.01 * su + tiny, "U")
+    return r
+
+
+def _workspace(nbytes):
+    torch = _t()
+    # filled with NaN patterns: nothing may be read before it is written
+    return torch.full((max(nbytes, 1),), 0xFF, dtype=torch.uint8, device="cuda")
+
+
+@pytest.mark.parametrize("layout", ["nk", "kn"])
+@pytest.mark.parametrize("size", SIZES, ids=str)
+def test_gated_forward(size, layout):
+    torch = _t()
+    M, N, K = size
+    for i, (dtype, act, off, keep) in enumerate((("bf16", "silu", 0, False), ("f16", "gelu_tanh", 0, True),
+                                                 ("bf16", "relu", 1, True))):
+        x, wg, wu = _gated_case(M, N, K, dtype, layout, 100 + i, off)
+        h, g, u = (Buf((M, N), _dt(dtype), off) for _ in range(3))
+        with spg.Gated(M, N, K, dtype, layout, act) as plan:
+            ws = _workspace(plan.workspace_bytes())
+            plan(x.t, wg.t, wu.t, h.t, G=g.t if keep else None, U=u.t if keep else None, workspace=ws)
+        torch.cuda.synchronize()
+        _check_forward(x.t, wg.t, wu.t, h.t, g.t if keep else None, u.t if keep else None, dtype, layout, act)
+        assert all(b.intact() for b in (x, wg, wu, h, g, u))
+
+
+def _check_backward(dh, x, wg, wu, g, u, dx, dwg, dwu, dtype, layout, act):
+    M, K = x.shape
+    N = g.shape[1]
+    e, tiny = _half_ulp(dtype), _tiny(dtype)
+    D, X, G, U = dh.double(), x.double(), g.double(), u.double()
+    gd, ud = _as_kn(wg, layout), _as_kn(wu, layout)
+    A, S = _act(G, act), _slope(G, act)
+    dG, dU = D * U * S, D * A
+    # what the rounded dG and dU may be off by
+    tg = e * dG.abs() + 1.01 * 2.0 ** -19 * D.abs() * U.abs() * (1 + G.abs()) + tiny
+    tu = e * dU.abs() + 1.01 * 2.0 ** -20 * D.abs() * G.abs() + tiny
+    want = dG @ gd.t() + dU @ ud.t()
+    tol = e * want.abs() + 1.01 * (tg @ gd.abs().t() + tu @ ud.abs().t()) + tiny
+    tol += 2 * N * U32 * ((dG.abs() + tg) @ gd.abs().t() + (dU.abs() + tu) @ ud.abs().t())
+    _within(dx, want, tol, "dX")
+    for name, got, d, t in (("dWg", dwg, dG, tg), ("dWu", dwu, dU, tu)):
+        w = X.t() @ d
+        tol = e * w.abs() + 1.01 * (X.abs().t() @ t) + M * U32 * (X.abs().t() @ (d.abs() + t)) + tiny
+        if layout == "nk":
+            w, tol = w.t(), tol.t()
+        _within(got, w, tol, name)
+
+
+@pytest.mark.parametrize("layout", ["nk", "kn"])
+@pytest.mark.parametrize("size", SIZES + [(2048, 1024, 256), (1000, 24, 1536)], ids=str)
+def test_gated_backward(size, layout):
+    torch = _t()
+    M, N, K = size
+    for i, (dtype, act, off) in enumerate((("bf16", "silu", 0), ("f16", "gelu_tanh", 0), ("bf16", "relu", 1))):
+        x, wg, wu = _gated_case(M, N, K, dtype, layout, 200 + i, off)
+        gen = _gen(300 + i)
+        dt = _dt(dtype)
+        g = Buf((M, N), dt, off, _normal(gen, (M, N), 1.0).to(dt))
+        u = Buf((M, N), dt, off, _normal(gen, (M, N), 1.0).to(dt))
+        dh = Buf((M, N), dt, off, _normal(gen, (M, N), 0.3).to(dt))
+        dx, dwg, dwu = Buf(x.t.shape, dt, off), Buf(wg.t.shape, dt, off), Buf(wu.t.shape, dt, off)
+        with spg.Gated(M, N, K, dtype, layout, act) as plan:
+            ws = _workspace(plan.workspace_bytes())
+            plan.backward(dh.t, x.t, wg.t, wu.t, g.t, u.t, dx.t, dwg.t, dwu.t, workspace=ws)
+        torch.cuda.synchronize()
+        _check_backward(dh.t, x.t, wg.t, wu.t, g.t, u.t, dx.t, dwg.t, dwu.t, dtype, layout, act)
+        assert all(b.intact() for b in (x, wg, wu, g, u, dh, dx, dwg, dwu))
+
+
+def test_gradient_against_differences():
+    # sum(R * H) differenced along random directions of X, Wg and Wu in 64 bits (central
+    # differences, error O(t^2)), against the fp16 gradients.  The gradients carry the
+    # roundings of G, U, dG, dU and their own: five of 2^-11 each, random in sign over more
+    # than 10^4 terms; 2^-8 of the norm of the products leaves each of them whole.
+    torch = _t()
+    M, N, K = 96, 160, 128
+    for act in ("silu", "gelu_tanh"):
+        for layout in ("nk", "kn"):
+            x, wg, wu = (b.t for b in _gated_case(M, N, K, "f16", layout, 7))
+            R = _normal(_gen(8), (M, N), 0.5).half()
+            h, g, u = (torch.empty(M, N, dtype=torch.float16, device="cuda") for _ in range(3))
+            dx, dwg, dwu = torch.empty_like(x), torch.empty_like(wg), torch.empty_like(wu)
+            with spg.Gated(M, N, K, "f16", layout, act) as plan:
+                ws = _workspace(plan.workspace_bytes())
+                plan(x, wg, wu, h, G=g, U=u, workspace=ws)
+                plan.backward(R, x, wg, wu, g, u, dx, dwg, dwu, workspace=ws)
+            for which, grad in ((0, dx), (1, dwg), (2, dwu)):
+                p = [x.double(), wg.double(), wu.double()]
+                v = _normal(_gen(20 + which), p[which].shape, 1.0).double()
+
+                def loss(t):
+                    q = list(p)
+                    q[which] = q[which] + t * v
+                    a, b = (q[i].t() if layout == "nk" else q[i] for i in (1, 2))
+                    return (R.double() * _act(q[0] @ a, act) * (q[0] @ b)).sum()
+
+                t = 1e-5
+                slope = float((loss(t) - loss(-t)) / (2 * t))
+                scale = float((grad.double() * v).norm())
+                assert abs(float((grad.double() * v).sum()) - slope) <= 2.0 ** -8 * scale + 1e-6, (act, layout, which)
+
+
+def test_gated_infinities_stay_in_their_row_and_column():
+    # a value of one row never reaches another row, whatever lies past a row's end
+    torch = _t()
+    for layout in ("nk", "kn"):
+        for M, N, K in ((5, 40, 72), (100, 136, 72), (100, 130, 75), (20, 130, 75), (300, 520, 200)):
+            x, wg, wu = (b.t for b in _gated_case(M, N, K, "bf16", layout, 11))
+            x[2, :] = float("inf")
+            x[M - 1, 0] = float("nan")
+            wgk = wg if layout == "nk" else wg.t()
+            wgk[7, 0] = float("nan")
+            wgk[N - 1, K - 1] = float("inf")
+            h = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+            with spg.Gated(M, N, K, "bf16", layout, "silu") as plan:
+                plan(x, wg, wu, h, workspace=_workspace(plan.workspace_bytes()))
+            ok = torch.isfinite(h.float())
+            rows = [m for m in range(M) if m not in (2, M - 1)]
+            cols = [n for n in range(N) if n not in (7, N - 1)]
+            assert bool(ok[rows][:, cols].all()), (layout, M, N, K)
+            assert bool(torch.isnan(h[:, 7].float()).all()) and bool(torch.isnan(h[M - 1].float()).all())
+
+
+@pytest.mark.parametrize("layout", ["nk", "kn"])
+def test_gated_sizes_without_a_chunk(layout):
+    # reductions and rows shorter than 16 bytes, and empty ones
+    torch = _t()
+    for M, N, K in ((5, 7, 3), (130, 5, 40), (4, 9, 0), (0, 5, 9), (6, 0, 9), (1, 1, 1), (9, 3, 17)):
+        x, wg, wu = _gated_case(M, N, max(K, 0), "f16", layout, 31) if K else (
+            Buf((M, 0), torch.float16), Buf((N, 0) if layout == "nk" else (0, N), torch.float16),
+            Buf((N, 0) if layout == "nk" else (0, N), torch.float16))
+        h, g, u = (Buf((M, N), torch.float16) for _ in range(3))
+        dh = Buf((M, N), torch.float16, 0, _normal(_gen(5), (M, N), 0.3).half())
+        dx, dwg, dwu = (Buf(b.t.shape, torch.float16) for b in (x, wg, wu))
+        with spg.Gated(M, N, K, "f16", layout, "silu") as plan:
+            ws = _workspace(plan.workspace_bytes())
+            plan(x.t, wg.t, wu.t, h.t, G=g.t, U=u.t, workspace=ws)
+            plan.backward(dh.t, x.t, wg.t, wu.t, g.t, u.t, dx.t, dwg.t, dwu.t, workspace=ws)
+        torch.cuda.synchronize()
+        _check_forward(x.t, wg.t, wu.t, h.t, g.t, u.t, "f16", layout, "silu")
+        _check_backward(dh.t, x.t, wg.t, wu.t, g.t, u.t, dx.t, dwg.t, dwu.t, "f16", layout, "silu")
+        assert all(b.intact() for b in (h, g, u, dx, dwg, dwu))
+
+
+def _ints(gen, shape):
+    torch = _t()
+    return torch.randint(-128, 128, shape, generator=gen, device="cuda", dtype=torch.int32).to(torch.int8)
+
+
+@pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("size", SIZES + [(1, 5, 7), (3, 4, 0), (90, 300, 5000), (1024, 768, 1280)], ids=str)
+def test_quantized_product(size, out):
+    torch = _t()
+    M, N, K = size
+    for i, (act, off) in enumerate((("none", 0), ("none", 3), ("silu", 0), ("gelu_tanh", 1), ("relu", 0))):
+        gen = _gen(400 + i)
+        a = Buf((M, K), torch.int8, off, _ints(gen, (M, K)))
+        b = [Buf((N, K), torch.int8, off, _ints(gen, (N, K))) for _ in range(2 if act != "none" else 1)]
+        std = 1.0 / (74.0 * 74.0 * max(K, 1) ** 0.5)          # products of uniform int8: about unit results
+        sa = torch.empty(M, device="cuda").uniform_(0.5, 1.5, generator=gen)
+        sb = [torch.empty(N, device="cuda").uniform_(0.5, 1.5, generator=gen) * std for _ in b]
+        c = Buf((M, N), _dt(out), off)
+        with spg.QuantizedGemm(M, N, K, out, act) as plan:
+            ws = _workspace(plan.workspace_bytes())
+            plan(a.t, sa, b[0].t, sb[0], c.t, B2=b[1].t if len(b) > 1 else None,
+                 scale_b2=sb[1] if len(b) > 1 else None, workspace=ws)
+        torch.cuda.synchronize()
+        # |acc| < 2^31 is exact in 64 bits; its conversion, the product of the scales and
+        # their product round once each in fp32
+        p = [(a.t.double() @ w.t.double().t()) * sa.double()[:, None] * s.double() for w, s in zip(b, sb)]
+        e, tiny = _half_ulp(out), _tiny(out)
+        if act == "none":
+            want, tol = p[0], (e + 3.01 * U32) * p[0].abs() + tiny
+        else:
+            A = _act(p[0], act)
+            want = A * p[1]
+            tol = (e * want.abs() + SLOPE * 3.01 * U32 * p[0].abs() * p[1].abs() * 1.01
+                   + 4.02 * U32 * want.abs() + 2.0 ** -20 * p[0].abs() * p[1].abs() + tiny)
+        _within(c.t, want, tol, f"C {act}")
+        assert c.intact() and a.intact() and all(w.intact() for w in b)
+
+
+def test_quantized_extremes():
+    # the largest sums: every operand -128, the longest reduction
+    torch = _t()
+    for M, K in ((2, 131071), (70, 131056), (70, 131071)):
+        a = torch.full((M, K), -128, dtype=torch.int8, device="cuda")
+        b = torch.full((40, K), -128, dtype=torch.int8, device="cuda")
+        one, c = torch.ones(M, device="cuda"), torch.empty(M, 40, device="cuda")
+        with spg.QuantizedGemm(M, 40, K, "f32") as plan:
+            plan(a, one, b, torch.ones(40, device="cuda"), c, workspace=_workspace(plan.workspace_bytes()))
+        assert bool((c == torch.tensor(16384.0 * K, dtype=torch.float64).float().item()).all())
+
+
+def _rounded_rows(x):
+    """The definition in 64 bits: 127 x / amax is off by less than 2^-46, and no quotient of
+    two fp32 values that is not a half lies closer to one than 2^-33."""
+    torch = _t()
+    d = x.double()
+    amax = d.abs().amax(dim=1, keepdim=True) if d.shape[1] else torch.zeros(d.shape[0], 1, dtype=torch.float64, device=d.device)
+    q = torch.round(d * 127.0 / torch.where(amax > 0, amax, torch.ones_like(amax)))
+    return q.to(torch.int8), (amax / 127.0).float().flatten()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_quantize_rows(dtype):
+    torch = _t()
+    dt = _dt(dtype)
+    for K in (1, 7, 8, 40, 129, 1001, 4096, 5000, 16384, 20011):
+        for off in (0, 1):
+            gen = _gen(500 + K)
+            M = 37
+            x = _normal(gen, (M, K), 1.0)
+            x[3] = 0.0
+            x[4] *= 1e-3
+            x[5] = 1.0
+            x[6] *= 1e4
+            if dtype != "f16":
+                x[7] *= 1e-30
+                x[8] *= 1e30
+                x[9] *= 1e-42          # subnormal in fp32
+            x[10] = -x[10].abs()
+            # quotients on and next to halves: amax = 254, values k + 1/2
+            r = torch.arange(K, device="cuda")
+            x[11] = (r % 254 - 127).float() + 0.5
+            x[11, K - 1] = 127.0
+            x[12] = x[11] * 2
+            xb = Buf((M, K), dt, off, x.to(dt))
+            a, s = Buf((M, K), torch.int8, off), Buf((M,), torch.float32)
+            spg.gemm_quantize_rows(xb.t, a.t, s.t)
+            torch.cuda.synchronize()
+            qa, qs = _rounded_rows(xb.t)
+            assert bool((a.t == qa).all()), (K, off, int((a.t != qa).sum()))
+            assert bool((s.t == qs).all()), (K, off)
+            assert a.intact() and s.intact() and xb.intact()
+
+
+def test_quantize_rows_halves_of_fp32():
+    # fp32 neighbours of every half: the rounding side is decided exactly
+    torch = _t()
+    for amax in (1.0, 3.3, 0.7531):
+        top = torch.tensor(amax, dtype=torch.float32)
+        half = torch.arange(-127, 127, dtype=torch.float64) + 0.5
+        x = (half * top.double() / 127.0).float()
+        rows = [x]
+        for _ in range(3):
+            rows.append(torch.nextafter(rows[-1], torch.tensor(float("inf"))))
+        x = torch.cat(rows + [top[None]]).cuda()[None].repeat(2, 1).contiguous()
+        a = torch.empty(x.shape, dtype=torch.int8, device="cuda")
+        s = torch.empty(2, device="cuda")
+        spg.gemm_quantize_rows(x, a, s)
+        qa, qs = _rounded_rows(x)
+        assert bool((a == qa).all()) and bool((s == qs).all())
+
+
+def test_quantized_rows_that_are_not_finite():
+    torch = _t()
+    x = _normal(_gen(1), (6, 300), 1.0).bfloat16()
+    x[1, 5] = float("inf")
+    x[4, 299] = float("nan")
+    a, s = torch.empty(6, 300, dtype=torch.int8, device="cuda"), torch.empty(6, device="cuda")
+    spg.gemm_quantize_rows(x, a, s)
+    b, sb, c = _ints(_gen(2), (50, 300)), torch.ones(50, device="cuda"), torch.empty(6, 50, device="cuda")
+    with spg.QuantizedGemm(6, 50, 300, "f32") as plan:
+        plan(a, s, b, sb, c, workspace=_workspace(plan.workspace_bytes()))
+    for m in range(6):
+        assert bool(torch.isnan(c[m]).all()) if m in (1, 4) else bool(torch.isfinite(c[m]).all())
+
+
+def test_other_stream_and_graph_replays():
+    torch = _t()
+    M, N, K = 200, 1024, 512
+    x, wg, wu = (b.t for b in _gated_case(M, N, K, "bf16", "nk", 61))
+    h, g, u, dh = (torch.zeros(M, N, dtype=torch.bfloat16, device="cuda") for _ in range(4))
+    dh.copy_(_normal(_gen(62), (M, N), 0.3))
+    grads = [torch.empty_like(t) for t in (x, wg, wu)]
+    a8, sa = torch.empty(M, N, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+    b8, sb = _ints(_gen(63), (K, N)), torch.full((K,), 1e-3, device="cuda")
+    y = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+    plan, down = spg.Gated(M, N, K, "bf16", "nk", "silu"), spg.QuantizedGemm(M, K, N, "bf16")
+    ws = _workspace(max(plan.workspace_bytes(), down.workspace_bytes()))
+
+    def once():
+        plan(x, wg, wu, h, G=g, U=u, workspace=ws)
+        plan.backward(dh, x, wg, wu, g, u, *grads, workspace=ws)
+        spg.gemm_quantize_rows(h, a8, sa)
+        down(a8, sa, b8, sb, y, workspace=ws)
+        return [h, g, u, *grads, y]
+
+    want = [t.clone() for t in once()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for t in once():
+            t.zero_()
+        got = once()
+    side.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(want, got))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        once()
+    for r in range(4):
+        for t in (h, g, u, *grads, y):
+            t.fill_(r)
+        ws.fill_(0xFF)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(want, (h, g, u, *grads, y))), r
+
+
+def test_repeated_passes_are_bitwise_equal():
+    # split reductions are added in a fixed order
+    torch = _t()
+    M, N, K = 96, 1536, 4096
+    for layout in ("nk", "kn"):
+        x, wg, wu = (b.t for b in _gated_case(M, N, K, "f16", layout, 71))
+        outs = []
+        for _ in range(3):
+            h, g, u = (torch.empty(M, N, dtype=torch.float16, device="cuda") for _ in range(3))
+            grads = [torch.empty_like(t) for t in (x, wg, wu)]
+            with spg.Gated(M, N, K, "f16", layout, "relu") as plan:
+                ws = _workspace(plan.workspace_bytes())
+                plan(x, wg, wu, h, G=g, U=u, workspace=ws)
+                plan.backward(h, x, wg, wu, g, u, *grads, workspace=ws)
+            outs.append([h, *grads])
+        for o in outs[1:]:
+            assert all(torch.equal(p, q) for p, q in zip(outs[0], o))
