@@ -326,26 +326,21 @@ def gemm_quantize_rows(X, A, scale, stream=None, dtype: Optional[str] = None,
                        shape: Optional[tuple] = None) -> None:
     """Quantise the rows of X into A (int8) and scale (fp32).  For tensors the type and the
     [rows, K] shape are X's; with raw device pointers they are given."""
-    if dtype is None or shape is None:
-        t = _torch_names()
-        dtype = t[X.dtype] if dtype is None else dtype
-        if shape is None:
-            if X.dim() < 1:
-                raise GemmError(1, "gemm_quantize_rows: X needs at least one dimension")
-            K = X.shape[-1]
-            shape = (X.numel() // K if K else _rows_of_empty(X.shape), K)
-        _expect("gemm_quantize_rows", X=(X, dtype, tuple(X.shape)), A=(A, "i8", tuple(X.shape)),
-                scale=(scale, "f32", tuple(X.shape[:-1])))
-    st = lib().gemm_quantize_rows(_ptr(X), DTYPES[dtype], shape[0], shape[1], _ptr(A), _ptr(scale),
-                                  _stream(stream, X, A))
-    _check(st, "gemm_quantize_rows")
-
-
-def _rows_of_empty(shape) -> int:
-    n = 1
-    for d in shape[:-1]:
-        n *= d
-    return n
+    if not isinstance(X, int) and X is not None:
+        names, full = _torch_names(), X.shape
+        if len(full) < 1 or X.dtype not in names or names[X.dtype] not in DTYPES:
+            raise GemmError(1, f"gemm_quantize_rows: X is {X.dtype} of shape {tuple(full)}")
+        device, (X_, A_, s_) = _dense("gemm_quantize_rows", ("X", X, X.dtype, full),
+                                      ("A", A, _torch_type("i8"), full),
+                                      ("scale", scale, _torch_type("f32"), full[:-1]))
+        dtype, shape = names[X.dtype], (full[:-1].numel(), full[-1])
+    else:
+        if dtype is None or shape is None:
+            raise GemmError(1, "gemm_quantize_rows: a raw X needs dtype and shape")
+        device, X_, A_, s_ = None, X, _ptr(A), _ptr(scale)
+    st = lib().gemm_quantize_rows(X_, DTYPES[dtype], shape[0], shape[1], A_, s_, _stream_on(stream, device))
+    if st:
+        _check(st, "gemm_quantize_rows")
 
 
 def _nbytes(workspace, given: Optional[int]) -> int:
@@ -353,41 +348,88 @@ def _nbytes(workspace, given: Optional[int]) -> int:
         return given
     if workspace is None or isinstance(workspace, int):
         return 0
-    return workspace.numel() * workspace.element_size()
+    return workspace.nbytes
 
 
-_names = None
+_names = _types = None
 
 
 def _torch_names():
     """torch dtype -> this library's name."""
-    global _names
+    global _names, _types
     if _names is None:
         import torch
         _names = {torch.float16: "f16", torch.bfloat16: "bf16", torch.float32: "f32", torch.int8: "i8"}
+        _types = {v: k for k, v in _names.items()}
     return _names
 
 
-def _expect(what: str, **tensors) -> None:
-    """Check tensors (raw pointers and None pass) against (tensor, dtype, shape): the kernels
-    read dense memory of exactly that shape, so anything else is refused here."""
-    names = _torch_names()
+def _torch_type(name: str):
+    """This library's name -> torch dtype (None without torch: raw pointers only)."""
+    if _types is None:
+        try:
+            _torch_names()
+        except ImportError:
+            return None
+    return _types[name]
+
+
+def _refuse(what: str, tensors) -> None:
+    """Raise for the first of (name, tensor, dtype, shape) that is not a dense GPU tensor of
+    that type and shape on the first one's device."""
     device = None
-    for name, (t, dtype, shape) in tensors.items():
+    for name, t, dtype, shape in tensors:
         if t is None or isinstance(t, int):
             continue
         if t.shape != shape:
             raise GemmError(1, f"{what}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-        if names.get(t.dtype) != dtype:
+        if t.dtype is not dtype:
             raise GemmError(1, f"{what}: {name} is {t.dtype}, not {dtype}")
         if not t.is_contiguous():
             raise GemmError(1, f"{what}: {name} is not contiguous")
         if not t.is_cuda:
             raise GemmError(1, f"{what}: {name} is not on a GPU")
         if device is None:
-            device = t.device
-        elif t.device != device:
+            device = t.get_device()
+        elif t.get_device() != device:
             raise GemmError(1, f"{what}: {name} is on another device")
+
+
+def _dense(what: str, *tensors) -> tuple:
+    """Check (name, tensor, dtype, shape) -- the kernels read dense memory of exactly that
+    shape; raw device pointers and None pass -- and return the device index (None without a
+    tensor) and the pointers.  Written for its cost: a call on one token is over in a few
+    microseconds, and each attribute of a tensor takes a tenth of one to read."""
+    device, ptrs = None, []
+    for _, t, dtype, shape in tensors:
+        if t is None or isinstance(t, int):
+            ptrs.append(t)
+            continue
+        d = t.get_device()
+        if device is None:
+            device = d
+        if d != device or d < 0 or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+            _refuse(what, tensors)
+        ptrs.append(t.data_ptr())
+    return device, ptrs
+
+
+_raw_stream = None
+
+
+def _stream_on(stream, device: Optional[int]) -> Optional[int]:
+    """The caller's stream, or the current one of `device`."""
+    if stream is not None:
+        return stream if isinstance(stream, int) else int(stream.cuda_stream)
+    if device is None:
+        return None
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        # torch's own accessor of the handle where there is one: it makes no Stream object
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda d: int(torch.cuda.current_stream(d).cuda_stream))
+    return _raw_stream(device)
 
 
 class Gated:
@@ -405,23 +447,29 @@ class Gated:
         self.handle = gemm_gated_create(M, N, K, dtype, layout, act)
         self._x, self._h = (M, K), (M, N)
         self._w = (N, K) if layout == "nk" else (K, N)
+        self._run, self._back = lib().gemm_gated_run, lib().gemm_gated_backward
+        self._type = _torch_type(dtype)
 
     def workspace_bytes(self) -> int:
         return gemm_gated_workspace(self.handle)
 
     def __call__(self, X, Wg, Wu, H, G=None, U=None, workspace=None, stream=None):
-        d = self.dtype
-        _expect("Gated", X=(X, d, self._x), Wg=(Wg, d, self._w), Wu=(Wu, d, self._w),
-                H=(H, d, self._h), G=(G, d, self._h), U=(U, d, self._h))
-        gemm_gated_run(self.handle, X, Wg, Wu, H, G, U, workspace, stream=stream)
+        d, x, w, h = self._type, self._x, self._w, self._h
+        dev, p = _dense("Gated", ("X", X, d, x), ("Wg", Wg, d, w), ("Wu", Wu, d, w), ("H", H, d, h),
+                        ("G", G, d, h), ("U", U, d, h))
+        st = self._run(self.handle, *p, _ptr(workspace), _nbytes(workspace, None), _stream_on(stream, dev))
+        if st:
+            _check(st, "gemm_gated_run")
         return H
 
     def backward(self, dH, X, Wg, Wu, G, U, dX, dWg, dWu, workspace=None, stream=None):
-        d = self.dtype
-        _expect("Gated.backward", dH=(dH, d, self._h), X=(X, d, self._x), Wg=(Wg, d, self._w),
-                Wu=(Wu, d, self._w), G=(G, d, self._h), U=(U, d, self._h), dX=(dX, d, self._x),
-                dWg=(dWg, d, self._w), dWu=(dWu, d, self._w))
-        gemm_gated_backward(self.handle, dH, X, Wg, Wu, G, U, dX, dWg, dWu, workspace, stream=stream)
+        d, x, w, h = self._type, self._x, self._w, self._h
+        dev, p = _dense("Gated.backward", ("dH", dH, d, h), ("X", X, d, x), ("Wg", Wg, d, w),
+                        ("Wu", Wu, d, w), ("G", G, d, h), ("U", U, d, h), ("dX", dX, d, x),
+                        ("dWg", dWg, d, w), ("dWu", dWu, d, w))
+        st = self._back(self.handle, *p, _ptr(workspace), _nbytes(workspace, None), _stream_on(stream, dev))
+        if st:
+            _check(st, "gemm_gated_backward")
         return dX, dWg, dWu
 
     def close(self):
@@ -453,16 +501,21 @@ class QuantizedGemm:
         self.M, self.N, self.K = M, N, K
         self.out_dtype, self.act = out_dtype, act
         self.handle = gemm_quantized_create(M, N, K, out_dtype, act)
+        self._a, self._b, self._c, self._m, self._n = (M, K), (N, K), (M, N), (M,), (N,)
+        self._run = lib().gemm_quantized_run
+        self._i8, self._f32, self._out = _torch_type("i8"), _torch_type("f32"), _torch_type(out_dtype)
 
     def workspace_bytes(self) -> int:
         return gemm_quantized_workspace(self.handle)
 
     def __call__(self, A, scale_a, B, scale_b, C, B2=None, scale_b2=None, workspace=None, stream=None):
-        M, N, K = self.M, self.N, self.K
-        _expect("QuantizedGemm", A=(A, "i8", (M, K)), scale_a=(scale_a, "f32", (M,)),
-                B=(B, "i8", (N, K)), scale_b=(scale_b, "f32", (N,)), C=(C, self.out_dtype, (M, N)),
-                B2=(B2, "i8", (N, K)), scale_b2=(scale_b2, "f32", (N,)))
-        gemm_quantized_run(self.handle, A, scale_a, B, scale_b, C, B2, scale_b2, workspace, stream=stream)
+        i8, f32, m, n, b = self._i8, self._f32, self._m, self._n, self._b
+        dev, p = _dense("QuantizedGemm", ("A", A, i8, self._a), ("scale_a", scale_a, f32, m), ("B", B, i8, b),
+                        ("scale_b", scale_b, f32, n), ("B2", B2, i8, b), ("scale_b2", scale_b2, f32, n),
+                        ("C", C, self._out, self._c))
+        st = self._run(self.handle, *p, _ptr(workspace), _nbytes(workspace, None), _stream_on(stream, dev))
+        if st:
+            _check(st, "gemm_quantized_run")
         return C
 
     def close(self):

@@ -41,24 +41,29 @@ struct Tiling {
     int64_t kt_part;
 };
 
-// Estimated microseconds of a tile class and a number of parts: rounds of the 256 CUs
-// (each tile class fills a CU's LDS, so one workgroup at a time) times the k-tiles of a
-// part, against the time memory needs; parts add their sums' traffic and a launch.
+// Estimated microseconds of a tile class and a number of parts.  A tile class fills a CU's
+// LDS, so a CU runs one workgroup at a time: rounds of the 256 CUs times a part's k-tiles and
+// a start and store per round, plus a launch; never less than the operands take to read.
+// Parts add a kernel and their sums' traffic.  Measured per k-tile with all CUs busy (us,
+// bf16): 256x256 1.5, 256x128 0.89, 128x128 0.53, 64x128 0.36, 64x64 0.25, about a third
+// less with few (a CU copies about 105 bytes a nanosecond into its LDS, which is what bounds
+// the small tiles); one k-tile alone 7, 5, 4, 4.4 and 4.8.  Register-staged tiles 1.35 times.
 Tiling choose(const Shape& s, bool reg) {
-    const double kt_us[spg::kTiles] = {1.40, 0.45, 0.30};
-    const double fixed_us[spg::kTiles] = {9.0, 5.0, 4.0};
+    const double kt_us[spg::kTiles] = {1.50, 0.89, 0.53, 0.36, 0.25};
+    const double start_us[spg::kTiles] = {5.5, 3.5, 2.5, 2.8, 3.2};
     Tiling best{spg::kTileSmall, 1, s.kt};
     double best_t = -1.0;
     for (int t = 0; t < spg::kTiles; ++t) {
         if (reg && t == spg::kTileBig) continue;   // register staging: no 256x256 tile
         const int64_t tiles = ceil_div(s.M, spg::kTileM[t]) * s.zm * ceil_div(s.N, spg::kTileN[t] / s.mats) * s.zn;
-        for (int64_t split = 1; split <= 64 && split <= s.kt; ++split) {
+        for (int64_t split = 1; split <= 32 && split <= s.kt; ++split) {
             const int64_t part = ceil_div(s.kt, split);
             if (split > 1 && (part < 4 || ceil_div(s.kt, part) != split)) continue;
             const double rounds = (double)ceil_div(tiles * split, 256);
-            double us = rounds * (kt_us[t] * (reg ? 1.3 : 1.0) * (double)part + fixed_us[t]);
-            us = std::max(us, s.bytes / 5.0e6);
-            if (split > 1) us += 3.0 + 2.0 * 4.0 * (double)split * s.M * s.zm * s.N * s.zn * s.mats / 4.0e6;
+            const double busy = 0.68 + 0.32 * std::min(1.0, (double)(tiles * split) / 256.0);
+            double us = 1.5 + rounds * (kt_us[t] * busy * (reg ? 1.35 : 1.0) * (double)part + start_us[t]);
+            us = std::max(us, 3.0 + s.bytes / 5.0e6);
+            if (split > 1) us += 3.5 + 2.0 * 4.0 * (double)split * s.M * s.zm * s.N * s.zn * s.mats / 5.0e6;
             if (best_t < 0 || us < best_t) {
                 best_t = us;
                 best = Tiling{t, (int)split, part};
@@ -105,7 +110,11 @@ gemm_status run_tiled(int product, int et, bool reg, const Shape& s, const Tilin
     a.zn = s.zn;
     a.tiles_m = (int32_t)ceil_div(s.M, spg::kTileM[t.tile]);
     a.tiles_n = (int32_t)ceil_div(s.N, spg::kTileN[t.tile] / s.mats);
-    a.group_m = 4;
+    // rows of tiles rastered together: 4 (measured at M = 8192, N = 12288: 2, 4, 8 and 16
+    // take 1198, 1186, 1200 and 1215 us), all of them when there are few, else even groups,
+    // so that no short last group reads every weight again
+    const int64_t rows = (int64_t)a.tiles_m * a.zm;
+    a.group_m = (int32_t)(rows <= 8 ? rows : ceil_div(rows, ceil_div(rows, 4)));
     a.split = t.split;
     a.kt_part = (int32_t)t.kt_part;
     a.part = t.split > 1 ? (float*)parts : nullptr;
@@ -132,10 +141,7 @@ gemm_status run_tiled(int product, int et, bool reg, const Shape& s, const Tilin
 
 template <int ET, bool DUAL>
 void stream_rows(const ProductArgs& a, hipStream_t st) {
-    const dim3 grid((unsigned)ceil_div(a.N, 16));
-    if (a.M <= 16) hipLaunchKernelGGL((spg::stream_kernel<ET, DUAL, 1, 1, 8, 8>), grid, dim3(512), 0, st, a);
-    else if (a.M <= 32) hipLaunchKernelGGL((spg::stream_kernel<ET, DUAL, 2, 1, 8, 4>), grid, dim3(512), 0, st, a);
-    else hipLaunchKernelGGL((spg::stream_kernel<ET, DUAL, 4, 1, 8, 4>), grid, dim3(512), 0, st, a);
+    hipLaunchKernelGGL((spg::stream_kernel<ET, DUAL, 8, 4>), dim3((unsigned)ceil_div(a.N, 16)), dim3(512), 0, st, a);
 }
 
 template <int ET, bool DUAL>
@@ -145,7 +151,7 @@ gemm_status run_simple(const spg::SimpleArgs& a, hipStream_t st) {
     return launched();
 }
 
-constexpr int64_t kStreamRows = 64;
+constexpr int64_t kStreamRows = 16;   // one MFMA tile of rows
 // Rows of operands are addressed by 32-bit offsets below 2^31: 256 of them fit up to here.
 constexpr int64_t kMaxRowBytes = ((int64_t)1 << 23) - 128;
 

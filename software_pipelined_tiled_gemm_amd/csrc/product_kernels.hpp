@@ -253,12 +253,14 @@ __device__ __forceinline__ void store_block(F&& val, char* stg, void* C, int M, 
 
 // Geometry of the tiled kernel: BM x BN tile, WM x WN per wave, S ring slots (DEEP: one
 // more of B).  DUAL: the BN columns are BN/2 of each B matrix, and every wave holds WN/2
-// of each for the same output columns.
-template <bool DUAL, int BM, int BN, int WM, int WN, int S, bool DEEP>
+// of each for the same output columns.  KG groups of NW waves each: group g multiplies the
+// k-tiles g, g + KG, ... of the whole tile, with a ring of its own, and their sums meet in
+// LDS at the end.
+template <bool DUAL, int BM, int BN, int WM, int WN, int S, bool DEEP, int KG>
 struct ProductGeom {
     static constexpr int WAVES_N = BN / WN;
     static constexpr int NW = (BM / WM) * WAVES_N;
-    static constexpr int NT = NW * 64;
+    static constexpr int NT = NW * KG * 64;
     static constexpr int TM = WM / 16, TN = WN / 16;
     static constexpr int BNS = DUAL ? BN / 2 : BN;      // columns of one B subtile
     static constexpr int WNS = DUAL ? WN / 2 : WN;      // a wave's columns of one B matrix
@@ -266,12 +268,15 @@ struct ProductGeom {
     static constexpr int A_OPS = A_BYTES / 1024 / NW, B_OPS = B_BYTES / 1024 / NW;
     static constexpr int L = A_OPS + B_OPS;
     static constexpr int NA = S, NB = S + (DEEP ? 1 : 0);
-    static constexpr int LDS = NA * A_BYTES + NB * B_BYTES;
+    static constexpr int RING = NA * A_BYTES + NB * B_BYTES;
+    static constexpr int LDS = RING * KG;
     static constexpr int STG = 32 * WNS * 4;            // staging of one wave
+    static constexpr int SUMS = (KG - 1) * NW * TM * TN * 1024;   // accumulators of the other groups
     static_assert(BM % WM == 0 && BN % WN == 0 && WM % 32 == 0 && WNS % 32 == 0, "wave tile");
     static_assert(A_OPS * 1024 * NW == A_BYTES && B_OPS * 1024 * NW == B_BYTES, "copy split");
     static_assert(!DUAL || NW % 2 == 0, "half of the waves copy each B matrix");
-    static_assert(LDS <= 160 * 1024 && NW * STG <= LDS, "LDS budget");
+    static_assert(LDS <= 160 * 1024 && SUMS + NW * STG <= LDS, "LDS budget");
+    static_assert(!DEEP || KG == 1, "ping-pong: one group of k-tiles");
     static_assert((S - 1) * L < 64, "vmcnt range");
     static_assert(!DEEP || S == 2, "the B-deep ring has two A and three B slots");
 };
@@ -286,17 +291,21 @@ struct ProductGeom {
 //   SEG   the sum may run over two segments with a B matrix each
 //   REG   operands whose rows or base are not 16-byte aligned: k-tiles go through VGPRs
 //         (two slots), loaded at any alignment; else they are copied straight into LDS
-// A k-tile's barrier sits after the last LDS read of its slot; it publishes the next k-tile
-// and releases the slot, which is refilled (k-tile t+S) behind it.  DEEP: the copies of B
-// have one k-tile more to land (k-tile t+3), those of A k-tile t+2.
+//   DEEP  a ring of two A and three B slots under the ping-pong schedule (the K loop)
+//   KG    the waves form KG groups that take the k-tiles in turn: more waves to hide the
+//         latencies of LDS reads, copies and barrier around the few MFMAs of a small tile
+//         (64 x 128, 256 workgroups, 128 k-tiles: 44.2 us with one group of four waves and
+//         six slots, 40.4 with two groups and three slots each)
+// Otherwise a k-tile's barrier sits after the last LDS read of its slot; it publishes the
+// next k-tile and releases the slot, which is refilled (k-tile t+S) behind it.
 // Reads past an operand: rows past the end fall outside the buffer resource and read zero.
 // A K-contiguous row's last k-tile masks the chunks past K by an offset outside every
 // resource, so nothing of the next row is read: a 0 * inf could not be undone.
 template <int ET, bool A_T, bool B_N, bool DUAL, bool SEG, bool REG, int BM, int BN, int WM, int WN,
-          int S, bool DEEP>
-__global__ void __launch_bounds__((ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP>::NT))
+          int S, bool DEEP, int KG>
+__global__ void __launch_bounds__((ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP, KG>::NT))
 product_kernel(ProductArgs args) {
-    using G = ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP>;
+    using G = ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP, KG>;
     constexpr int TM = G::TM, TN = G::TN, BNS = G::BNS, WNS = G::WNS, NW = G::NW;
     constexpr int A_OPS = G::A_OPS, B_OPS = G::B_OPS, L = G::L;
     constexpr int ES = ET == kElI8 ? 1 : 2;           // bytes of an element
@@ -307,16 +316,18 @@ product_kernel(ProductArgs args) {
     static_assert(!DUAL || !A_T, "gated: A is [M,K]");
 
     __shared__ __attribute__((aligned(1024))) char lds[G::LDS];
-    SPG_LDS char* ring = (SPG_LDS char*)lds;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave_id = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int kg = KG > 1 ? wave_id / NW : 0;         // group of k-tiles, wave within it
+    const int wave = KG > 1 ? wave_id - kg * NW : wave_id;
+    SPG_LDS char* ring = (SPG_LDS char*)lds + kg * G::RING;
     struct Slot { SPG_LDS char* a; SPG_LDS char* b; };
-    constexpr int NS = DEEP ? 6 : S;                  // period of the slot pattern
+    constexpr int NS = DEEP ? 6 : REG ? 4 : S;        // period of the slot (and register) pattern
     auto slot_of = [&](auto ic) -> Slot {
         constexpr int i = decltype(ic)::value % NS;
         return Slot{ring + (i % G::NA) * G::A_BYTES, ring + G::NA * G::A_BYTES + (i % G::NB) * G::B_BYTES};
     };
 
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / G::WAVES_N, wn = wave % G::WAVES_N;
 
     if constexpr (kPoison) {
@@ -335,7 +346,8 @@ product_kernel(ProductArgs args) {
     const int nkt = SEG ? seg_kt * args.segments : seg_kt;
     const int kt0 = sp * args.kt_part;
     const int kt1 = kt0 + args.kt_part < nkt ? kt0 + args.kt_part : nkt;
-    const int nk = kt1 - kt0;                         // k-tiles of this part (>= 1)
+    const int nk = (kt1 - kt0 + KG - 1) / KG;         // k-tiles of this part a group takes (>= 1)
+    auto kt_of = [&](int t) { return kt0 + t * KG + kg; };
     const int tail = K * ES - (seg_kt - 1) * 128;     // bytes of a segment's last k-tile
 
     // ---- copy sources ----
@@ -492,22 +504,37 @@ product_kernel(ProductArgs args) {
             if constexpr (!REG) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         }
     };
-    // register staging: one k-tile of loads in flight
-    u32x4 staged[REG ? L : 1];
-    auto gload = [&](int kt) __attribute__((always_inline)) {
+    // register staging: PD k-tiles of loads in flight (a k-tile of a small tile is multiplied
+    // in a fraction of the memory's latency)
+    constexpr int PD = L >= 6 ? 2 : 4;
+    u32x4 staged[REG ? PD : 1][REG ? L : 1];
+    auto gload = [&](auto pc, int kt) __attribute__((always_inline)) {
+        constexpr int p = decltype(pc)::value % PD;
         const Win a = a_win(kt), b = b_win(kt);
         const auto ra = make_rsrc_b((const void*)(uintptr_t)a.p, a.n), rb = make_rsrc_b((const void*)(uintptr_t)b.p, b.n);
         const int lim = klim(kt);
         static_for<0, L>([&](auto jc) {
             constexpr int j = decltype(jc)::value;
-            staged[j] = __builtin_amdgcn_raw_buffer_load_b128(j < A_OPS ? ra : rb, (int)src_off(jc, lim), 0, 0);
+            staged[p][j] = __builtin_amdgcn_raw_buffer_load_b128(j < A_OPS ? ra : rb, (int)src_off(jc, lim), 0, 0);
         });
     };
-    auto lwrite = [&](const Slot& s, int kt) __attribute__((always_inline)) {
+    // columns past the last reach into this workgroup's tile
+    const bool cut = (A_T && m0 + BM > args.a_cols) || (B_N && n0 + BNS > args.b_cols);
+    auto lwrite = [&](const Slot& s, auto pc, int kt) __attribute__((always_inline)) {
+        constexpr int p = decltype(pc)::value % PD;
         const int lim = klim(kt);
+        // only the last k-tile and the last column tile have chunks to realign: a 128-bit
+        // shift by a lane's own amount is about 20 instructions, and doing it for every
+        // chunk took longer than the multiplications of the small tiles
+        if (lim == 128 && !cut) {
+            static_for<0, L>([&](auto jc) {
+                *(SPG_LDS u32x4*)(lds_dst(s, jc) + lane * 16) = staged[p][decltype(jc)::value];
+            });
+            return;
+        }
         static_for<0, L>([&](auto jc) {
             constexpr int j = decltype(jc)::value;
-            *(SPG_LDS u32x4*)(lds_dst(s, jc) + lane * 16) = shr128(staged[j], src_shift(jc, lim));
+            *(SPG_LDS u32x4*)(lds_dst(s, jc) + lane * 16) = shr128(staged[p][j], src_shift(jc, lim));
         });
     };
 
@@ -601,60 +628,131 @@ product_kernel(ProductArgs args) {
         });
     };
 
-    Frags fr[2];
     using C0 = std::integral_constant<int, 0>;
     using C1 = std::integral_constant<int, 1>;
-    const Src none{};
+    using C2 = std::integral_constant<int, 2>;
     if constexpr (REG) {
-        gload(kt0);
-        lwrite(slot_of(C0{}), kt0);
-        gload(kt0 + 1);
+        static_for<0, PD>([&](auto pc) { gload(pc, kt_of(decltype(pc)::value)); });
+        lwrite(slot_of(C0{}), C0{}, kt_of(0));
+        gload(C0{}, kt_of(PD));
     } else if constexpr (DEEP) {
         issue(slot_of(C0{}), kt0);
         issue(slot_of(C1{}), kt0 + 1);
         const Src src = src_ab(kt0 + 2, kt0 + 2);
-        static_for<A_OPS, L>([&](auto jc) { dma_op(slot_of(std::integral_constant<int, 2>{}), src, jc); });
+        static_for<A_OPS, L>([&](auto jc) { dma_op(slot_of(C2{}), src, jc); });
         wait_vmcnt<L + B_OPS>();
     } else {
-        static_for<0, S>([&](auto sc) { issue(slot_of(sc), kt0 + decltype(sc)::value); });
+        static_for<0, S>([&](auto sc) { issue(slot_of(sc), kt_of(decltype(sc)::value)); });
         wait_vmcnt<(S - 1) * L>();
     }
     lds_barrier();
-    static_for<0, NRD>([&](auto rc) { read_op(slot_of(C0{}), 0, fr[0], rc); });
-
-    auto ktile = [&](auto sc, int kt) __attribute__((always_inline)) {
-        constexpr int s = decltype(sc)::value;
-        const Slot cur = slot_of(sc);
-        const Slot nxt = slot_of(std::integral_constant<int, s + 1>{});
-        stage(fr[0], cur, 1, fr[1], cur, none, std::false_type{});
-        if constexpr (REG) {
-            // nxt was released by the previous barrier
-            poison_slot(nxt);
-            lwrite(nxt, kt + 1);
-            gload(kt + 2);
-        } else {
-            wait_vmcnt<DEEP ? B_OPS : (S - 2) * L>();
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        lds_barrier();
-        __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_setprio(1);
-        if constexpr (REG) {
-            stage(fr[1], nxt, 0, fr[0], cur, none, std::false_type{});
-        } else {
-            poison_slot(cur);
-            const Src src = DEEP ? src_ab(kt + 2, kt + 3) : src_ab(kt + S, kt + S);
-            stage(fr[1], nxt, 0, fr[0], cur, src, std::true_type{});
-        }
-        __builtin_amdgcn_s_setprio(0);
+    auto over_ktiles = [&](auto&& ktile) __attribute__((always_inline)) {
+        int t = 0;
+        for (; t + NS <= nk; t += NS) static_for<0, NS>([&](auto sc) { ktile(sc, t + decltype(sc)::value); });
+        const int rem = nk - t;
+        static_for<0, NS - 1>([&](auto sc) {
+            if (decltype(sc)::value < rem) ktile(sc, t + decltype(sc)::value);
+        });
     };
-    int t = 0;
-    for (; t + NS <= nk; t += NS)
-        static_for<0, NS>([&](auto sc) { ktile(sc, kt0 + t + decltype(sc)::value); });
-    const int rem = nk - t;
-    static_for<0, NS - 1>([&](auto sc) {
-        if (decltype(sc)::value < rem) ktile(sc, kt0 + t + decltype(sc)::value);
-    });
+    if constexpr (DEEP) {
+        // The large tile runs the ping-pong schedule of pipelined_gemm (schedule 2 there): the
+        // two waves of a SIMD (w and w + 4) take turns, one issuing a k-step's MFMAs while
+        // the other reads the next fragments and copies, a workgroup barrier between turns.
+        // Group 1 runs one phase behind group 0.  K-tile u is read in phases 4u .. 4u+3; its
+        // slots are refilled (A of u+2, B of u+3) in the first memory phase of k-tile u+1;
+        // before the barrier that opens k-tile u+1's first read every wave has waited for
+        // its copies of A(u+1) and B(u+1), leaving B(u+2) in flight.  One fragment set is
+        // enough, which leaves the registers that the masks and addresses need: with two
+        // sets (the schedule of the smaller tiles) this tile spills up to 60 registers.
+        static_assert(!DEEP || NW == 8, "two groups of four waves");
+        const int grp = wave >> 2;
+        auto phase_barrier = []() __attribute__((always_inline)) {
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("s_barrier" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        Frags f;
+        auto matrix_phase = [&]() __attribute__((always_inline)) {
+            static_for<0, NMMA>([&](auto ic) {
+                constexpr int i = decltype(ic)::value, bn = i / TM, bm = i % TM;
+                acc[bn][bm] = mma<ET>(f.b[bn], f.a[bm], acc[bn][bm]);
+            });
+        };
+        if (grp == 1) phase_barrier();
+        over_ktiles([&](auto sc, int u) __attribute__((always_inline)) {
+            constexpr int i = decltype(sc)::value;
+            const Slot cur = slot_of(sc);
+            const Slot prev = slot_of(std::integral_constant<int, i + 5>{});
+            static_for<0, NRD>([&](auto rc) { read_op(cur, 0, f, rc); });
+            if (u >= 1) {
+                poison_slot(prev);
+                const Src src = src_ab(kt0 + u + 1, kt0 + u + 2);
+                static_for<0, L>([&](auto jc) { dma_op(prev, src, jc); });
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            phase_barrier();
+            matrix_phase();
+            phase_barrier();
+            static_for<0, NRD>([&](auto rc) { read_op(cur, 1, f, rc); });
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            if (grp == 1) wait_vmcnt<B_OPS>();
+            phase_barrier();
+            matrix_phase();
+            if (grp == 0) wait_vmcnt<B_OPS>();
+            phase_barrier();
+        });
+        if (grp == 0) phase_barrier();
+    } else {
+        Frags fr[2];
+        static_for<0, NRD>([&](auto rc) { read_op(slot_of(C0{}), 0, fr[0], rc); });
+        const Src none{};
+        over_ktiles([&](auto sc, int t) __attribute__((always_inline)) {
+            constexpr int s = decltype(sc)::value;
+            using Next = std::integral_constant<int, s + 1>;
+            const Slot cur = slot_of(sc);
+            const Slot nxt = slot_of(Next{});
+            stage(fr[0], cur, 1, fr[1], cur, none, std::false_type{});
+            if constexpr (REG) {
+                // nxt was released by the previous barrier
+                poison_slot(nxt);
+                lwrite(nxt, Next{}, kt_of(t + 1));
+                gload(Next{}, kt_of(t + 1 + PD));
+            } else {
+                wait_vmcnt<(S - 2) * L>();
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            lds_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_setprio(1);
+            if constexpr (REG) {
+                stage(fr[1], nxt, 0, fr[0], cur, none, std::false_type{});
+            } else {
+                poison_slot(cur);
+                const Src src = src_ab(kt_of(t + S), kt_of(t + S));
+                stage(fr[1], nxt, 0, fr[0], cur, src, std::true_type{});
+            }
+            __builtin_amdgcn_s_setprio(0);
+        });
+    }
+
+    // ---- the groups' sums meet, added in group order ----
+    if constexpr (KG > 1) {
+        wait_vmcnt<0>();
+        __syncthreads();
+        SPG_LDS AccOf<ET>* sums = (SPG_LDS AccOf<ET>*)(SPG_LDS char*)lds;
+        if (kg > 0) {
+#pragma unroll
+            for (int i = 0; i < TN * TM; ++i)
+                sums[(((kg - 1) * NW + wave) * TN * TM + i) * 64 + lane] = acc[i / TM][i % TM];
+        }
+        __syncthreads();
+        if (kg > 0) return;
+#pragma unroll
+        for (int g = 1; g < KG; ++g)
+#pragma unroll
+            for (int i = 0; i < TN * TM; ++i)
+                acc[i / TM][i % TM] += sums[(((g - 1) * NW + wave) * TN * TM + i) * 64 + lane];
+    }
 
     // ---- epilogue ----
     const int m_base = m0 + wm * WM, n_base = n0 + wn * WNS;
@@ -677,9 +775,11 @@ product_kernel(ProductArgs args) {
         wait_vmcnt<0>();   // the zero-fill copies past the last k-tile land before the LDS is given up
         return;
     }
-    wait_vmcnt<0>();
-    __syncthreads();
-    char* stg = lds + wave * G::STG;
+    if constexpr (KG == 1) {
+        wait_vmcnt<0>();
+        __syncthreads();
+    }
+    char* stg = lds + G::SUMS + wave * G::STG;
     if constexpr (ET == kElI8) {
         float rs[TM];
 #pragma unroll
@@ -736,27 +836,31 @@ product_kernel(ProductArgs args) {
 }
 
 // ---------------------------------------------------------------------------
-// few rows: the weights stream through registers
+// up to 16 rows: the weights stream through registers
 // ---------------------------------------------------------------------------
 //
-// For M <= 16 TM rows and K-contiguous weights the product is the reading of the weights:
-// every weight is used by one workgroup, so nothing is gained by LDS tiles.  A workgroup
-// takes 16 NB columns of each B matrix, its NW waves share K (wave w the chunks w, w + NW,
-// ... of U * 64 bytes a row), each lane loads its 16-byte MFMA operands straight from
-// memory at any alignment (row l%16, bytes 16 (l/16) of every 64), and the waves' sums meet
-// in LDS, added in wave order.
-template <int ET, bool DUAL, int TM, int NB, int NW, int U>
+// For M <= 16 and K-contiguous weights the product is the reading of the weights: every
+// weight is used once, so nothing is gained by LDS tiles.  A workgroup takes 16 columns of
+// each B matrix; its NW waves share K (wave w the chunks w, w + NW, ... of U * 64 bytes a
+// row), each lane loads its 16-byte MFMA operands straight from memory at any alignment
+// (row l%16, bytes 16 (l/16) of every 64), and the waves' sums meet in LDS, added in wave
+// order.  Each load touches 16 rows, half a cache line each: about 20 bytes a cycle and CU,
+// twice what HBM delivers, so for more rows, whose X is loaded the same way by every
+// workgroup, LDS tiles are faster (M = 64, N = 4096, K = 12288 int8: 28.5 us this way, 13
+// with a tile).  Measured at M = 1, N = 12288, K = 4096 bf16, two weights: 38.3 us, 5.25
+// TB/s; a second chunk in flight a wave 41.0, 16 waves 37.6 to 42.6, 4 waves 40.3,
+// loads marked nontemporal 39.6 (int8, M = 4: 10.7 against 14.6).
+template <int ET, bool DUAL, int NW, int U>
 __global__ void __launch_bounds__(NW * 64) stream_kernel(ProductArgs args) {
     constexpr int ES = ET == kElI8 ? 1 : 2;
     constexpr int NM = DUAL ? 2 : 1;
-    constexpr int FR = NM * NB * TM;                  // accumulators of a wave
-    __shared__ __attribute__((aligned(16))) AccOf<ET> sums[NW][FR][64];
+    __shared__ __attribute__((aligned(16))) AccOf<ET> sums[NW][NM][64];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int M = args.M, N = args.N;
     const int kb = args.K * ES;                       // bytes of a row
-    const int n0 = blockIdx.x * (16 * NB);
-    const int rows = N - n0 < 16 * NB ? N - n0 : 16 * NB;
+    const int n0 = blockIdx.x * 16;
+    const int rows = N - n0 < 16 ? N - n0 : 16;
     const uint32_t ldb = (uint32_t)args.ldb, lda = (uint32_t)args.lda;
     const uint32_t bbytes = (uint32_t)(rows - 1) * ldb + (uint32_t)kb;
     const auto rx = make_rsrc_b(args.A[0], (uint32_t)(M - 1) * lda + (uint32_t)kb);
@@ -764,36 +868,25 @@ __global__ void __launch_bounds__(NW * 64) stream_kernel(ProductArgs args) {
     const auto rb1 = make_rsrc_b((DUAL ? args.B[1] : args.B[0]) + (size_t)n0 * ldb, bbytes);
     const bool ragged = (kb & 15) != 0;
 
-    AccOf<ET> acc[NM][NB][TM];
+    AccOf<ET> acc[NM];
 #pragma unroll
     for (int q = 0; q < NM; ++q)
 #pragma unroll
-        for (int i = 0; i < NB; ++i)
-#pragma unroll
-            for (int j = 0; j < TM; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[q][i][j][e] = 0;
+        for (int e = 0; e < 4; ++e) acc[q][e] = 0;
 
     const uint32_t wrow = (uint32_t)(lane & 15) * ldb, xrow = (uint32_t)(lane & 15) * lda;
     for (int base = wave * (U * 64); base < kb; base += NW * U * 64) {
-        u32x4 w[NM][NB][U], x[TM][U];
+        u32x4 w[NM][U], x[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int k = base + u * 64 + 16 * (lane >> 4);
-            // the chunk past K reads zero; the one that straddles it, the 16 bytes ending at K
-            const int kw = k + 16 <= kb ? k : kb - 16;
+            // the bytes past K read zero; the 16 that straddle it are the 16 ending at K
+            const uint32_t kw = (uint32_t)(k + 16 <= kb ? k : kb - 16);
             const bool in = k < kb;
-#pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                const uint32_t o = in ? wrow + (uint32_t)(i * 16) * ldb + (uint32_t)kw : kOOB;
-                w[0][i][u] = __builtin_amdgcn_raw_buffer_load_b128(rb0, (int)o, 0, 0);
-                if constexpr (DUAL) w[NM - 1][i][u] = __builtin_amdgcn_raw_buffer_load_b128(rb1, (int)o, 0, 0);
-            }
-#pragma unroll
-            for (int j = 0; j < TM; ++j) {
-                const uint32_t o = in ? xrow + (uint32_t)(j * 16) * lda + (uint32_t)kw : kOOB;
-                x[j][u] = __builtin_amdgcn_raw_buffer_load_b128(rx, (int)o, 0, 0);
-            }
+            const uint32_t o = in ? wrow + kw : kOOB;
+            w[0][u] = __builtin_amdgcn_raw_buffer_load_b128(rb0, (int)o, 0, 0);
+            if constexpr (DUAL) w[NM - 1][u] = __builtin_amdgcn_raw_buffer_load_b128(rb1, (int)o, 0, 0);
+            x[u] = __builtin_amdgcn_raw_buffer_load_b128(rx, (int)(in ? xrow + kw : kOOB), 0, 0);
         }
         if (ragged && base + U * 64 > kb) {
 #pragma unroll
@@ -801,46 +894,31 @@ __global__ void __launch_bounds__(NW * 64) stream_kernel(ProductArgs args) {
                 const int k = base + u * 64 + 16 * (lane >> 4);
                 const uint32_t sh = k < kb && k + 16 > kb ? 8u * (uint32_t)(k + 16 - kb) : 0u;
 #pragma unroll
-                for (int i = 0; i < NB; ++i)
-#pragma unroll
-                    for (int q = 0; q < NM; ++q) w[q][i][u] = shr128(w[q][i][u], sh);
-#pragma unroll
-                for (int j = 0; j < TM; ++j) x[j][u] = shr128(x[j][u], sh);
+                for (int q = 0; q < NM; ++q) w[q][u] = shr128(w[q][u], sh);
+                x[u] = shr128(x[u], sh);
             }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int q = 0; q < NM; ++q)
-#pragma unroll
-                for (int i = 0; i < NB; ++i)
-#pragma unroll
-                    for (int j = 0; j < TM; ++j) acc[q][i][j] = mma<ET>(w[q][i][u], x[j][u], acc[q][i][j]);
+            for (int q = 0; q < NM; ++q) acc[q] = mma<ET>(w[q][u], x[u], acc[q]);
     }
 #pragma unroll
-    for (int q = 0; q < NM; ++q)
-#pragma unroll
-        for (int i = 0; i < NB; ++i)
-#pragma unroll
-            for (int j = 0; j < TM; ++j) sums[wave][(q * NB + i) * TM + j][lane] = acc[q][i][j];
+    for (int q = 0; q < NM; ++q) sums[wave][q][lane] = acc[q];
     __syncthreads();
 
-    // output: 4 consecutive columns of one row per item
-    for (int it = tid; it < NB * TM * 64; it += NW * 64) {
-        const int f = it >> 6, l = it & 63;
-        const int m = (f % TM) * 16 + (l & 15), n = n0 + (f / TM) * 16 + 4 * (l >> 4);
-        if (m >= M || n >= N) continue;
-        AccOf<ET> s[NM];
+    // output: 4 consecutive columns of one row a lane of the first wave
+    if (wave > 0) return;
+    const int m = lane & 15, n = n0 + 4 * (lane >> 4);
+    if (m >= M || n >= N) return;
+    AccOf<ET> s[NM];
 #pragma unroll
-        for (int q = 0; q < NM; ++q) {
-            s[q] = sums[0][q * NB * TM + f][l];
+    for (int q = 0; q < NM; ++q) {
+        s[q] = sums[0][q][lane];
 #pragma unroll
-            for (int w = 1; w < NW; ++w) s[q] += sums[w][q * NB * TM + f][l];
-        }
-        const int left = N - n < 4 ? N - n : 4;
-        const size_t o = (size_t)m * N + n;
-        finish4<ET, DUAL>(s[0], s[NM - 1], m, n, left, o, args);
+        for (int w = 1; w < NW; ++w) s[q] += sums[w][q][lane];
     }
+    finish4<ET, DUAL>(s[0], s[NM - 1], m, n, N - n < 4 ? N - n : 4, (size_t)m * N + n, args);
 }
 
 // ---------------------------------------------------------------------------

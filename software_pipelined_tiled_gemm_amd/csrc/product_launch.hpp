@@ -22,39 +22,49 @@ enum {
 };
 
 // Tile classes: rows x columns of a workgroup's tile (DUAL: columns of both matrices)
-enum { kTileBig = 0, kTileMid = 1, kTileSmall = 2, kTiles = 3 };
-constexpr int kTileM[kTiles] = {256, 128, 64};
-constexpr int kTileN[kTiles] = {256, 128, 128};
+enum { kTileBig = 0, kTileTall = 1, kTileMid = 2, kTileSmall = 3, kTileNarrow = 4, kTiles = 5 };
+constexpr int kTileM[kTiles] = {256, 256, 128, 64, 64};
+constexpr int kTileN[kTiles] = {256, 128, 128, 128, 64};
 
 template <int ET, int P, bool REG>
 void launch_product(int tile, const ProductArgs& a, dim3 grid, hipStream_t st);
 
 #ifdef SPG_DEFINE_PRODUCT
-template <int ET, int P, bool REG, int BM, int BN, int WM, int WN, int S, bool DEEP>
+template <int ET, int P, bool REG, int BM, int BN, int WM, int WN, int S, bool DEEP, int KG>
 void launch_tile(const ProductArgs& a, dim3 grid, hipStream_t st) {
     constexpr bool AT = P == kGradW, BNC = P == kGatedKN || P == kGradXNK || P == kGradW;
     constexpr bool DUAL = P == kGatedNK || P == kGatedKN || P == kInt8Gated;
     constexpr bool SEG = P == kGradXNK || P == kGradXKN;
-    hipLaunchKernelGGL((product_kernel<ET, AT, BNC, DUAL, SEG, REG, BM, BN, WM, WN, S, DEEP>), grid,
-                       dim3(ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP>::NT), 0, st, a);
+    hipLaunchKernelGGL((product_kernel<ET, AT, BNC, DUAL, SEG, REG, BM, BN, WM, WN, S, DEEP, KG>), grid,
+                       dim3(ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP, KG>::NT), 0, st, a);
 }
 
 template <int ET, int P, bool REG>
 void launch_product(int tile, const ProductArgs& a, dim3 grid, hipStream_t st) {
     constexpr bool DUAL = P == kGatedNK || P == kGatedKN || P == kInt8Gated;
+    // The ping-pong schedule and its deeper ring (DEEP) where B is K-contiguous and for the
+    // long sum of the input gradient; the compiler-placed one on two slots where the
+    // reduction-major reads need more addresses.
+    constexpr bool DEEP = P != kGatedKN && P != kGradW;
     if constexpr (!REG) {
         if (tile == kTileBig) {
             // DUAL: 64 x 128 per wave, so that a wave's output rows are whole 128-byte lines
-            if constexpr (DUAL) launch_tile<ET, P, REG, 256, 256, 64, 128, 2, false>(a, grid, st);
-            else launch_tile<ET, P, REG, 256, 256, 128, 64, 2, false>(a, grid, st);
+            if constexpr (DUAL) launch_tile<ET, P, REG, 256, 256, 64, 128, 2, DEEP, 1>(a, grid, st);
+            else launch_tile<ET, P, REG, 256, 256, 128, 64, 2, DEEP, 1>(a, grid, st);
+        } else if (tile == kTileTall) {
+            launch_tile<ET, P, REG, 256, 128, 64, 64, 3, false, 1>(a, grid, st);
         } else if (tile == kTileMid) {
-            launch_tile<ET, P, REG, 128, 128, 32, 64, 4, false>(a, grid, st);
+            launch_tile<ET, P, REG, 128, 128, 32, 64, 4, false, 1>(a, grid, st);
+        } else if (tile == kTileSmall) {
+            launch_tile<ET, P, REG, 64, 128, 32, 64, 3, false, 2>(a, grid, st);
         } else {
-            launch_tile<ET, P, REG, 64, 128, 32, 64, 6, false>(a, grid, st);
+            launch_tile<ET, P, REG, 64, 64, 32, 64, 2, false, 4>(a, grid, st);
         }
     } else {
-        if (tile == kTileMid) launch_tile<ET, P, REG, 128, 128, 32, 64, 2, false>(a, grid, st);
-        else launch_tile<ET, P, REG, 64, 128, 32, 64, 2, false>(a, grid, st);
+        if (tile == kTileTall) launch_tile<ET, P, REG, 256, 128, 64, 64, 2, false, 1>(a, grid, st);
+        else if (tile == kTileMid) launch_tile<ET, P, REG, 128, 128, 32, 64, 2, false, 1>(a, grid, st);
+        else if (tile == kTileSmall) launch_tile<ET, P, REG, 64, 128, 32, 64, 2, false, 1>(a, grid, st);
+        else launch_tile<ET, P, REG, 64, 64, 32, 64, 2, false, 4>(a, grid, st);
     }
 }
 #endif
