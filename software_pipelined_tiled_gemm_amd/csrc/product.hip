@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <new>
 
 #include "errors.hpp"
@@ -39,6 +40,7 @@ struct Shape {
 struct Tiling {
     int tile, split;
     int64_t kt_part;
+    double us;         // estimated
 };
 
 // Estimated microseconds of a tile class and a number of parts.  A tile class fills a CU's
@@ -51,7 +53,7 @@ struct Tiling {
 Tiling choose(const Shape& s, bool reg) {
     const double kt_us[spg::kTiles] = {1.50, 0.89, 0.53, 0.36, 0.25};
     const double start_us[spg::kTiles] = {5.5, 3.5, 2.5, 2.8, 3.2};
-    Tiling best{spg::kTileSmall, 1, s.kt};
+    Tiling best{spg::kTileSmall, 1, s.kt, 0.0};
     double best_t = -1.0;
     for (int t = 0; t < spg::kTiles; ++t) {
         if (reg && t == spg::kTileBig) continue;   // register staging: no 256x256 tile
@@ -66,17 +68,83 @@ Tiling choose(const Shape& s, bool reg) {
             if (split > 1) us += 3.5 + 2.0 * 4.0 * (double)split * s.M * s.zm * s.N * s.zn * s.mats / 5.0e6;
             if (best_t < 0 || us < best_t) {
                 best_t = us;
-                best = Tiling{t, (int)split, part};
+                best = Tiling{t, (int)split, part, us};
             }
         }
     }
     return best;
 }
 
+// A matrix of a product as its caller stores it, and its copy with 128-byte rows.
+struct Stored {
+    int64_t rows, row_bytes;
+    int64_t pitch() const { return up(row_bytes, 128); }
+    int64_t bytes() const { return rows * pitch(); }
+    bool aligned() const { return row_bytes % 16 == 0; }
+};
+
+// A product of a plan: its tilings with direct copies and register-staged, and whether
+// misaligned operands are laid out again first.
+struct Planned {
+    Shape s;
+    Tiling t[2];        // [register-staged]
+    bool pack;
+    int64_t parts;      // bytes of partial sums
+    int64_t packed;     // bytes of the copies
+    int64_t bytes() const { return parts + packed; }
+};
+
+// The copy reads and writes the misaligned matrices once (about 4.5 TB/s, and a launch).
+// M = 2048, N = 4096, K = 1001, two weights: register-staged 51.2 us, direct 30.3 and the
+// copy of 20 MB about 12; at M = 300, N = 2731 13.4 against 11.5 and 8.
+Planned plan_product(const Shape& s, std::initializer_list<Stored> mats);
+
 int64_t part_ld(const Shape& s) { return up(s.N, 4) * s.mats * s.zn; }
 int64_t part_bytes(const Shape& s, const Tiling& t) {
     return t.split > 1 ? up((int64_t)t.split * s.M * s.zm * part_ld(s) * 4, kAlign) : 0;
 }
+
+Planned plan_product(const Shape& s, std::initializer_list<Stored> mats) {
+    Planned p{s, {choose(s, false), choose(s, true)}, false, 0, 0};
+    int64_t all = 0, bad = 0;
+    for (const Stored& m : mats) {
+        all += up(m.bytes(), kAlign);
+        if (!m.aligned()) bad += m.bytes();
+    }
+    p.pack = bad > 0 && p.t[0].us + 3.0 + 2.0 * (double)bad / 4.5e6 < p.t[1].us;
+    p.parts = std::max(part_bytes(s, p.t[0]), part_bytes(s, p.t[1]));
+    p.packed = p.pack ? all : 0;
+    return p;
+}
+
+// Operands of one product on their way to a launch: pointers and pitches, replaced by those
+// of the copies where a plan lays misaligned ones out again.
+struct Operands {
+    spg::PackArgs pk{};
+    int n = 0;
+    int64_t total = 0;
+    char* at;           // where the next copy goes
+    explicit Operands(void* ws) : at((char*)ws) {}
+    void copy(const Stored& m, const char*& p, int64_t& pitch) {
+        pk.src[n] = p;
+        pk.dst[n] = at;
+        pk.row[n] = m.row_bytes;
+        pk.per[n] = (int32_t)(m.pitch() / 16);
+        pk.chunks[n] = m.bytes() / 16;
+        total += pk.chunks[n];
+        p = at;
+        pitch = m.pitch();
+        at += up(m.bytes(), kAlign);
+        ++n;
+    }
+    gemm_status launch(int es, hipStream_t st) const {
+        if (!n) return GEMM_OK;
+        const dim3 grid((unsigned)ceil_div(total, 256));
+        if (es == 1) hipLaunchKernelGGL(spg::pack_rows<1>, grid, dim3(256), 0, st, pk);
+        else hipLaunchKernelGGL(spg::pack_rows<2>, grid, dim3(256), 0, st, pk);
+        return launched();
+    }
+};
 
 template <int P, bool REG>
 void launch_type(int et, int tile, const ProductArgs& a, dim3 grid, hipStream_t st) {
@@ -104,8 +172,9 @@ void launch_tiled(int product, int et, bool reg, int tile, const ProductArgs& a,
 }
 
 // The tiled product and, for a split reduction, the sum of its parts.
-gemm_status run_tiled(int product, int et, bool reg, const Shape& s, const Tiling& t, ProductArgs a, void* parts,
-                      hipStream_t st) {
+gemm_status run_tiled(int product, int et, bool reg, const Planned& p, ProductArgs a, void* parts, hipStream_t st) {
+    const Shape& s = p.s;
+    const Tiling& t = p.t[reg];
     a.zm = s.zm;
     a.zn = s.zn;
     a.tiles_m = (int32_t)ceil_div(s.M, spg::kTileM[t.tile]);
@@ -164,8 +233,8 @@ struct gemm_gated_plan {
     int act;
     bool simple, simple_back;
     int64_t np;              // columns of dG and of dU in the workspace
-    Shape fwd, dx, dw;
-    Tiling t_fwd[2], t_dx[2], t_dw[2];   // [register-staged]
+    Stored x, w;
+    Planned fwd, dx, dw;
     int64_t ws_fwd, ws_back, off_part;
 };
 
@@ -173,10 +242,15 @@ struct gemm_quantized_plan {
     int64_t M, N, K;
     int out, act;
     bool simple;
-    Shape s;
-    Tiling t[2];
+    Stored a, b;
+    Planned p;
     int64_t ws;
 };
+
+namespace {
+// few rows with K-contiguous weights: the streaming kernel
+bool streams(const gemm_gated_plan* p) { return p->nk && p->M <= kStreamRows; }
+}  // namespace
 
 extern "C" {
 
@@ -204,25 +278,20 @@ gemm_status gemm_gated_create(gemm_gated_handle* out, int64_t M, int64_t N, int6
     p->simple = empty || K < 8 || (!p->nk && N < 8) || K * 2 > kMaxRowBytes || (!p->nk && N * 2 > kMaxRowBytes);
     p->np = up(N, 64);
     p->simple_back = p->simple || p->np * 4 > kMaxRowBytes || K == 0;
-    p->fwd = Shape{M, N, ceil_div(K, 64), 1, 1, 2, 2 * (m * k + 2 * n * k + m * n)};
-    p->dx = Shape{M, K, 2 * ceil_div(N, 64), 1, 1, 1, 2 * (2 * m * n + 2 * n * k + m * k)};
-    p->dw = p->nk ? Shape{N, K, ceil_div(M, 64), 2, 1, 1, 2 * (2 * m * n + 2 * n * k + m * k)}
-                  : Shape{K, N, ceil_div(M, 64), 1, 2, 1, 2 * (2 * m * n + 2 * n * k + m * k)};
-    p->ws_fwd = 0;
-    int64_t parts = 0;
-    for (int r = 0; r < 2; ++r) {
-        if (!p->simple) {
-            p->t_fwd[r] = choose(p->fwd, r == 1);
-            p->ws_fwd = std::max(p->ws_fwd, part_bytes(p->fwd, p->t_fwd[r]));
-        }
-        if (!p->simple_back) {
-            p->t_dx[r] = choose(p->dx, r == 1);
-            p->t_dw[r] = choose(p->dw, r == 1);
-            parts = std::max(parts, std::max(part_bytes(p->dx, p->t_dx[r]), part_bytes(p->dw, p->t_dw[r])));
-        }
+    p->x = Stored{M, K * 2};
+    p->w = p->nk ? Stored{N, K * 2} : Stored{K, N * 2};
+    const double grad_bytes = 2 * (2 * m * n + 2 * n * k + m * k);
+    p->fwd = p->dx = p->dw = Planned{};
+    if (!p->simple && !streams(p))
+        p->fwd = plan_product(Shape{M, N, ceil_div(K, 64), 1, 1, 2, 2 * (m * k + 2 * n * k + m * n)}, {p->x, p->w, p->w});
+    if (!p->simple_back) {
+        p->dx = plan_product(Shape{M, K, 2 * ceil_div(N, 64), 1, 1, 1, grad_bytes}, {p->w, p->w});
+        p->dw = plan_product(p->nk ? Shape{N, K, ceil_div(M, 64), 2, 1, 1, grad_bytes}
+                                   : Shape{K, N, ceil_div(M, 64), 1, 2, 1, grad_bytes}, {p->x});
     }
+    p->ws_fwd = p->fwd.bytes();
     p->off_part = up(M * p->np * 4, kAlign);
-    p->ws_back = p->off_part + parts;
+    p->ws_back = p->off_part + std::max(p->dx.bytes(), p->dw.bytes());
     *out = p;
     return GEMM_OK;
 }
@@ -253,16 +322,28 @@ gemm_status gemm_gated_run(gemm_gated_handle h, const void* X, const void* Wg, c
         spg::SimpleArgs s{a, h->K, 1, h->nk ? h->K : 1, h->nk ? 1 : h->N, 0};
         return h->et == spg::kElBF16 ? run_simple<spg::kElBF16, true>(s, stream) : run_simple<spg::kElF16, true>(s, stream);
     }
-    if (h->nk && h->M <= kStreamRows) {
+    if (streams(h)) {
         if (h->et == spg::kElBF16) stream_rows<spg::kElBF16, true>(a, stream);
         else stream_rows<spg::kElF16, true>(a, stream);
         return launched();
     }
-    const bool reg = a.lda % 16 != 0 || a.ldb % 16 != 0 || !is16(X) || !is16(Wg) || !is16(Wu);
-    const Tiling& t = h->t_fwd[reg];
-    if (t.split > 1 && (!workspace || (uintptr_t)workspace % 16 != 0 || workspace_bytes < part_bytes(h->fwd, t)))
-        return GEMM_ERR_INVALID_ARG;
-    return run_tiled(h->nk ? spg::kGatedNK : spg::kGatedKN, h->et, reg, h->fwd, t, a, workspace, stream);
+    const bool xa = a.lda % 16 == 0 && is16(X), wa = a.ldb % 16 == 0 && is16(Wg) && is16(Wu);
+    const bool pack = h->fwd.pack && !(xa && wa);
+    const bool reg = !pack && !(xa && wa);
+    const int64_t need = (pack ? h->fwd.packed : 0) + part_bytes(h->fwd.s, h->fwd.t[reg]);
+    if (need > 0 && (!workspace || (uintptr_t)workspace % 16 != 0 || workspace_bytes < h->ws_fwd)) return GEMM_ERR_INVALID_ARG;
+    if (pack) {
+        Operands o((char*)workspace + h->fwd.parts);
+        if (!xa) o.copy(h->x, a.A[0], a.lda);
+        if (!wa) {
+            o.copy(h->w, a.B[0], a.ldb);
+            o.copy(h->w, a.B[1], a.ldb);
+            a.b_cols = (int32_t)up(h->N, 8);
+        }
+        const gemm_status e = o.launch(2, stream);
+        if (e != GEMM_OK) return e;
+    }
+    return run_tiled(h->nk ? spg::kGatedNK : spg::kGatedKN, h->et, reg, h->fwd, a, workspace, stream);
 }
 
 gemm_status gemm_gated_backward(gemm_gated_handle h, const void* dH, const void* X, const void* Wg, const void* Wu,
@@ -308,8 +389,15 @@ gemm_status gemm_gated_backward(gemm_gated_handle h, const void* dH, const void*
             spg::SimpleArgs s{a, 2 * h->np, 1, h->nk ? 1 : N, h->nk ? K : 1, h->np};
             e = bf ? run_simple<spg::kElBF16, false>(s, stream) : run_simple<spg::kElF16, false>(s, stream);
         } else {
-            const bool reg = a.ldb % 16 != 0 || !is16(Wg) || !is16(Wu);
-            e = run_tiled(h->nk ? spg::kGradXNK : spg::kGradXKN, h->et, reg, h->dx, h->t_dx[reg], a, parts, stream);
+            const bool wa = a.ldb % 16 == 0 && is16(Wg) && is16(Wu);
+            if (!wa && h->dx.pack) {
+                Operands o((char*)parts + h->dx.parts);
+                o.copy(h->w, a.B[0], a.ldb);
+                o.copy(h->w, a.B[1], a.ldb);
+                a.b_cols = (int32_t)up(K, 8);
+                if ((e = o.launch(2, stream)) != GEMM_OK) return e;
+            }
+            e = run_tiled(h->nk ? spg::kGradXNK : spg::kGradXKN, h->et, !wa && !h->dx.pack, h->dx, a, parts, stream);
         }
         if (e != GEMM_OK) return e;
     }
@@ -344,8 +432,18 @@ gemm_status gemm_gated_backward(gemm_gated_handle h, const void* dH, const void*
             }
             return GEMM_OK;
         }
-        const bool reg = K % 8 != 0 || !is16(X);
-        return run_tiled(spg::kGradW, h->et, reg, h->dw, h->t_dw[reg], a, parts, stream);
+        const bool xa = K % 8 == 0 && is16(X);
+        if (!xa && h->dw.pack) {
+            Operands o((char*)parts + h->dw.parts);
+            const char* x = (const char*)X;
+            int64_t& pitch = h->nk ? a.ldb : a.lda;
+            o.copy(h->x, x, pitch);
+            (h->nk ? a.B : a.A)[0] = (h->nk ? a.B : a.A)[1] = x;
+            (h->nk ? a.b_cols : a.a_cols) = (int32_t)up(K, 8);
+            const gemm_status e = o.launch(2, stream);
+            if (e != GEMM_OK) return e;
+        }
+        return run_tiled(spg::kGradW, h->et, !xa && !h->dw.pack, h->dw, a, parts, stream);
     }
     return GEMM_OK;
 }
@@ -376,13 +474,14 @@ gemm_status gemm_quantized_create(gemm_quantized_handle* out, int64_t M, int64_t
     p->simple = M == 0 || N == 0 || K < 16;
     const double m = (double)M, n = (double)N, k = (double)K;
     const int mats = act == GEMM_ACT_NONE ? 1 : 2;
-    p->s = Shape{M, N, ceil_div(K, 128), 1, 1, mats, m * k + mats * n * k + m * n * (out_dtype == GEMM_F32 ? 4 : 2)};
-    p->ws = 0;
-    if (!p->simple)
-        for (int r = 0; r < 2; ++r) {
-            p->t[r] = choose(p->s, r == 1);
-            p->ws = std::max(p->ws, part_bytes(p->s, p->t[r]));
-        }
+    p->a = Stored{M, K};
+    p->b = Stored{N, K};
+    p->p = Planned{};
+    if (!p->simple && M > kStreamRows) {
+        const Shape s{M, N, ceil_div(K, 128), 1, 1, mats, m * k + mats * n * k + m * n * (out_dtype == GEMM_F32 ? 4 : 2)};
+        p->p = mats == 2 ? plan_product(s, {p->a, p->b, p->b}) : plan_product(s, {p->a, p->b});
+    }
+    p->ws = p->p.bytes();
     *out = p;
     return GEMM_OK;
 }
@@ -422,11 +521,22 @@ gemm_status gemm_quantized_run(gemm_quantized_handle h, const int8_t* A, const f
         else stream_rows<spg::kElI8, false>(a, stream);
         return launched();
     }
-    const bool reg = h->K % 16 != 0 || !is16(A) || !is16(B) || (dual && !is16(B2));
-    const Tiling& t = h->t[reg];
-    if (t.split > 1 && (!workspace || (uintptr_t)workspace % 16 != 0 || workspace_bytes < part_bytes(h->s, t)))
-        return GEMM_ERR_INVALID_ARG;
-    return run_tiled(dual ? spg::kInt8Gated : spg::kInt8, spg::kElI8, reg, h->s, t, a, workspace, stream);
+    const bool aa = h->K % 16 == 0 && is16(A), ba = h->K % 16 == 0 && is16(B) && (!dual || is16(B2));
+    const bool pack = h->p.pack && !(aa && ba);
+    const bool reg = !pack && !(aa && ba);
+    const int64_t need = (pack ? h->p.packed : 0) + part_bytes(h->p.s, h->p.t[reg]);
+    if (need > 0 && (!workspace || (uintptr_t)workspace % 16 != 0 || workspace_bytes < h->ws)) return GEMM_ERR_INVALID_ARG;
+    if (pack) {
+        Operands o((char*)workspace + h->p.parts);
+        if (!aa) o.copy(h->a, a.A[0], a.lda);
+        if (!ba) {
+            o.copy(h->b, a.B[0], a.ldb);
+            if (dual) o.copy(h->b, a.B[1], a.ldb);
+        }
+        const gemm_status e = o.launch(1, stream);
+        if (e != GEMM_OK) return e;
+    }
+    return run_tiled(dual ? spg::kInt8Gated : spg::kInt8, spg::kElI8, reg, h->p, a, workspace, stream);
 }
 
 gemm_status gemm_quantized_destroy(gemm_quantized_handle h) {

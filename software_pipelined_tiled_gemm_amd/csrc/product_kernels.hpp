@@ -349,6 +349,9 @@ product_kernel(ProductArgs args) {
     const int nk = (kt1 - kt0 + KG - 1) / KG;         // k-tiles of this part a group takes (>= 1)
     auto kt_of = [&](int t) { return kt0 + t * KG + kg; };
     const int tail = K * ES - (seg_kt - 1) * 128;     // bytes of a segment's last k-tile
+    // bytes of a K-contiguous row that may be read: direct copies move whole 16-byte chunks,
+    // of rows that are a multiple of that or have been laid out again, padded with zeros
+    const uint32_t row_bytes = REG ? (uint32_t)(K * ES) : ((uint32_t)(K * ES) + 15u) & ~15u;
 
     // ---- copy sources ----
     const char* a_ptr = args.A[!DUAL && args.zm == 2 ? z : 0];
@@ -372,7 +375,7 @@ product_kernel(ProductArgs args) {
             return Win{(uint64_t)(uintptr_t)a_ptr + sh, kt < kt1 ? (uint32_t)(left < tile ? left : tile) : 0u};
         } else {
             const uint32_t all = (uint32_t)(a_rows - 1) * (uint32_t)args.lda +
-                                 (SEG ? (uint32_t)args.lda : (uint32_t)(K * ES));
+                                 (SEG ? (uint32_t)args.lda : row_bytes);
             const uint32_t sh = (uint32_t)kt * 128u;
             return Win{(uint64_t)(uintptr_t)a_ptr + (uint64_t)m0 * (uint64_t)args.lda + sh - kBack,
                        kt < kt1 ? all - sh + kBack : 0u};
@@ -390,7 +393,7 @@ product_kernel(ProductArgs args) {
             const uint64_t left = all - sh, tile = 64u * (uint64_t)args.ldb;
             return Win{(uint64_t)(uintptr_t)p + sh, kt < kt1 ? (uint32_t)(left < tile ? left : tile) : 0u};
         } else {
-            const uint32_t all = (uint32_t)(b_rows - 1) * (uint32_t)args.ldb + (uint32_t)(K * ES);
+            const uint32_t all = (uint32_t)(b_rows - 1) * (uint32_t)args.ldb + row_bytes;
             const uint32_t sh = (uint32_t)k * 128u;
             return Win{(uint64_t)(uintptr_t)p + (uint64_t)n0 * (uint64_t)args.ldb + sh - kBack,
                        kt < kt1 ? all - sh + kBack : 0u};
@@ -711,15 +714,15 @@ product_kernel(ProductArgs args) {
             using Next = std::integral_constant<int, s + 1>;
             const Slot cur = slot_of(sc);
             const Slot nxt = slot_of(Next{});
-            stage(fr[0], cur, 1, fr[1], cur, none, std::false_type{});
             if constexpr (REG) {
-                // nxt was released by the previous barrier
+                // nxt was released by the previous barrier; its writes go first, so that they
+                // drain behind the MFMAs of this stage
                 poison_slot(nxt);
                 lwrite(nxt, Next{}, kt_of(t + 1));
                 gload(Next{}, kt_of(t + 1 + PD));
-            } else {
-                wait_vmcnt<(S - 2) * L>();
             }
+            stage(fr[0], cur, 1, fr[1], cur, none, std::false_type{});
+            if constexpr (!REG) wait_vmcnt<(S - 2) * L>();
             __builtin_amdgcn_sched_barrier(0);
             lds_barrier();
             __builtin_amdgcn_sched_barrier(0);
@@ -919,6 +922,45 @@ __global__ void __launch_bounds__(NW * 64) stream_kernel(ProductArgs args) {
         for (int w = 1; w < NW; ++w) s[q] += sums[w][q][lane];
     }
     finish4<ET, DUAL>(s[0], s[NM - 1], m, n, N - n < 4 ? N - n : 4, (size_t)m * N + n, args);
+}
+
+// ---------------------------------------------------------------------------
+// operands laid out again
+// ---------------------------------------------------------------------------
+//
+// Rows that do not start on 16 bytes, copied to rows that start on 128, zero past their end:
+// for large products the copy costs less than register-staged tiles lose.  One launch for
+// the matrices of a product; a thread moves 16 bytes.
+struct PackArgs {
+    const char* src[3];
+    char* dst[3];
+    int64_t chunks[3];    // 16-byte chunks of each destination (0: none)
+    int64_t row[3];       // bytes of a source row
+    int32_t per[3];       // chunks of a destination row
+};
+
+template <int ES>
+__global__ void __launch_bounds__(256) pack_rows(PackArgs a) {
+    int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    int q = 0;
+    while (q < 3 && i >= a.chunks[q]) i -= a.chunks[q++];
+    if (q == 3) return;
+    const int64_t r = i / a.per[q];
+    const int64_t c = (i - r * a.per[q]) * 16, left = a.row[q] - c;
+    const char* s = a.src[q] + r * a.row[q] + c;
+    u32x4 v = {};
+    if (left >= 16) {
+        struct __attribute__((packed, aligned(ES))) B { u32x4 v; };
+        v = ((const B*)s)->v;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 16; e += ES)
+            if (e < left) {
+                const uint32_t x = ES == 1 ? *(const uint8_t*)(s + e) : *(const uint16_t*)(s + e);
+                v[e >> 2] |= x << ((e & 3) * 8);
+            }
+    }
+    *(u32x4*)(a.dst[q] + i * 16) = v;
 }
 
 // ---------------------------------------------------------------------------

@@ -103,10 +103,11 @@ def _within(got, want, tol, what):
 
 
 # (M, N, K): few rows (1, 16, 17, 33, 64), tiles cut on every side, odd rows, one k-tile,
-# more parts of the reduction than one, grids of the 256-wide tile
+# more parts of the reduction than one, grids of the 256-wide tile, odd rows that are laid
+# out again
 SIZES = [(1, 48, 40), (1, 4096, 1001), (3, 130, 64), (16, 72, 200), (17, 96, 136), (33, 40, 8), (48, 56, 777),
          (64, 264, 512), (65, 100, 64), (129, 257, 320), (200, 64, 2048), (300, 2731, 1001), (511, 520, 500),
-         (70, 33, 9), (96, 1536, 4096), (1280, 2304, 192)]
+         (70, 33, 9), (96, 1536, 4096), (1280, 2304, 192), (1300, 2051, 1003)]
 
 
 def _gated_case(M, N, K, dtype, layout, seed, off=0):
