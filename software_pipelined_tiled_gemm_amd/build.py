@@ -6,7 +6,8 @@ number (with -DSPG_UNIT_IS_<n>=~,1 selecting that unit's lines), so the units co
 in parallel.  csrc/gemm.hip holds the GEMM's host side (C ABI, variant table) and
 csrc/gelu.hip the standalone elementwise GELU (include/spgelu.h).  The feed-forward
 operators are csrc/product.hip (host side) and csrc/product_unit.hip, compiled once per
-element type, product and copy mode.
+element type, product and copy mode.  csrc/binding.cpp becomes a module of its own,
+_calls.so.
 """
 
 from __future__ import annotations
@@ -15,6 +16,7 @@ import os
 import re
 import subprocess
 import sys
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
@@ -22,6 +24,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libspgemm.so")
+CALLS_OUT = os.path.join(HERE, "_calls.so")
 POISON_OUT = os.path.join(HERE, "libspgemm_poison.so")
 # Units of the poison library (a test instrument: -DSPG_POISON turns the ring's released
 # regions into NaN; see kPoison in csrc/gemm_kernels.hpp): every direct-to-LDS ring
@@ -88,6 +91,19 @@ def build(out: str = OUT, extra=(), poison: bool = False) -> str:
         tmp_out = out + ".tmp"
         subprocess.run(["hipcc", *FLAGS, "-shared", *objs, "-o", tmp_out], check=True)
         os.replace(tmp_out, out)
+    return out
+
+
+def build_calls(out: str = CALLS_OUT) -> str:
+    """Compile csrc/binding.cpp, the wrappers' call path for torch tensors (host code; the
+    Python and DLPack headers only, nothing linked)."""
+    import torch
+    inc = ["-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(os.path.dirname(torch.__file__), "include")]
+    tmp_out = out + ".tmp"
+    subprocess.run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", *inc,
+                    os.path.join(CSRC, "binding.cpp"), "-o", tmp_out], check=True)
+    os.replace(tmp_out, out)
     return out
 
 

@@ -43,6 +43,19 @@ struct Tiling {
     double us;         // estimated
 };
 
+// Measured per k-tile and per workgroup (us), see choose()
+constexpr double kTileUs[spg::kTiles] = {1.50, 0.89, 0.53, 0.36, 0.25};
+constexpr double kStartUs[spg::kTiles] = {5.5, 3.5, 2.5, 2.8, 3.2};
+constexpr double kStaged = 1.35;      // register-staged against direct copies
+constexpr double kLaunchUs = 1.5;
+
+double sum_us(const Shape& s, int64_t split) {
+    return split > 1 ? 3.5 + 2.0 * 4.0 * (double)split * s.M * s.zm * s.N * s.zn * s.mats / 5.0e6 : 0.0;
+}
+int64_t tiles_of(const Shape& s, int t) {
+    return ceil_div(s.M, spg::kTileM[t]) * s.zm * ceil_div(s.N, spg::kTileN[t] / s.mats) * s.zn;
+}
+
 // Estimated microseconds of a tile class and a number of parts.  A tile class fills a CU's
 // LDS, so a CU runs one workgroup at a time: rounds of the 256 CUs times a part's k-tiles and
 // a start and store per round, plus a launch; never less than the operands take to read.
@@ -51,21 +64,18 @@ struct Tiling {
 // less with few (a CU copies about 105 bytes a nanosecond into its LDS, which is what bounds
 // the small tiles); one k-tile alone 7, 5, 4, 4.4 and 4.8.  Register-staged tiles 1.35 times.
 Tiling choose(const Shape& s, bool reg) {
-    const double kt_us[spg::kTiles] = {1.50, 0.89, 0.53, 0.36, 0.25};
-    const double start_us[spg::kTiles] = {5.5, 3.5, 2.5, 2.8, 3.2};
     Tiling best{spg::kTileSmall, 1, s.kt, 0.0};
     double best_t = -1.0;
     for (int t = 0; t < spg::kTiles; ++t) {
         if (reg && t == spg::kTileBig) continue;   // register staging: no 256x256 tile
-        const int64_t tiles = ceil_div(s.M, spg::kTileM[t]) * s.zm * ceil_div(s.N, spg::kTileN[t] / s.mats) * s.zn;
+        const int64_t tiles = tiles_of(s, t);
         for (int64_t split = 1; split <= 32 && split <= s.kt; ++split) {
             const int64_t part = ceil_div(s.kt, split);
             if (split > 1 && (part < 4 || ceil_div(s.kt, part) != split)) continue;
             const double rounds = (double)ceil_div(tiles * split, 256);
             const double busy = 0.68 + 0.32 * std::min(1.0, (double)(tiles * split) / 256.0);
-            double us = 1.5 + rounds * (kt_us[t] * busy * (reg ? 1.35 : 1.0) * (double)part + start_us[t]);
-            us = std::max(us, 3.0 + s.bytes / 5.0e6);
-            if (split > 1) us += 3.5 + 2.0 * 4.0 * (double)split * s.M * s.zm * s.N * s.zn * s.mats / 5.0e6;
+            double us = kLaunchUs + rounds * (kTileUs[t] * busy * (reg ? kStaged : 1.0) * (double)part + kStartUs[t]);
+            us = std::max(us, 3.0 + s.bytes / 5.0e6) + sum_us(s, split);
             if (best_t < 0 || us < best_t) {
                 best_t = us;
                 best = Tiling{t, (int)split, part, us};
@@ -146,6 +156,39 @@ struct Operands {
     }
 };
 
+// Both gradients in one launch: tile class and parts of dX.
+struct Merged {
+    bool on;
+    int tile, split;
+    int64_t kt_part;
+};
+
+// One launch if its estimate is below that of two: the longest workgroup, or the work of all
+// of them over the CUs.  M = 511, N = 1365, K = 500: 10.0 + 3.9 (dX in 8 parts and their sum)
+// and 10.2 us apart.
+Merged merge(const Planned& x, const Planned& w, bool reg) {
+    Merged best{false, 0, 1, 0};
+    if (x.pack || w.pack) return best;
+    double best_us = x.t[reg].us + w.t[reg].us;
+    for (int t : {(int)spg::kTileMid, (int)spg::kTileSmall})
+        for (int64_t split = 1; split <= 16 && split <= x.s.kt; ++split) {
+            const int64_t part = ceil_div(x.s.kt, split);
+            if (split > 1 && (part < 4 || ceil_div(x.s.kt, part) != split)) continue;
+            const double k = kTileUs[t] * (reg ? kStaged : 1.0);
+            const double cx = k * (double)part + kStartUs[t], cw = k * (double)w.s.kt + kStartUs[t];
+            const int64_t nx = tiles_of(x.s, t) * split, nw = tiles_of(w.s, t);
+            const double all = ((double)nx * cx + (double)nw * cw) / 256.0;
+            // past one round the last workgroups leave CUs idle: half of one's time
+            double us = std::max(std::max(cx, cw), nx + nw > 256 ? all + 0.5 * std::max(cx, cw) : 0.0);
+            us = kLaunchUs + std::max(us, 3.0 + x.s.bytes / 5.0e6) + sum_us(x.s, split);
+            if (us < best_us) {
+                best_us = us;
+                best = Merged{true, t, (int)split, part};
+            }
+        }
+    return best;
+}
+
 template <int P, bool REG>
 void launch_type(int et, int tile, const ProductArgs& a, dim3 grid, hipStream_t st) {
     if constexpr (P == spg::kInt8 || P == spg::kInt8Gated) spg::launch_product<spg::kElI8, P, REG>(tile, a, grid, st);
@@ -171,27 +214,26 @@ void launch_tiled(int product, int et, bool reg, int tile, const ProductArgs& a,
     }
 }
 
-// The tiled product and, for a split reduction, the sum of its parts.
-gemm_status run_tiled(int product, int et, bool reg, const Planned& p, ProductArgs a, void* parts, hipStream_t st) {
-    const Shape& s = p.s;
-    const Tiling& t = p.t[reg];
+// Fill in the tile grid of a product; returns its workgroups.
+int64_t set_grid(ProductArgs& a, const Shape& s, int tile, int split, int64_t kt_part, void* parts) {
     a.zm = s.zm;
     a.zn = s.zn;
-    a.tiles_m = (int32_t)ceil_div(s.M, spg::kTileM[t.tile]);
-    a.tiles_n = (int32_t)ceil_div(s.N, spg::kTileN[t.tile] / s.mats);
+    a.tiles_m = (int32_t)ceil_div(s.M, spg::kTileM[tile]);
+    a.tiles_n = (int32_t)ceil_div(s.N, spg::kTileN[tile] / s.mats);
     // rows of tiles rastered together: 4 (measured at M = 8192, N = 12288: 2, 4, 8 and 16
     // take 1198, 1186, 1200 and 1215 us), all of them when there are few, else even groups,
     // so that no short last group reads every weight again
     const int64_t rows = (int64_t)a.tiles_m * a.zm;
     a.group_m = (int32_t)(rows <= 8 ? rows : ceil_div(rows, ceil_div(rows, 4)));
-    a.split = t.split;
-    a.kt_part = (int32_t)t.kt_part;
-    a.part = t.split > 1 ? (float*)parts : nullptr;
+    a.split = split;
+    a.kt_part = (int32_t)kt_part;
+    a.part = split > 1 ? (float*)parts : nullptr;
     a.ldp = part_ld(s);
-    const int64_t wgs = (int64_t)a.tiles_m * a.zm * a.tiles_n * a.zn * t.split;
-    launch_tiled(product, et, reg, t.tile, a, dim3((unsigned)wgs), st);
-    gemm_status e = launched();
-    if (e != GEMM_OK || t.split == 1) return e;
+    return rows * a.tiles_n * a.zn * split;
+}
+
+// The sum of a split reduction's parts.
+gemm_status run_sum(int et, const Shape& s, const ProductArgs& a, hipStream_t st) {
     const int64_t quads = s.M * s.zm * (up(s.N, 4) / 4) * s.zn;
     const dim3 grid((unsigned)ceil_div(quads, 256));
     const bool dual = s.mats == 2;
@@ -206,6 +248,36 @@ gemm_status run_tiled(int product, int et, bool reg, const Planned& p, ProductAr
         else hipLaunchKernelGGL((spg::sum_parts<spg::kElF16, false>), grid, dim3(256), 0, st, a);
     }
     return launched();
+}
+
+gemm_status run_tiled(int product, int et, bool reg, const Planned& p, ProductArgs a, void* parts, hipStream_t st) {
+    const Tiling& t = p.t[reg];
+    const int64_t wgs = set_grid(a, p.s, t.tile, t.split, t.kt_part, parts);
+    launch_tiled(product, et, reg, t.tile, a, dim3((unsigned)wgs), st);
+    const gemm_status e = launched();
+    return e != GEMM_OK || t.split == 1 ? e : run_sum(et, p.s, a, st);
+}
+
+template <int P>
+void launch_merged(int et, bool reg, int tile, const ProductArgs& x, const ProductArgs& w, int nx, dim3 grid, hipStream_t st) {
+    if (et == spg::kElBF16) {
+        if (reg) spg::launch_gradients<spg::kElBF16, P, true>(tile, x, w, nx, grid, st);
+        else spg::launch_gradients<spg::kElBF16, P, false>(tile, x, w, nx, grid, st);
+    } else {
+        if (reg) spg::launch_gradients<spg::kElF16, P, true>(tile, x, w, nx, grid, st);
+        else spg::launch_gradients<spg::kElF16, P, false>(tile, x, w, nx, grid, st);
+    }
+}
+
+gemm_status run_merged(bool nk, int et, bool reg, const Merged& m, const Shape& sx, const Shape& sw, ProductArgs x,
+                       ProductArgs w, void* parts, hipStream_t st) {
+    const int64_t nx = set_grid(x, sx, m.tile, m.split, m.kt_part, parts);
+    const int64_t nw = set_grid(w, sw, m.tile, 1, sw.kt, nullptr);
+    const dim3 grid((unsigned)(nx + nw));
+    if (nk) launch_merged<spg::kGradXNK>(et, reg, m.tile, x, w, (int)nx, grid, st);
+    else launch_merged<spg::kGradXKN>(et, reg, m.tile, x, w, (int)nx, grid, st);
+    const gemm_status e = launched();
+    return e != GEMM_OK || m.split == 1 ? e : run_sum(et, sx, x, st);
 }
 
 template <int ET, bool DUAL>
@@ -235,6 +307,7 @@ struct gemm_gated_plan {
     int64_t np;              // columns of dG and of dU in the workspace
     Stored x, w;
     Planned fwd, dx, dw;
+    Merged both[2];          // [register-staged]
     int64_t ws_fwd, ws_back, off_part;
 };
 
@@ -289,9 +362,14 @@ gemm_status gemm_gated_create(gemm_gated_handle* out, int64_t M, int64_t N, int6
         p->dw = plan_product(p->nk ? Shape{N, K, ceil_div(M, 64), 2, 1, 1, grad_bytes}
                                    : Shape{K, N, ceil_div(M, 64), 1, 2, 1, grad_bytes}, {p->x});
     }
+    int64_t merged = 0;
+    for (int r = 0; r < 2; ++r) {
+        p->both[r] = p->simple_back ? Merged{} : merge(p->dx, p->dw, r == 1);
+        if (p->both[r].on) merged = std::max(merged, part_bytes(p->dx.s, Tiling{0, p->both[r].split, 0, 0.0}));
+    }
     p->ws_fwd = p->fwd.bytes();
     p->off_part = up(M * p->np * 4, kAlign);
-    p->ws_back = p->off_part + std::max(p->dx.bytes(), p->dw.bytes());
+    p->ws_back = p->off_part + std::max(merged, std::max(p->dx.bytes(), p->dw.bytes()));
     *out = p;
     return GEMM_OK;
 }
@@ -371,81 +449,77 @@ gemm_status gemm_gated_backward(gemm_gated_handle h, const void* dH, const void*
         if (e != GEMM_OK) return e;
     }
     // dX = [dG dU] . [Wg; Wu]: one sum over both segments
-    if (M > 0) {
-        ProductArgs a{};
-        a.A[0] = (const char*)D;
-        a.B[0] = (const char*)Wg;
-        a.B[1] = (const char*)Wu;
-        a.C[0] = dX;
-        a.M = (int32_t)M;
-        a.N = (int32_t)K;
-        a.K = (int32_t)N;
-        a.lda = h->np * 4;
-        a.ldb = (h->nk ? K : N) * 2;
-        a.b_cols = (int32_t)K;
-        a.segments = 2;
-        gemm_status e;
-        if (h->simple_back) {
-            spg::SimpleArgs s{a, 2 * h->np, 1, h->nk ? 1 : N, h->nk ? K : 1, h->np};
-            e = bf ? run_simple<spg::kElBF16, false>(s, stream) : run_simple<spg::kElF16, false>(s, stream);
-        } else {
-            const bool wa = a.ldb % 16 == 0 && is16(Wg) && is16(Wu);
-            if (!wa && h->dx.pack) {
-                Operands o((char*)parts + h->dx.parts);
-                o.copy(h->w, a.B[0], a.ldb);
-                o.copy(h->w, a.B[1], a.ldb);
-                a.b_cols = (int32_t)up(K, 8);
-                if ((e = o.launch(2, stream)) != GEMM_OK) return e;
-            }
-            e = run_tiled(h->nk ? spg::kGradXNK : spg::kGradXKN, h->et, !wa && !h->dx.pack, h->dx, a, parts, stream);
-        }
-        if (e != GEMM_OK) return e;
-    }
+    ProductArgs x{};
+    x.A[0] = (const char*)D;
+    x.B[0] = (const char*)Wg;
+    x.B[1] = (const char*)Wu;
+    x.C[0] = dX;
+    x.M = (int32_t)M;
+    x.N = (int32_t)K;
+    x.K = (int32_t)N;
+    x.lda = h->np * 4;
+    x.ldb = (h->nk ? K : N) * 2;
+    x.b_cols = (int32_t)K;
+    x.segments = 2;
     // dWg, dWu: [N,K] weights dG^T X and dU^T X, [K,N] weights X^T dG and X^T dU
-    if (N > 0) {
-        const char* D0 = (const char*)D;
-        const char* D1 = (const char*)(D + h->np);
-        ProductArgs a{};
-        a.A[0] = h->nk ? D0 : (const char*)X;
-        a.A[1] = h->nk ? D1 : (const char*)X;
-        a.B[0] = h->nk ? (const char*)X : D0;
-        a.B[1] = h->nk ? (const char*)X : D1;
-        a.C[0] = dWg;
-        a.C[1] = dWu;
-        a.M = (int32_t)(h->nk ? N : K);
-        a.N = (int32_t)(h->nk ? K : N);
-        a.K = (int32_t)M;
-        a.lda = h->nk ? h->np * 4 : K * 2;
-        a.ldb = h->nk ? K * 2 : h->np * 4;
-        a.a_cols = (int32_t)(h->nk ? h->np : K);
-        a.b_cols = (int32_t)(h->nk ? K : h->np);
-        a.segments = 1;
-        if (h->simple_back) {
-            for (int z = 0; z < 2; ++z) {
-                ProductArgs b = a;
-                b.A[0] = a.A[z];
-                b.B[0] = a.B[z];
-                b.C[0] = a.C[z];
-                spg::SimpleArgs s{b, 1, a.lda / 2, 1, a.ldb / 2, 0};
-                const gemm_status e = bf ? run_simple<spg::kElBF16, false>(s, stream) : run_simple<spg::kElF16, false>(s, stream);
-                if (e != GEMM_OK) return e;
-            }
-            return GEMM_OK;
-        }
-        const bool xa = K % 8 == 0 && is16(X);
-        if (!xa && h->dw.pack) {
-            Operands o((char*)parts + h->dw.parts);
-            const char* x = (const char*)X;
-            int64_t& pitch = h->nk ? a.ldb : a.lda;
-            o.copy(h->x, x, pitch);
-            (h->nk ? a.B : a.A)[0] = (h->nk ? a.B : a.A)[1] = x;
-            (h->nk ? a.b_cols : a.a_cols) = (int32_t)up(K, 8);
-            const gemm_status e = o.launch(2, stream);
+    ProductArgs w{};
+    for (int z = 0; z < 2; ++z) {
+        const char* d = (const char*)(D + z * h->np);
+        w.A[z] = h->nk ? d : (const char*)X;
+        w.B[z] = h->nk ? (const char*)X : d;
+    }
+    w.C[0] = dWg;
+    w.C[1] = dWu;
+    w.M = (int32_t)(h->nk ? N : K);
+    w.N = (int32_t)(h->nk ? K : N);
+    w.K = (int32_t)M;
+    w.lda = h->nk ? h->np * 4 : K * 2;
+    w.ldb = h->nk ? K * 2 : h->np * 4;
+    w.a_cols = (int32_t)(h->nk ? h->np : K);
+    w.b_cols = (int32_t)(h->nk ? K : h->np);
+    w.segments = 1;
+    if (h->simple_back) {
+        if (M > 0) {
+            spg::SimpleArgs s{x, 2 * h->np, 1, h->nk ? 1 : N, h->nk ? K : 1, h->np};
+            const gemm_status e = bf ? run_simple<spg::kElBF16, false>(s, stream) : run_simple<spg::kElF16, false>(s, stream);
             if (e != GEMM_OK) return e;
         }
-        return run_tiled(spg::kGradW, h->et, !xa && !h->dw.pack, h->dw, a, parts, stream);
+        for (int z = 0; z < 2 && N > 0; ++z) {
+            ProductArgs one = w;
+            one.A[0] = w.A[z];
+            one.B[0] = w.B[z];
+            one.C[0] = w.C[z];
+            spg::SimpleArgs s{one, 1, w.lda / 2, 1, w.ldb / 2, 0};
+            const gemm_status e = bf ? run_simple<spg::kElBF16, false>(s, stream) : run_simple<spg::kElF16, false>(s, stream);
+            if (e != GEMM_OK) return e;
+        }
+        return GEMM_OK;
     }
-    return GEMM_OK;
+    const bool wa = x.ldb % 16 == 0 && is16(Wg) && is16(Wu);
+    const bool xa = K % 8 == 0 && is16(X);
+    const Merged& both = h->both[!(wa && xa)];
+    if (both.on)
+        return run_merged(h->nk, h->et, !(wa && xa), both, h->dx.s, h->dw.s, x, w, parts, stream);
+    if (!wa && h->dx.pack) {
+        Operands o((char*)parts + h->dx.parts);
+        o.copy(h->w, x.B[0], x.ldb);
+        o.copy(h->w, x.B[1], x.ldb);
+        x.b_cols = (int32_t)up(K, 8);
+        const gemm_status e = o.launch(2, stream);
+        if (e != GEMM_OK) return e;
+    }
+    const gemm_status e = run_tiled(h->nk ? spg::kGradXNK : spg::kGradXKN, h->et, !wa && !h->dx.pack, h->dx, x, parts, stream);
+    if (e != GEMM_OK) return e;
+    if (!xa && h->dw.pack) {
+        Operands o((char*)parts + h->dw.parts);
+        const char* p = (const char*)X;
+        o.copy(h->x, p, h->nk ? w.ldb : w.lda);
+        (h->nk ? w.B : w.A)[0] = (h->nk ? w.B : w.A)[1] = p;
+        (h->nk ? w.b_cols : w.a_cols) = (int32_t)up(K, 8);
+        const gemm_status e2 = o.launch(2, stream);
+        if (e2 != GEMM_OK) return e2;
+    }
+    return run_tiled(spg::kGradW, h->et, !xa && !h->dw.pack, h->dw, w, parts, stream);
 }
 
 gemm_status gemm_gated_destroy(gemm_gated_handle h) {

@@ -195,7 +195,7 @@ __device__ __forceinline__ void finish4(const AccOf<ET>& s0, const AccOf<ET>& s1
 // staging area (4 consecutive columns per lane and accumulator) and read back as 16-byte
 // row segments.  val(bn, bm, e) is the output of accumulator (bn, bm), element e.
 template <int OD, int TM, int TNO, int WNO, typename F>
-__device__ __forceinline__ void store_block(F&& val, char* stg, void* C, int M, int N, int m_base,
+__device__ __forceinline__ void store_block(F&& val, SPG_LDS char* stg, void* C, int M, int N, int m_base,
                                             int n_base, int lane) {
     constexpr int OB = OD == kOutF32 ? 4 : 2;
     constexpr int ROWB = WNO * OB;
@@ -221,7 +221,7 @@ __device__ __forceinline__ void store_block(F&& val, char* stg, void* C, int M, 
 #pragma unroll
                 for (int e = 0; e < 4; ++e) b[e] = out_bits<OD>(val(bn, bm, e));
                 const int byte = (bn * 16 + 4 * (lane >> 4)) * OB;
-                char* dst = stg + row * ROWB + (((byte >> 4) ^ swz(row)) << 4) + (byte & 15);
+                SPG_LDS char* dst = stg + row * ROWB + (((byte >> 4) ^ swz(row)) << 4) + (byte & 15);
                 if constexpr (OD == kOutF32) *(SPG_LDS u32x4*)dst = u32x4{b[0], b[1], b[2], b[3]};
                 else *(SPG_LDS u32x2*)dst = u32x2{b[0] | (b[1] << 16), b[2] | (b[3] << 16)};
             }
@@ -303,8 +303,7 @@ struct ProductGeom {
 // resource, so nothing of the next row is read: a 0 * inf could not be undone.
 template <int ET, bool A_T, bool B_N, bool DUAL, bool SEG, bool REG, int BM, int BN, int WM, int WN,
           int S, bool DEEP, int KG>
-__global__ void __launch_bounds__((ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP, KG>::NT))
-product_kernel(ProductArgs args) {
+__device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, SPG_LDS char* lds) {
     using G = ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP, KG>;
     constexpr int TM = G::TM, TN = G::TN, BNS = G::BNS, WNS = G::WNS, NW = G::NW;
     constexpr int A_OPS = G::A_OPS, B_OPS = G::B_OPS, L = G::L;
@@ -315,12 +314,11 @@ product_kernel(ProductArgs args) {
     static_assert(!SEG || (!A_T && !DUAL), "two segments: the input gradient");
     static_assert(!DUAL || !A_T, "gated: A is [M,K]");
 
-    __shared__ __attribute__((aligned(1024))) char lds[G::LDS];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave_id = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int kg = KG > 1 ? wave_id / NW : 0;         // group of k-tiles, wave within it
     const int wave = KG > 1 ? wave_id - kg * NW : wave_id;
-    SPG_LDS char* ring = (SPG_LDS char*)lds + kg * G::RING;
+    SPG_LDS char* ring = lds + kg * G::RING;
     struct Slot { SPG_LDS char* a; SPG_LDS char* b; };
     constexpr int NS = DEEP ? 6 : REG ? 4 : S;        // period of the slot (and register) pattern
     auto slot_of = [&](auto ic) -> Slot {
@@ -331,12 +329,12 @@ product_kernel(ProductArgs args) {
     const int wm = wave / G::WAVES_N, wn = wave % G::WAVES_N;
 
     if constexpr (kPoison) {
-        for (int o = tid * 16; o < G::LDS; o += G::NT * 16) *(u32x4*)(lds + o) = u32x4{~0u, ~0u, ~0u, ~0u};
+        for (int o = tid * 16; o < G::LDS; o += G::NT * 16) *(SPG_LDS u32x4*)(lds + o) = u32x4{~0u, ~0u, ~0u, ~0u};
         __syncthreads();
     }
 
     int tm, tn, sp;
-    product_tile(blockIdx.x, args, tm, tn, sp);
+    product_tile(wg, args, tm, tn, sp);
     int z = 0;
     if (tm >= args.tiles_m) { tm -= args.tiles_m; z = 1; }
     if (tn >= args.tiles_n) { tn -= args.tiles_n; z = 1; }
@@ -366,38 +364,33 @@ product_kernel(ProductArgs args) {
     // REG: the chunk that straddles K is loaded from the 16 bytes that end at K, which may
     // begin before the k-tile: the resource of K-contiguous rows starts 16 bytes early
     constexpr uint32_t kBack = REG ? 16u : 0u;
-    // K-contiguous rows: 128 bytes further per k-tile; reduction-major: 64 rows further
+    // Start and size of an operand's resource for a k-tile (0 past this part's last one: reads
+    // zero).  K-contiguous rows: 128 bytes further per k-tile, up to the end of the tile's
+    // last row.  Reduction-major: 64 rows further, as many of them as exist; columns past the
+    // last are masked by offset.  Written as selects: a branch here would cut the k-step that
+    // carries the copies in two.
+    const uint32_t lda = (uint32_t)args.lda, ldb = (uint32_t)args.ldb;
+    const uint64_t a_at = (uint64_t)(uintptr_t)a_ptr + (A_T ? 0 : (uint64_t)m0 * lda - kBack);
+    const uint64_t b_at[2] = {(uint64_t)(uintptr_t)b_mine + (B_N ? 0 : (uint64_t)n0 * ldb - kBack),
+                              (uint64_t)(uintptr_t)(SEG ? b_ptr1 : b_mine) + (B_N ? 0 : (uint64_t)n0 * ldb - kBack)};
+    const uint32_t a_all = (uint32_t)(a_rows - 1) * lda + (SEG ? lda : row_bytes) + kBack;
+    const uint32_t b_all = (uint32_t)(b_rows - 1) * ldb + row_bytes + kBack;
+    auto tr_win = [&](uint64_t p, uint32_t ld, int k, bool in) __attribute__((always_inline)) -> Win {
+        const int left = K - k * 64;
+        int rows = left < 64 ? left : 64;
+        rows = in ? rows : 0;
+        return Win{p + (uint64_t)(uint32_t)(k * 64) * ld, (uint32_t)rows * ld};
+    };
     auto a_win = [&](int kt) __attribute__((always_inline)) -> Win {
-        if constexpr (A_T) {
-            const uint64_t sh = (uint64_t)kt * 64u * (uint64_t)args.lda;
-            const uint64_t all = (uint64_t)(K - 1) * (uint64_t)args.lda + 2u * (uint64_t)args.a_cols;
-            const uint64_t left = all - sh, tile = 64u * (uint64_t)args.lda;
-            return Win{(uint64_t)(uintptr_t)a_ptr + sh, kt < kt1 ? (uint32_t)(left < tile ? left : tile) : 0u};
-        } else {
-            const uint32_t all = (uint32_t)(a_rows - 1) * (uint32_t)args.lda +
-                                 (SEG ? (uint32_t)args.lda : row_bytes);
-            const uint32_t sh = (uint32_t)kt * 128u;
-            return Win{(uint64_t)(uintptr_t)a_ptr + (uint64_t)m0 * (uint64_t)args.lda + sh - kBack,
-                       kt < kt1 ? all - sh + kBack : 0u};
-        }
+        if constexpr (A_T) return tr_win(a_at, lda, kt, kt < kt1);
+        else return Win{a_at + (uint32_t)kt * 128u, kt < kt1 ? a_all - (uint32_t)kt * 128u : 0u};
     };
     auto b_win = [&](int kt) __attribute__((always_inline)) -> Win {
-        const char* p = b_mine;
-        int k = kt;
-        if constexpr (SEG) {
-            if (kt >= seg_kt) { p = b_ptr1; k = kt - seg_kt; }
-        }
-        if constexpr (B_N) {
-            const uint64_t sh = (uint64_t)k * 64u * (uint64_t)args.ldb;
-            const uint64_t all = (uint64_t)(K - 1) * (uint64_t)args.ldb + 2u * (uint64_t)args.b_cols;
-            const uint64_t left = all - sh, tile = 64u * (uint64_t)args.ldb;
-            return Win{(uint64_t)(uintptr_t)p + sh, kt < kt1 ? (uint32_t)(left < tile ? left : tile) : 0u};
-        } else {
-            const uint32_t all = (uint32_t)(b_rows - 1) * (uint32_t)args.ldb + row_bytes;
-            const uint32_t sh = (uint32_t)k * 128u;
-            return Win{(uint64_t)(uintptr_t)p + (uint64_t)n0 * (uint64_t)args.ldb + sh - kBack,
-                       kt < kt1 ? all - sh + kBack : 0u};
-        }
+        const bool second = SEG && kt >= seg_kt;
+        const int k = second ? kt - seg_kt : kt;
+        const uint64_t p = second ? b_at[1] : b_at[0];
+        if constexpr (B_N) return tr_win(p, ldb, k, kt < kt1);
+        else return Win{p + (uint32_t)k * 128u, kt < kt1 ? b_all - (uint32_t)k * 128u : 0u};
     };
     // bytes of a K-contiguous row's part of k-tile kt that exist
     auto klim = [&](int kt) __attribute__((always_inline)) -> int {
@@ -742,7 +735,7 @@ product_kernel(ProductArgs args) {
     if constexpr (KG > 1) {
         wait_vmcnt<0>();
         __syncthreads();
-        SPG_LDS AccOf<ET>* sums = (SPG_LDS AccOf<ET>*)(SPG_LDS char*)lds;
+        SPG_LDS AccOf<ET>* sums = (SPG_LDS AccOf<ET>*)lds;
         if (kg > 0) {
 #pragma unroll
             for (int i = 0; i < TN * TM; ++i)
@@ -782,7 +775,7 @@ product_kernel(ProductArgs args) {
         wait_vmcnt<0>();
         __syncthreads();
     }
-    char* stg = lds + G::SUMS + wave * G::STG;
+    SPG_LDS char* stg = lds + G::SUMS + wave * G::STG;
     if constexpr (ET == kElI8) {
         float rs[TM];
 #pragma unroll
@@ -836,6 +829,26 @@ product_kernel(ProductArgs args) {
                                          stg, args.C[z], M, N, m_base, n_base, lane);
         }
     }
+}
+
+template <int ET, bool A_T, bool B_N, bool DUAL, bool SEG, bool REG, int BM, int BN, int WM, int WN,
+          int S, bool DEEP, int KG>
+__global__ void __launch_bounds__((ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP, KG>::NT))
+product_kernel(ProductArgs args) {
+    __shared__ __attribute__((aligned(1024))) char lds[ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP, KG>::LDS];
+    product_tile_of<ET, A_T, B_N, DUAL, SEG, REG, BM, BN, WM, WN, S, DEEP, KG>(args, blockIdx.x, (SPG_LDS char*)lds);
+}
+
+// The input gradient and the weights' gradients of a small training step in one launch:
+// workgroups 0 .. nx-1 the tiles of dX, the rest those of dWg and dWu.  Neither fills the
+// device, and each launch has its own start, last store and gap (about 4 us of 11).
+template <int ET, bool NK, bool REG, int BM, int BN, int WM, int WN, int S, int KG>
+__global__ void __launch_bounds__((ProductGeom<false, BM, BN, WM, WN, S, false, KG>::NT))
+gradients_kernel(ProductArgs x, ProductArgs w, int nx) {
+    __shared__ __attribute__((aligned(1024))) char lds[ProductGeom<false, BM, BN, WM, WN, S, false, KG>::LDS];
+    const int wg = blockIdx.x;
+    if (wg < nx) product_tile_of<ET, false, NK, false, true, REG, BM, BN, WM, WN, S, false, KG>(x, wg, (SPG_LDS char*)lds);
+    else product_tile_of<ET, true, true, false, false, REG, BM, BN, WM, WN, S, false, KG>(w, wg - nx, (SPG_LDS char*)lds);
 }
 
 // ---------------------------------------------------------------------------

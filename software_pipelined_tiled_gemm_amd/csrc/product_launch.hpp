@@ -29,6 +29,11 @@ constexpr int kTileN[kTiles] = {256, 128, 128, 128, 64};
 template <int ET, int P, bool REG>
 void launch_product(int tile, const ProductArgs& a, dim3 grid, hipStream_t st);
 
+// dX, then dWg and dWu, in one launch of nx + nw workgroups (tiles Mid and Small); P says
+// how the weights are stored (kGradXNK, kGradXKN)
+template <int ET, int P, bool REG>
+void launch_gradients(int tile, const ProductArgs& x, const ProductArgs& w, int nx, dim3 grid, hipStream_t st);
+
 #ifdef SPG_DEFINE_PRODUCT
 template <int ET, int P, bool REG, int BM, int BN, int WM, int WN, int S, bool DEEP, int KG>
 void launch_tile(const ProductArgs& a, dim3 grid, hipStream_t st) {
@@ -65,6 +70,23 @@ void launch_product(int tile, const ProductArgs& a, dim3 grid, hipStream_t st) {
         else if (tile == kTileMid) launch_tile<ET, P, REG, 128, 128, 32, 64, 2, false, 1>(a, grid, st);
         else if (tile == kTileSmall) launch_tile<ET, P, REG, 64, 128, 32, 64, 2, false, 1>(a, grid, st);
         else launch_tile<ET, P, REG, 64, 64, 32, 64, 2, false, 4>(a, grid, st);
+    }
+}
+
+template <int ET, int P, bool REG, int BM, int BN, int WM, int WN, int S, int KG>
+void launch_gradient_tile(const ProductArgs& x, const ProductArgs& w, int nx, dim3 grid, hipStream_t st) {
+    hipLaunchKernelGGL((gradients_kernel<ET, P == kGradXNK, REG, BM, BN, WM, WN, S, KG>), grid,
+                       dim3(ProductGeom<false, BM, BN, WM, WN, S, false, KG>::NT), 0, st, x, w, nx);
+}
+
+template <int ET, int P, bool REG>
+void launch_gradients(int tile, const ProductArgs& x, const ProductArgs& w, int nx, dim3 grid, hipStream_t st) {
+    if constexpr (!REG) {
+        if (tile == kTileMid) launch_gradient_tile<ET, P, REG, 128, 128, 32, 64, 4, 1>(x, w, nx, grid, st);
+        else launch_gradient_tile<ET, P, REG, 64, 128, 32, 64, 3, 2>(x, w, nx, grid, st);
+    } else {
+        if (tile == kTileMid) launch_gradient_tile<ET, P, REG, 128, 128, 32, 64, 2, 1>(x, w, nx, grid, st);
+        else launch_gradient_tile<ET, P, REG, 64, 128, 32, 64, 2, 1>(x, w, nx, grid, st);
     }
 }
 #endif
