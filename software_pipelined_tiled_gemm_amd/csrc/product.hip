@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <cmath>
 #include <initializer_list>
 #include <new>
 
@@ -44,9 +45,12 @@ struct Tiling {
 };
 
 // Measured per k-tile and per workgroup (us), see choose()
-constexpr double kTileUs[spg::kTiles] = {1.50, 0.89, 0.53, 0.36, 0.25};
+constexpr double kTileUs[spg::kTiles] = {1.45, 0.80, 0.48, 0.29, 0.25};
 constexpr double kStartUs[spg::kTiles] = {5.5, 3.5, 2.5, 2.8, 3.2};
-constexpr double kStaged = 1.35;      // register-staged against direct copies
+// ... and register-staged (no 256x256 tile); of the 64x128 tile two workgroups share a CU
+constexpr double kStagedUs[spg::kTiles] = {0.0, 1.30, 0.84, 0.65, 0.43};
+double tile_us(int t, bool reg) { return reg ? kStagedUs[t] : kTileUs[t]; }
+double slots(int t, bool reg) { return reg && t == spg::kTileSmall ? 512.0 : 256.0; }
 constexpr double kLaunchUs = 1.5;
 
 double sum_us(const Shape& s, int64_t split) {
@@ -59,10 +63,10 @@ int64_t tiles_of(const Shape& s, int t) {
 // Estimated microseconds of a tile class and a number of parts.  A tile class fills a CU's
 // LDS, so a CU runs one workgroup at a time: rounds of the 256 CUs times a part's k-tiles and
 // a start and store per round, plus a launch; never less than the operands take to read.
-// Parts add a kernel and their sums' traffic.  Measured per k-tile with all CUs busy (us,
-// bf16): 256x256 1.5, 256x128 0.89, 128x128 0.53, 64x128 0.36, 64x64 0.25, about a third
-// less with few (a CU copies about 105 bytes a nanosecond into its LDS, which is what bounds
-// the small tiles); one k-tile alone 7, 5, 4, 4.4 and 4.8.  Register-staged tiles 1.35 times.
+// Parts add a kernel and their sums' traffic.  Measured per k-tile with all CUs busy (us):
+// 256x256 1.45, 256x128 0.80, 128x128 0.48, 64x128 0.29, 64x64 0.25, about a third less with
+// few (a CU copies about 105 bytes a nanosecond into its LDS, which is what bounds the small
+// tiles); one k-tile alone 7, 5, 4, 4.4 and 4.8.
 Tiling choose(const Shape& s, bool reg) {
     Tiling best{spg::kTileSmall, 1, s.kt, 0.0};
     double best_t = -1.0;
@@ -72,9 +76,9 @@ Tiling choose(const Shape& s, bool reg) {
         for (int64_t split = 1; split <= 32 && split <= s.kt; ++split) {
             const int64_t part = ceil_div(s.kt, split);
             if (split > 1 && (part < 4 || ceil_div(s.kt, part) != split)) continue;
-            const double rounds = (double)ceil_div(tiles * split, 256);
-            const double busy = 0.68 + 0.32 * std::min(1.0, (double)(tiles * split) / 256.0);
-            double us = kLaunchUs + rounds * (kTileUs[t] * busy * (reg ? kStaged : 1.0) * (double)part + kStartUs[t]);
+            const double rounds = std::ceil((double)(tiles * split) / slots(t, reg));
+            const double busy = 0.68 + 0.32 * std::min(1.0, (double)(tiles * split) / slots(t, reg));
+            double us = kLaunchUs + rounds * (tile_us(t, reg) * busy * (double)part + kStartUs[t]);
             us = std::max(us, 3.0 + s.bytes / 5.0e6) + sum_us(s, split);
             if (best_t < 0 || us < best_t) {
                 best_t = us;
@@ -174,12 +178,12 @@ Merged merge(const Planned& x, const Planned& w, bool reg) {
         for (int64_t split = 1; split <= 16 && split <= x.s.kt; ++split) {
             const int64_t part = ceil_div(x.s.kt, split);
             if (split > 1 && (part < 4 || ceil_div(x.s.kt, part) != split)) continue;
-            const double k = kTileUs[t] * (reg ? kStaged : 1.0);
+            const double k = tile_us(t, reg);
             const double cx = k * (double)part + kStartUs[t], cw = k * (double)w.s.kt + kStartUs[t];
             const int64_t nx = tiles_of(x.s, t) * split, nw = tiles_of(w.s, t);
-            const double all = ((double)nx * cx + (double)nw * cw) / 256.0;
+            const double all = ((double)nx * cx + (double)nw * cw) / slots(t, reg);
             // past one round the last workgroups leave CUs idle: half of one's time
-            double us = std::max(std::max(cx, cw), nx + nw > 256 ? all + 0.5 * std::max(cx, cw) : 0.0);
+            double us = std::max(std::max(cx, cw), nx + nw > slots(t, reg) ? all + 0.5 * std::max(cx, cw) : 0.0);
             us = kLaunchUs + std::max(us, 3.0 + x.s.bytes / 5.0e6) + sum_us(x.s, split);
             if (us < best_us) {
                 best_us = us;

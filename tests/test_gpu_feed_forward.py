@@ -467,3 +467,50 @@ def test_repeated_passes_are_bitwise_equal():
             outs.append([h, *grads])
         for o in outs[1:]:
             assert all(torch.equal(p, q) for p, q in zip(outs[0], o))
+
+
+def test_wrappers_on_device_tensors(monkeypatch):
+    # both call paths (compiled and Python) make the same calls and the same refusals
+    torch = _t()
+    M, N, K = 20, 72, 64
+    x, wg, wu = (b.t for b in _gated_case(M, N, K, "bf16", "nk", 91))
+    a8, sa = torch.empty(M, K, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+    b8, sb = _ints(_gen(92), (N, K)), torch.full((N,), 1e-2, device="cuda")
+    results = []
+    for compiled in (True, False):
+        if compiled:
+            assert spg._calls_module() is not None, "the compiled call path is not built"
+        else:
+            monkeypatch.setattr(spg, "_calls", None)
+        h, c = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda"), torch.zeros(M, N, device="cuda")
+        side = torch.cuda.Stream()
+        with spg.Gated(M, N, K, "bf16", "nk", "silu") as plan, spg.QuantizedGemm(M, N, K, "f32") as q:
+            ws = _workspace(max(plan.workspace_bytes(), q.workspace_bytes()))
+            side.wait_stream(torch.cuda.current_stream())
+            plan(x, torch.nn.Parameter(wg), wu.detach().requires_grad_(True), h, workspace=ws, stream=side)
+            side.synchronize()
+            spg.gemm_quantize_rows(x.view(4, 5, K), a8.view(4, 5, K), sa.view(4, 5))
+            q(a8, sa, b8, sb, c, workspace=ws)
+            raw = torch.zeros_like(h)
+            plan(x.data_ptr(), wg.data_ptr(), wu.data_ptr(), raw.data_ptr(), workspace=ws.data_ptr(),
+                 stream=torch.cuda.current_stream().cuda_stream)
+            torch.cuda.synchronize()
+            results.append([h, c, raw, a8.clone(), sa.clone()])
+            wide = torch.zeros(M, 2 * N, dtype=torch.bfloat16, device="cuda")
+            for args in ((x.half(), wg, wu, h), (x, wg[:-1], wu, h), (x, wg, wu, wide[:, :N]), (x, wg, wu.cpu(), h),
+                         (x[None], wg, wu, h)):
+                with pytest.raises(spg.GemmError) as e:
+                    plan(*args, workspace=ws)
+                assert e.value.status == 1
+            with pytest.raises(spg.GemmError):
+                plan(x, wg, wu, None, workspace=ws)
+            with pytest.raises(spg.GemmError):
+                plan(x, wg, wu, h, G=torch.zeros_like(h), workspace=ws)
+            for args in ((a8, sa, b8, sb.double(), c), (a8, sa[:-1], b8, sb, c), (a8.float(), sa, b8, sb, c)):
+                with pytest.raises(spg.GemmError):
+                    q(*args, workspace=ws)
+            for args in ((x, a8[:-1], sa), (x, a8, sa.double()), (x.double(), a8, sa), (x, a8.t(), sa)):
+                with pytest.raises(spg.GemmError):
+                    spg.gemm_quantize_rows(*args)
+    assert torch.equal(results[0][0], results[0][2])
+    assert all(torch.equal(p, q) for p, q in zip(*results))
