@@ -45,12 +45,20 @@ struct Tiling {
 };
 
 // Measured per k-tile and per workgroup (us), see choose()
-constexpr double kTileUs[spg::kTiles] = {1.45, 0.80, 0.48, 0.29, 0.25};
-constexpr double kStartUs[spg::kTiles] = {5.5, 3.5, 2.5, 2.8, 3.2};
-// ... and register-staged (no 256x256 tile); of the 64x128 tile two workgroups share a CU
-constexpr double kStagedUs[spg::kTiles] = {0.0, 1.30, 0.84, 0.65, 0.43};
-double tile_us(int t, bool reg) { return reg ? kStagedUs[t] : kTileUs[t]; }
-double slots(int t, bool reg) { return reg && t == spg::kTileSmall ? 512.0 : 256.0; }
+constexpr double kTileUs[spg::kTiles] = {1.45, 0.80, 0.48, 0.29, 0.25, 0.88};
+constexpr double kStartUs[spg::kTiles] = {5.5, 3.5, 2.5, 2.8, 3.2, 3.2};
+// ... and register-staged (no 256x256 and no pair tile)
+constexpr double kStagedUs[spg::kTiles] = {0.0, 1.30, 0.95, 0.62, 0.43, 0.0};
+constexpr double kStagedStartUs[spg::kTiles] = {0.0, 4.5, 3.0, 2.8, 3.2, 0.0};
+double start_us(int t, bool reg) { return reg ? kStagedStartUs[t] : kStartUs[t]; }
+// of `wgs` workgroups: with two on a CU the staged 64x128 tile takes 0.94 each
+double tile_us(int t, bool reg, int64_t wgs) {
+    if (reg && t == spg::kTileSmall && wgs > 256) return 0.94;
+    return reg ? kStagedUs[t] : kTileUs[t];
+}
+// two workgroups on a CU: the pair tile, and the register-staged 64x128 one
+bool paired(int t, bool reg) { return t == (reg ? (int)spg::kTileSmall : (int)spg::kTilePair); }
+double slots(int t, bool reg) { return paired(t, reg) ? 512.0 : 256.0; }
 constexpr double kLaunchUs = 1.5;
 
 double sum_us(const Shape& s, int64_t split) {
@@ -66,19 +74,22 @@ int64_t tiles_of(const Shape& s, int t) {
 // Parts add a kernel and their sums' traffic.  Measured per k-tile with all CUs busy (us):
 // 256x256 1.45, 256x128 0.80, 128x128 0.48, 64x128 0.29, 64x64 0.25, about a third less with
 // few (a CU copies about 105 bytes a nanosecond into its LDS, which is what bounds the small
-// tiles); one k-tile alone 7, 5, 4, 4.4 and 4.8.
+// tiles); one k-tile alone 7, 5, 4, 4.4 and 4.8.  Two 128x128 workgroups on a CU take 0.88 a
+// k-tile each, but a round of 512 of them only 3.4 beside: 4096 x 8192 outputs of 64, 256
+// and 1024 reductions take 36, 55 and 140 us against 54, 73 and 164 one at a time, and 32,
+// 49 and 121 with the 256x256 tile, which needs a large grid.
 Tiling choose(const Shape& s, bool reg) {
     Tiling best{spg::kTileSmall, 1, s.kt, 0.0};
     double best_t = -1.0;
     for (int t = 0; t < spg::kTiles; ++t) {
-        if (reg && t == spg::kTileBig) continue;   // register staging: no 256x256 tile
+        if (reg && (t == spg::kTileBig || t == spg::kTilePair)) continue;   // not staged through registers
         const int64_t tiles = tiles_of(s, t);
         for (int64_t split = 1; split <= 32 && split <= s.kt; ++split) {
             const int64_t part = ceil_div(s.kt, split);
             if (split > 1 && (part < 4 || ceil_div(s.kt, part) != split)) continue;
             const double rounds = std::ceil((double)(tiles * split) / slots(t, reg));
-            const double busy = 0.68 + 0.32 * std::min(1.0, (double)(tiles * split) / slots(t, reg));
-            double us = kLaunchUs + rounds * (tile_us(t, reg) * busy * (double)part + kStartUs[t]);
+            const double busy = paired(t, reg) ? 1.0 : 0.68 + 0.32 * std::min(1.0, (double)(tiles * split) / 256.0);
+            double us = kLaunchUs + rounds * (tile_us(t, reg, tiles * split) * busy * (double)part + start_us(t, reg));
             us = std::max(us, 3.0 + s.bytes / 5.0e6) + sum_us(s, split);
             if (best_t < 0 || us < best_t) {
                 best_t = us;
@@ -178,9 +189,9 @@ Merged merge(const Planned& x, const Planned& w, bool reg) {
         for (int64_t split = 1; split <= 16 && split <= x.s.kt; ++split) {
             const int64_t part = ceil_div(x.s.kt, split);
             if (split > 1 && (part < 4 || ceil_div(x.s.kt, part) != split)) continue;
-            const double k = tile_us(t, reg);
-            const double cx = k * (double)part + kStartUs[t], cw = k * (double)w.s.kt + kStartUs[t];
             const int64_t nx = tiles_of(x.s, t) * split, nw = tiles_of(w.s, t);
+            const double k = tile_us(t, reg, nx + nw);
+            const double cx = k * (double)part + start_us(t, reg), cw = k * (double)w.s.kt + start_us(t, reg);
             const double all = ((double)nx * cx + (double)nw * cw) / slots(t, reg);
             // past one round the last workgroups leave CUs idle: half of one's time
             double us = std::max(std::max(cx, cw), nx + nw > slots(t, reg) ? all + 0.5 * std::max(cx, cw) : 0.0);
@@ -286,7 +297,10 @@ gemm_status run_merged(bool nk, int et, bool reg, const Merged& m, const Shape& 
 
 template <int ET, bool DUAL>
 void stream_rows(const ProductArgs& a, hipStream_t st) {
-    hipLaunchKernelGGL((spg::stream_kernel<ET, DUAL, 8, 4>), dim3((unsigned)ceil_div(a.N, 16)), dim3(512), 0, st, a);
+    const dim3 grid((unsigned)ceil_div(a.N, 16)), wg(512);
+    const uintptr_t all = (uintptr_t)a.A[0] | (uintptr_t)a.B[0] | (DUAL ? (uintptr_t)a.B[1] : 0) | (uintptr_t)a.lda | (uintptr_t)a.ldb;
+    if (all % 4 == 0) hipLaunchKernelGGL((spg::stream_kernel<ET, DUAL, true, 8, 4>), grid, wg, 0, st, a);
+    else hipLaunchKernelGGL((spg::stream_kernel<ET, DUAL, false, 8, 4>), grid, wg, 0, st, a);
 }
 
 template <int ET, bool DUAL>

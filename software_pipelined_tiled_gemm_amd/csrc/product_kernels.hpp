@@ -128,6 +128,17 @@ __device__ __forceinline__ AccOf<ET> mma(const u32x4& x, const u32x4& y, const A
         return mfma16<ET == kElBF16>(x, y, c);
 }
 
+// The top `bits` (a multiple of 8, 0 .. 120) of 128 cleared.
+__device__ __forceinline__ u32x4 clear_top(u32x4 v, uint32_t bits) {
+    u32x4 r;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int keep = 128 - (int)bits - 32 * e;        // bits of this word that stay
+        r[e] = keep >= 32 ? v[e] : keep <= 0 ? 0u : v[e] & ((1u << keep) - 1u);
+    }
+    return r;
+}
+
 // A store of 16 bytes to an address that is only element-aligned: compute queues run in
 // unaligned-access mode, so it is one instruction.
 struct __attribute__((packed, aligned(2))) Bytes16 { u32x4 v; };
@@ -832,8 +843,8 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, 
 }
 
 template <int ET, bool A_T, bool B_N, bool DUAL, bool SEG, bool REG, int BM, int BN, int WM, int WN,
-          int S, bool DEEP, int KG>
-__global__ void __launch_bounds__((ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP, KG>::NT))
+          int S, bool DEEP, int KG, int WPS>
+__global__ void __launch_bounds__((ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP, KG>::NT), WPS)
 product_kernel(ProductArgs args) {
     __shared__ __attribute__((aligned(1024))) char lds[ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP, KG>::LDS];
     product_tile_of<ET, A_T, B_N, DUAL, SEG, REG, BM, BN, WM, WN, S, DEEP, KG>(args, blockIdx.x, (SPG_LDS char*)lds);
@@ -866,7 +877,13 @@ gradients_kernel(ProductArgs x, ProductArgs w, int nx) {
 // with a tile).  Measured at M = 1, N = 12288, K = 4096 bf16, two weights: 38.3 us, 5.25
 // TB/s; a second chunk in flight a wave 41.0, 16 waves 37.6 to 42.6, 4 waves 40.3,
 // loads marked nontemporal 39.6 (int8, M = 4: 10.7 against 14.6).
-template <int ET, bool DUAL, int NW, int U>
+//
+// WORDS: all rows start on 4 bytes.  Otherwise (odd K in 16 bits, most K in 8) a lane loads
+// the 16 bytes from the 4-byte word its chunk starts in, takes the word after them from the
+// lane that holds the row's next 16 bytes, and shifts by its row's 1 to 3 bytes: loads that
+// are not word-aligned run at half the rate (K = 4095 against 4094: 54.6 and 31.5 us, int8
+// 20.4 and 8.3).  Only whole words that hold a byte of the operand are read.
+template <int ET, bool DUAL, bool WORDS, int NW, int U>
 __global__ void __launch_bounds__(NW * 64) stream_kernel(ProductArgs args) {
     constexpr int ES = ET == kElI8 ? 1 : 2;
     constexpr int NM = DUAL ? 2 : 1;
@@ -878,10 +895,21 @@ __global__ void __launch_bounds__(NW * 64) stream_kernel(ProductArgs args) {
     const int n0 = blockIdx.x * 16;
     const int rows = N - n0 < 16 ? N - n0 : 16;
     const uint32_t ldb = (uint32_t)args.ldb, lda = (uint32_t)args.lda;
-    const uint32_t bbytes = (uint32_t)(rows - 1) * ldb + (uint32_t)kb;
-    const auto rx = make_rsrc_b(args.A[0], (uint32_t)(M - 1) * lda + (uint32_t)kb);
-    const auto rb0 = make_rsrc_b(args.B[0] + (size_t)n0 * ldb, bbytes);
-    const auto rb1 = make_rsrc_b((DUAL ? args.B[1] : args.B[0]) + (size_t)n0 * ldb, bbytes);
+    // a matrix: its resource from the word its first row starts in, this lane's row from
+    // there, and how many bytes past a word the row starts
+    struct Rows {
+        __amdgpu_buffer_rsrc_t r;
+        uint32_t row, shift;
+    };
+    auto rows_of = [&](const char* p, uint32_t ld, int n) __attribute__((always_inline)) -> Rows {
+        const uint32_t skip = WORDS ? 0u : (uint32_t)(uintptr_t)p & 3u;
+        const uint32_t bytes = skip + (uint32_t)(n - 1) * ld + (uint32_t)kb;
+        const uint32_t at = skip + (uint32_t)(lane & 15) * ld;
+        return Rows{make_rsrc_b(p - skip, WORDS ? bytes : (bytes + 3u) & ~3u), WORDS ? at : at & ~3u, WORDS ? 0u : at & 3u};
+    };
+    const Rows x = rows_of(args.A[0], lda, M);
+    const Rows b0 = rows_of(args.B[0] + (size_t)n0 * ldb, ldb, rows);
+    const Rows b1 = rows_of((DUAL ? args.B[1] : args.B[0]) + (size_t)n0 * ldb, ldb, rows);
     const bool ragged = (kb & 15) != 0;
 
     AccOf<ET> acc[NM];
@@ -890,34 +918,66 @@ __global__ void __launch_bounds__(NW * 64) stream_kernel(ProductArgs args) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[q][e] = 0;
 
-    const uint32_t wrow = (uint32_t)(lane & 15) * ldb, xrow = (uint32_t)(lane & 15) * lda;
+    const int next = ((lane + 16) & 63) * 4;          // the lane with the row's next 16 bytes
+    struct Chunks { u32x4 v[U]; uint32_t end; };
     for (int base = wave * (U * 64); base < kb; base += NW * U * 64) {
-        u32x4 w[NM][U], x[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = base + u * 64 + 16 * (lane >> 4);
-            // the bytes past K read zero; the 16 that straddle it are the 16 ending at K
-            const uint32_t kw = (uint32_t)(k + 16 <= kb ? k : kb - 16);
-            const bool in = k < kb;
-            const uint32_t o = in ? wrow + kw : kOOB;
-            w[0][u] = __builtin_amdgcn_raw_buffer_load_b128(rb0, (int)o, 0, 0);
-            if constexpr (DUAL) w[NM - 1][u] = __builtin_amdgcn_raw_buffer_load_b128(rb1, (int)o, 0, 0);
-            x[u] = __builtin_amdgcn_raw_buffer_load_b128(rx, (int)(in ? xrow + kw : kOOB), 0, 0);
-        }
-        if (ragged && base + U * 64 > kb) {
+        auto load = [&](const Rows& m) __attribute__((always_inline)) -> Chunks {
+            Chunks c;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int k = base + u * 64 + 16 * (lane >> 4);
-                const uint32_t sh = k < kb && k + 16 > kb ? 8u * (uint32_t)(k + 16 - kb) : 0u;
-#pragma unroll
-                for (int q = 0; q < NM; ++q) w[q][u] = shr128(w[q][u], sh);
-                x[u] = shr128(x[u], sh);
+                // WORDS: bytes past K read zero, the 16 that straddle it are the 16 ending at K.
+                // Otherwise the words up to the one that holds the row's last byte are read:
+                // the chunk before may need the first of these
+                const uint32_t kw = (uint32_t)(WORDS && k + 16 > kb ? kb - 16 : k);
+                const bool in = k < kb + (int)m.shift;
+                c.v[u] = __builtin_amdgcn_raw_buffer_load_b128(m.r, (int)(in ? m.row + kw : kOOB), 0, 0);
             }
+            // the word after the last chunk, for the lanes with the row's last 16 bytes of it
+            if constexpr (!WORDS)
+                c.end = __builtin_amdgcn_raw_buffer_load_b32(m.r, (int)(m.row + (uint32_t)(base + U * 64)), 0, 0);
+            return c;
+        };
+        auto align = [&](const Rows& m, Chunks& c) __attribute__((always_inline)) {
+            if constexpr (!WORDS) {
+                const bool last = lane >= 48;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    // lanes 48 .. 63 need the first word of lanes 0 .. 15 one chunk further
+                    const uint32_t here = (uint32_t)__builtin_amdgcn_ds_bpermute(next, (int)c.v[u].x);
+                    const uint32_t further = u + 1 < U ? (uint32_t)__builtin_amdgcn_ds_bpermute(next, (int)c.v[u + 1 < U ? u + 1 : u].x) : c.end;
+                    const uint32_t w[5] = {c.v[u].x, c.v[u].y, c.v[u].z, c.v[u].w, last ? further : here};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) c.v[u][e] = __builtin_amdgcn_alignbyte(w[e + 1], w[e], m.shift);
+                }
+            }
+            if ((ragged || !WORDS) && base + U * 64 > kb) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int k = base + u * 64 + 16 * (lane >> 4);
+                    if constexpr (WORDS) {
+                        const uint32_t sh = k < kb && k + 16 > kb ? 8u * (uint32_t)(k + 16 - kb) : 0u;
+                        c.v[u] = shr128(c.v[u], sh);
+                    } else {
+                        // what follows the row's end is the next row's
+                        const int gone = k + 16 - kb;
+                        const uint32_t sh = gone > 0 && gone < 16 ? 8u * (uint32_t)gone : 0u;
+                        const u32x4 kept = clear_top(c.v[u], sh);
+                        c.v[u] = gone >= 16 ? u32x4{} : kept;
+                    }
+                }
+            }
+        };
+        Chunks cx = load(x), c0 = load(b0), c1;
+        if constexpr (DUAL) c1 = load(b1);
+        align(x, cx);
+        align(b0, c0);
+        if constexpr (DUAL) align(b1, c1);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            acc[0] = mma<ET>(c0.v[u], cx.v[u], acc[0]);
+            if constexpr (DUAL) acc[NM - 1] = mma<ET>(c1.v[u], cx.v[u], acc[NM - 1]);
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int q = 0; q < NM; ++q) acc[q] = mma<ET>(w[q][u], x[u], acc[q]);
     }
 #pragma unroll
     for (int q = 0; q < NM; ++q) sums[wave][q][lane] = acc[q];
@@ -995,9 +1055,21 @@ __global__ void __launch_bounds__(256) sum_parts(ProductArgs args) {
     const size_t step = (size_t)rows * args.ldp / 4;
     AccOf<ET> s0 = p[0], s1 = s0;
     if constexpr (DUAL) s1 = p[np4 / 4];
-    for (int k = 1; k < args.split; ++k) {
-        s0 += p[k * step];
-        if constexpr (DUAL) s1 += p[k * step + np4 / 4];
+    // eight parts' loads in flight at a time, added in order
+    for (int k = 1; k < args.split; k += 8) {
+        AccOf<ET> v[8], w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int q = k + j < args.split ? k + j : k;
+            v[j] = p[q * step];
+            if constexpr (DUAL) w[j] = p[q * step + np4 / 4];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (k + j < args.split) {
+                s0 += v[j];
+                if constexpr (DUAL) s1 += w[j];
+            }
     }
     int z = 0;
     if (m >= args.M) { m -= args.M; z = 1; }

@@ -22,9 +22,11 @@ enum {
 };
 
 // Tile classes: rows x columns of a workgroup's tile (DUAL: columns of both matrices)
-enum { kTileBig = 0, kTileTall = 1, kTileMid = 2, kTileSmall = 3, kTileNarrow = 4, kTiles = 5 };
-constexpr int kTileM[kTiles] = {256, 256, 128, 64, 64};
-constexpr int kTileN[kTiles] = {256, 128, 128, 128, 64};
+// Pair: two workgroups share a CU (64 KiB of LDS and at most 128 registers each), so that
+// one's start and store overlap the other's k-tiles: for short reductions
+enum { kTileBig = 0, kTileTall = 1, kTileMid = 2, kTileSmall = 3, kTileNarrow = 4, kTilePair = 5, kTiles = 6 };
+constexpr int kTileM[kTiles] = {256, 256, 128, 64, 64, 128};
+constexpr int kTileN[kTiles] = {256, 128, 128, 128, 64, 128};
 
 template <int ET, int P, bool REG>
 void launch_product(int tile, const ProductArgs& a, dim3 grid, hipStream_t st);
@@ -35,12 +37,12 @@ template <int ET, int P, bool REG>
 void launch_gradients(int tile, const ProductArgs& x, const ProductArgs& w, int nx, dim3 grid, hipStream_t st);
 
 #ifdef SPG_DEFINE_PRODUCT
-template <int ET, int P, bool REG, int BM, int BN, int WM, int WN, int S, bool DEEP, int KG>
+template <int ET, int P, bool REG, int BM, int BN, int WM, int WN, int S, bool DEEP, int KG, int WPS = 1>
 void launch_tile(const ProductArgs& a, dim3 grid, hipStream_t st) {
     constexpr bool AT = P == kGradW, BNC = P == kGatedKN || P == kGradXNK || P == kGradW;
     constexpr bool DUAL = P == kGatedNK || P == kGatedKN || P == kInt8Gated;
     constexpr bool SEG = P == kGradXNK || P == kGradXKN;
-    hipLaunchKernelGGL((product_kernel<ET, AT, BNC, DUAL, SEG, REG, BM, BN, WM, WN, S, DEEP, KG>), grid,
+    hipLaunchKernelGGL((product_kernel<ET, AT, BNC, DUAL, SEG, REG, BM, BN, WM, WN, S, DEEP, KG, WPS>), grid,
                        dim3(ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP, KG>::NT), 0, st, a);
 }
 
@@ -60,6 +62,8 @@ void launch_product(int tile, const ProductArgs& a, dim3 grid, hipStream_t st) {
             launch_tile<ET, P, REG, 256, 128, 64, 64, 3, false, 1>(a, grid, st);
         } else if (tile == kTileMid) {
             launch_tile<ET, P, REG, 128, 128, 32, 64, 4, false, 1>(a, grid, st);
+        } else if (tile == kTilePair) {
+            launch_tile<ET, P, REG, 128, 128, 32, 64, 2, false, 1, 4>(a, grid, st);
         } else if (tile == kTileSmall) {
             launch_tile<ET, P, REG, 64, 128, 32, 64, 3, false, 2>(a, grid, st);
         } else {
