@@ -234,7 +234,7 @@ const char* gemm_last_hip_error(void);
 /* ---------------------------------------------------------------------------------
  * Feed-forward operators: the gated projection with its backward pass, and products of
  * 8-bit integers.  The conventions above hold: dense row-major matrices, device pointers
- * owned by the caller, any element alignment (16-byte aligned rows and pointers are
+ * owned by the caller, any element alignment (rows and pointers on 4 bytes are
  * faster), status codes, checks before any HIP call, asynchronous on `stream`, no
  * allocation and no synchronization, so every call may be captured into a HIP graph.
  * Outputs must not overlap inputs (not checked).

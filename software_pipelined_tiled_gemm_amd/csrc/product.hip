@@ -23,7 +23,8 @@ constexpr int64_t kAlign = 256;   // sections of a workspace
 int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-bool is16(const void* p) { return (uintptr_t)p % 16 == 0; }
+// direct copies read from 4-byte aligned addresses
+bool words(const void* p) { return (uintptr_t)p % 4 == 0; }
 
 gemm_status launched() {
     const hipError_t e = hipGetLastError();
@@ -105,7 +106,7 @@ struct Stored {
     int64_t rows, row_bytes;
     int64_t pitch() const { return up(row_bytes, 128); }
     int64_t bytes() const { return rows * pitch(); }
-    bool aligned() const { return row_bytes % 16 == 0; }
+    bool aligned() const { return row_bytes % 4 == 0; }
 };
 
 // A product of a plan: its tilings with direct copies and register-staged, and whether
@@ -423,7 +424,7 @@ gemm_status gemm_gated_run(gemm_gated_handle h, const void* X, const void* Wg, c
         else stream_rows<spg::kElF16, true>(a, stream);
         return launched();
     }
-    const bool xa = a.lda % 16 == 0 && is16(X), wa = a.ldb % 16 == 0 && is16(Wg) && is16(Wu);
+    const bool xa = a.lda % 4 == 0 && words(X), wa = a.ldb % 4 == 0 && words(Wg) && words(Wu);
     const bool pack = h->fwd.pack && !(xa && wa);
     const bool reg = !pack && !(xa && wa);
     const int64_t need = (pack ? h->fwd.packed : 0) + part_bytes(h->fwd.s, h->fwd.t[reg]);
@@ -513,8 +514,8 @@ gemm_status gemm_gated_backward(gemm_gated_handle h, const void* dH, const void*
         }
         return GEMM_OK;
     }
-    const bool wa = x.ldb % 16 == 0 && is16(Wg) && is16(Wu);
-    const bool xa = K % 8 == 0 && is16(X);
+    const bool wa = x.ldb % 4 == 0 && words(Wg) && words(Wu);
+    const bool xa = K % 2 == 0 && words(X);
     const Merged& both = h->both[!(wa && xa)];
     if (both.on)
         return run_merged(h->nk, h->et, !(wa && xa), both, h->dx.s, h->dw.s, x, w, parts, stream);
@@ -613,7 +614,7 @@ gemm_status gemm_quantized_run(gemm_quantized_handle h, const int8_t* A, const f
         else stream_rows<spg::kElI8, false>(a, stream);
         return launched();
     }
-    const bool aa = h->K % 16 == 0 && is16(A), ba = h->K % 16 == 0 && is16(B) && (!dual || is16(B2));
+    const bool aa = h->K % 4 == 0 && words(A), ba = h->K % 4 == 0 && words(B) && (!dual || words(B2));
     const bool pack = h->p.pack && !(aa && ba);
     const bool reg = !pack && !(aa && ba);
     const int64_t need = (pack ? h->p.packed : 0) + part_bytes(h->p.s, h->p.t[reg]);

@@ -300,9 +300,12 @@ struct ProductGeom {
 //         gate's and the up projection's sums of the same outputs, so their product needs
 //         no exchange
 //   SEG   the sum may run over two segments with a B matrix each
-//   REG   operands whose rows or base are not 16-byte aligned: k-tiles go through VGPRs
+//   REG   operands whose rows or base do not start on 4 bytes: k-tiles go through VGPRs
 //         (two slots), loaded at any alignment; else they are copied straight into LDS
 //   DEEP  a ring of two A and three B slots under the ping-pong schedule (the K loop)
+//   TAIL  the sum may end inside a 16-byte chunk of a K-contiguous row (direct copies);
+//         without it the large tiles save the registers and the code: int8 8192 x 4096 x
+//         12288 takes 296 us without and 302 to 318 with it
 //   KG    the waves form KG groups that take the k-tiles in turn: more waves to hide the
 //         latencies of LDS reads, copies and barrier around the few MFMAs of a small tile
 //         (64 x 128, 256 workgroups, 128 k-tiles: 44.2 us with one group of four waves and
@@ -311,9 +314,10 @@ struct ProductGeom {
 // next k-tile and releases the slot, which is refilled (k-tile t+S) behind it.
 // Reads past an operand: rows past the end fall outside the buffer resource and read zero.
 // A K-contiguous row's last k-tile masks the chunks past K by an offset outside every
-// resource, so nothing of the next row is read: a 0 * inf could not be undone.
+// resource and clears the part of one that straddles K, so nothing of the next row is
+// multiplied: a 0 * inf could not be undone.
 template <int ET, bool A_T, bool B_N, bool DUAL, bool SEG, bool REG, int BM, int BN, int WM, int WN,
-          int S, bool DEEP, int KG>
+          int S, bool DEEP, int KG, bool TAIL>
 __device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, SPG_LDS char* lds) {
     using G = ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP, KG>;
     constexpr int TM = G::TM, TN = G::TN, BNS = G::BNS, WNS = G::WNS, NW = G::NW;
@@ -358,9 +362,9 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, 
     const int nk = (kt1 - kt0 + KG - 1) / KG;         // k-tiles of this part a group takes (>= 1)
     auto kt_of = [&](int t) { return kt0 + t * KG + kg; };
     const int tail = K * ES - (seg_kt - 1) * 128;     // bytes of a segment's last k-tile
-    // bytes of a K-contiguous row that may be read: direct copies move whole 16-byte chunks,
-    // of rows that are a multiple of that or have been laid out again, padded with zeros
-    const uint32_t row_bytes = REG ? (uint32_t)(K * ES) : ((uint32_t)(K * ES) + 15u) & ~15u;
+    // bytes of a K-contiguous row that may be read: whole words for direct copies (rows of
+    // whole words, or laid out again and padded with zeros)
+    const uint32_t row_bytes = REG ? (uint32_t)(K * ES) : ((uint32_t)(K * ES) + 3u) & ~3u;
 
     // ---- copy sources ----
     const char* a_ptr = args.A[!DUAL && args.zm == 2 ? z : 0];
@@ -437,8 +441,11 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, 
         const int r = d * RP + lane / CPR, c = (lane % CPR) ^ nswz_t<CPR>(r);
         over = col0 + c * 8 + 8 - cols;
         off = (uint32_t)r * (uint32_t)ld + (uint32_t)(col0 + c * 8) * 2u;
-        if (over >= (REG ? 8 : 1)) off = kOOB;
-        else if (REG && over > 0) off -= 2u * (uint32_t)over;   // the 16 bytes ending at the last column
+        // columns past the last of a chunk: REG loads the 16 bytes that end at the last column
+        // (and shifts them); a direct copy takes what follows, the next row's first columns
+        // or zeros past the end, which only reach results that are not stored
+        if (over >= 8) off = kOOB;
+        else if (REG && over > 0) off -= 2u * (uint32_t)over;
     };
     if constexpr (A_T) {
 #pragma unroll
@@ -498,6 +505,28 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, 
     auto dma_op = [&](const Slot& s, const Src& src, auto jc) __attribute__((always_inline)) {
         constexpr bool ISA = decltype(jc)::value < A_OPS;
         dma16(ISA ? src.a : src.b, lds_dst(s, jc), src_off(jc, ISA ? src.lim_a : src.lim_b));
+    };
+    // A K-contiguous row's last chunk of a segment that ends inside it: what follows K there
+    // is the next row's and is cleared in LDS, by the lane that copied it, once this wave's
+    // copies of the k-tile have landed and before the barrier that publishes it.
+    auto clear_tail = [&](const Slot& s, int kt) __attribute__((always_inline)) {
+        if constexpr (TAIL && !REG && (!A_T || !B_N)) {
+            const int lim = klim(kt);
+            if ((lim & 15) == 0) return;
+            // loops, not unrolled: the code stands behind every k-tile of the unrolled pattern
+            auto clear = [&](SPG_LDS char* at, int ops, int pos) __attribute__((always_inline)) {
+#pragma unroll 1
+                for (int j = 0; j < ops; ++j) {
+                    if ((pos ^ ((j & 1) * 64)) == (lim & ~15)) {
+                        SPG_LDS u32x4* p = (SPG_LDS u32x4*)(at + j * 1024 + lane * 16);
+                        *p = clear_top(*p, 8u * (uint32_t)(16 - (lim & 15)));
+                    }
+                }
+            };
+            if constexpr (!A_T) clear(s.a + firstA * 1024, A_OPS, posA);
+            if constexpr (!B_N) clear(s.b + wave * B_OPS * 1024, B_OPS, posB);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        }
     };
     auto issue = [&](const Slot& s, int kt) __attribute__((always_inline)) {
         const Src src = src_ab(kt, kt);
@@ -648,9 +677,11 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, 
         const Src src = src_ab(kt0 + 2, kt0 + 2);
         static_for<A_OPS, L>([&](auto jc) { dma_op(slot_of(C2{}), src, jc); });
         wait_vmcnt<L + B_OPS>();
+        clear_tail(slot_of(C0{}), kt0);
     } else {
         static_for<0, S>([&](auto sc) { issue(slot_of(sc), kt_of(decltype(sc)::value)); });
         wait_vmcnt<(S - 1) * L>();
+        clear_tail(slot_of(C0{}), kt_of(0));
     }
     lds_barrier();
     auto over_ktiles = [&](auto&& ktile) __attribute__((always_inline)) {
@@ -702,10 +733,17 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, 
             phase_barrier();
             static_for<0, NRD>([&](auto rc) { read_op(cur, 1, f, rc); });
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            if (grp == 1) wait_vmcnt<B_OPS>();
+            const Slot nxt = slot_of(std::integral_constant<int, i + 1>{});
+            if (grp == 1) {
+                wait_vmcnt<B_OPS>();
+                clear_tail(nxt, kt0 + u + 1);
+            }
             phase_barrier();
             matrix_phase();
-            if (grp == 0) wait_vmcnt<B_OPS>();
+            if (grp == 0) {
+                wait_vmcnt<B_OPS>();
+                clear_tail(nxt, kt0 + u + 1);
+            }
             phase_barrier();
         });
         if (grp == 0) phase_barrier();
@@ -726,7 +764,10 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, 
                 gload(Next{}, kt_of(t + 1 + PD));
             }
             stage(fr[0], cur, 1, fr[1], cur, none, std::false_type{});
-            if constexpr (!REG) wait_vmcnt<(S - 2) * L>();
+            if constexpr (!REG) {
+                wait_vmcnt<(S - 2) * L>();
+                clear_tail(nxt, kt_of(t + 1));
+            }
             __builtin_amdgcn_sched_barrier(0);
             lds_barrier();
             __builtin_amdgcn_sched_barrier(0);
@@ -843,11 +884,11 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, 
 }
 
 template <int ET, bool A_T, bool B_N, bool DUAL, bool SEG, bool REG, int BM, int BN, int WM, int WN,
-          int S, bool DEEP, int KG, int WPS>
+          int S, bool DEEP, int KG, bool TAIL, int WPS>
 __global__ void __launch_bounds__((ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP, KG>::NT), WPS)
 product_kernel(ProductArgs args) {
     __shared__ __attribute__((aligned(1024))) char lds[ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP, KG>::LDS];
-    product_tile_of<ET, A_T, B_N, DUAL, SEG, REG, BM, BN, WM, WN, S, DEEP, KG>(args, blockIdx.x, (SPG_LDS char*)lds);
+    product_tile_of<ET, A_T, B_N, DUAL, SEG, REG, BM, BN, WM, WN, S, DEEP, KG, TAIL>(args, blockIdx.x, (SPG_LDS char*)lds);
 }
 
 // The input gradient and the weights' gradients of a small training step in one launch:
@@ -858,8 +899,8 @@ __global__ void __launch_bounds__((ProductGeom<false, BM, BN, WM, WN, S, false, 
 gradients_kernel(ProductArgs x, ProductArgs w, int nx) {
     __shared__ __attribute__((aligned(1024))) char lds[ProductGeom<false, BM, BN, WM, WN, S, false, KG>::LDS];
     const int wg = blockIdx.x;
-    if (wg < nx) product_tile_of<ET, false, NK, false, true, REG, BM, BN, WM, WN, S, false, KG>(x, wg, (SPG_LDS char*)lds);
-    else product_tile_of<ET, true, true, false, false, REG, BM, BN, WM, WN, S, false, KG>(w, wg - nx, (SPG_LDS char*)lds);
+    if (wg < nx) product_tile_of<ET, false, NK, false, true, REG, BM, BN, WM, WN, S, false, KG, true>(x, wg, (SPG_LDS char*)lds);
+    else product_tile_of<ET, true, true, false, false, REG, BM, BN, WM, WN, S, false, KG, true>(w, wg - nx, (SPG_LDS char*)lds);
 }
 
 // ---------------------------------------------------------------------------

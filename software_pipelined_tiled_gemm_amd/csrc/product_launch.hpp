@@ -39,11 +39,19 @@ void launch_gradients(int tile, const ProductArgs& x, const ProductArgs& w, int 
 #ifdef SPG_DEFINE_PRODUCT
 template <int ET, int P, bool REG, int BM, int BN, int WM, int WN, int S, bool DEEP, int KG, int WPS = 1>
 void launch_tile(const ProductArgs& a, dim3 grid, hipStream_t st) {
+    constexpr int ES = ET == kElI8 ? 1 : 2;
+    constexpr bool LARGE = BM == 256 && !REG;   // compiled with and without the tails of rows
     constexpr bool AT = P == kGradW, BNC = P == kGatedKN || P == kGradXNK || P == kGradW;
     constexpr bool DUAL = P == kGatedNK || P == kGatedKN || P == kInt8Gated;
     constexpr bool SEG = P == kGradXNK || P == kGradXKN;
-    hipLaunchKernelGGL((product_kernel<ET, AT, BNC, DUAL, SEG, REG, BM, BN, WM, WN, S, DEEP, KG, WPS>), grid,
-                       dim3(ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP, KG>::NT), 0, st, a);
+    auto go = [&](auto tail) {
+        hipLaunchKernelGGL((product_kernel<ET, AT, BNC, DUAL, SEG, REG, BM, BN, WM, WN, S, DEEP, KG, decltype(tail)::value, WPS>),
+                           grid, dim3(ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP, KG>::NT), 0, st, a);
+    };
+    if constexpr (LARGE && P != kGradW) {
+        if (a.K * ES % 16 == 0) return go(std::false_type{});
+    }
+    go(std::bool_constant<P != kGradW>{});
 }
 
 template <int ET, int P, bool REG>

@@ -12,7 +12,8 @@ pytestmark = pytest.mark.gpu
 
 # (M, N, K): 64x64 .. 256x256 tiles, one to many k-tiles, split reductions, ragged rows
 SIZES = [(64, 64, 64), (40, 200, 128), (65, 264, 192), (96, 512, 2048), (300, 1024, 448), (300, 2731, 1001),
-         (511, 1365, 500), (512, 4096, 320), (1024, 2048, 1024), (2048, 4096, 832), (1300, 2051, 1003)]
+         (511, 1365, 500), (512, 4096, 320), (1024, 2048, 1024), (2048, 4096, 832), (1300, 2051, 1003),
+         (150, 262, 1002), (2100, 2050, 334)]
 
 
 def _both(fn, monkeypatch):
