@@ -38,6 +38,7 @@ struct Shape {
     int zm, zn;        // results stacked along rows / columns
     int mats;          // B matrices side by side in a tile (2: gated)
     double bytes;      // operands and results, read or written once
+    bool crooked;      // rows that are not whole 128-byte lines
 };
 struct Tiling {
     int tile, split;
@@ -45,21 +46,28 @@ struct Tiling {
     double us;         // estimated
 };
 
-// Measured per k-tile and per workgroup (us), see choose()
-constexpr double kTileUs[spg::kTiles] = {1.45, 0.80, 0.48, 0.29, 0.25, 0.88};
-constexpr double kStartUs[spg::kTiles] = {5.5, 3.5, 2.5, 2.8, 3.2, 3.2};
-// ... and register-staged (no 256x256 and no pair tile)
-constexpr double kStagedUs[spg::kTiles] = {0.0, 1.30, 0.95, 0.62, 0.43, 0.0};
-constexpr double kStagedStartUs[spg::kTiles] = {0.0, 4.5, 3.0, 2.8, 3.2, 0.0};
-double start_us(int t, bool reg) { return reg ? kStagedStartUs[t] : kStartUs[t]; }
-// of `wgs` workgroups: with two on a CU the staged 64x128 tile takes 0.94 each
-double tile_us(int t, bool reg, int64_t wgs) {
-    if (reg && t == spg::kTileSmall && wgs > 256) return 0.94;
-    return reg ? kStagedUs[t] : kTileUs[t];
-}
-// two workgroups on a CU: the pair tile, and the register-staged 64x128 one
+// Microseconds of a tile class: a k-tile, and a workgroup's start and store, with direct
+// copies and register-staged (which has no 256x256 and no pair tile); see choose()
+constexpr double kTileUs[spg::kTiles] = {1.18, 0.77, 0.45, 0.33, 0.26, 0.68};
+constexpr double kStartUs[spg::kTiles] = {5.5, 5.6, 2.6, 2.75, 3.2, 2.9};
+constexpr double kStagedUs[spg::kTiles] = {0.0, 1.30, 0.65, 0.48, 0.42, 0.0};
+constexpr double kStagedStartUs[spg::kTiles] = {0.0, 5.3, 3.8, 2.9, 3.2, 0.0};
+// direct copies of rows that are not whole 128-byte lines: each 128-byte chunk of a k-tile is
+// two lines' halves
+constexpr double kCrooked[spg::kTiles] = {1.16, 1.0, 1.17, 1.17, 1.0, 1.17};
+// two workgroups on a CU: the pair tile, and the register-staged 64x128 one; alone on their
+// CUs the first starts faster and the second multiplies faster
 bool paired(int t, bool reg) { return t == (reg ? (int)spg::kTileSmall : (int)spg::kTilePair); }
 double slots(int t, bool reg) { return paired(t, reg) ? 512.0 : 256.0; }
+double tile_us(int t, bool reg, bool crooked, int64_t wgs) {
+    const bool two = paired(t, reg) && wgs > 256;
+    if (reg) return two ? 0.84 : kStagedUs[t];
+    return (two ? 0.82 : kTileUs[t]) * (crooked ? kCrooked[t] : 1.0);
+}
+double start_us(int t, bool reg, int64_t wgs) {
+    if (!reg && paired(t, reg) && wgs <= 256) return 1.2;
+    return reg ? kStagedStartUs[t] : kStartUs[t];
+}
 constexpr double kLaunchUs = 1.5;
 
 double sum_us(const Shape& s, int64_t split) {
@@ -69,16 +77,16 @@ int64_t tiles_of(const Shape& s, int t) {
     return ceil_div(s.M, spg::kTileM[t]) * s.zm * ceil_div(s.N, spg::kTileN[t] / s.mats) * s.zn;
 }
 
-// Estimated microseconds of a tile class and a number of parts.  A tile class fills a CU's
-// LDS, so a CU runs one workgroup at a time: rounds of the 256 CUs times a part's k-tiles and
-// a start and store per round, plus a launch; never less than the operands take to read.
-// Parts add a kernel and their sums' traffic.  Measured per k-tile with all CUs busy (us):
-// 256x256 1.45, 256x128 0.80, 128x128 0.48, 64x128 0.29, 64x64 0.25, about a third less with
-// few (a CU copies about 105 bytes a nanosecond into its LDS, which is what bounds the small
-// tiles); one k-tile alone 7, 5, 4, 4.4 and 4.8.  Two 128x128 workgroups on a CU take 0.88 a
-// k-tile each, but a round of 512 of them only 3.4 beside: 4096 x 8192 outputs of 64, 256
-// and 1024 reductions take 36, 55 and 140 us against 54, 73 and 164 one at a time, and 32,
-// 49 and 121 with the 256x256 tile, which needs a large grid.
+// Estimated microseconds of a tile class and a number of parts.  A workgroup fills a CU's LDS
+// (half of it for a paired tile): rounds of the CUs times a part's k-tiles and a start and
+// store, plus a launch; never less than the operands take to read.  Parts add a kernel and
+// their sums' traffic.  The constants are fitted to the measured times of every tile class
+// and up to 16 parts at 360 shapes of the seven products, 1 to 12288 rows, columns and
+// reductions: the choice takes 1% longer than the fastest on average, 30% at worst.  What
+// bounds the small tiles is that a CU copies about 105 bytes a nanosecond into its LDS; what
+// bounds short reductions, the start and the store.  Pairs: 4096 x 8192 outputs of 64, 256
+// and 1024 reductions take 36, 55 and 140 us against 54, 73 and 164 with one 128x128 tile a
+// CU, and 32, 49 and 121 with the 256x256 tile, which needs a large grid.
 Tiling choose(const Shape& s, bool reg) {
     Tiling best{spg::kTileSmall, 1, s.kt, 0.0};
     double best_t = -1.0;
@@ -89,8 +97,7 @@ Tiling choose(const Shape& s, bool reg) {
             const int64_t part = ceil_div(s.kt, split);
             if (split > 1 && (part < 4 || ceil_div(s.kt, part) != split)) continue;
             const double rounds = std::ceil((double)(tiles * split) / slots(t, reg));
-            const double busy = paired(t, reg) ? 1.0 : 0.68 + 0.32 * std::min(1.0, (double)(tiles * split) / 256.0);
-            double us = kLaunchUs + rounds * (tile_us(t, reg, tiles * split) * busy * (double)part + start_us(t, reg));
+            double us = kLaunchUs + rounds * (tile_us(t, reg, s.crooked, tiles * split) * (double)part + start_us(t, reg, tiles * split));
             us = std::max(us, 3.0 + s.bytes / 5.0e6) + sum_us(s, split);
             if (best_t < 0 || us < best_t) {
                 best_t = us;
@@ -123,20 +130,23 @@ struct Planned {
 // The copy reads and writes the misaligned matrices once (about 4.5 TB/s, and a launch).
 // M = 2048, N = 4096, K = 1001, two weights: register-staged 51.2 us, direct 30.3 and the
 // copy of 20 MB about 12; at M = 300, N = 2731 13.4 against 11.5 and 8.
-Planned plan_product(const Shape& s, std::initializer_list<Stored> mats);
+Planned plan_product(Shape s, std::initializer_list<Stored> mats);
 
 int64_t part_ld(const Shape& s) { return up(s.N, 4) * s.mats * s.zn; }
 int64_t part_bytes(const Shape& s, const Tiling& t) {
     return t.split > 1 ? up((int64_t)t.split * s.M * s.zm * part_ld(s) * 4, kAlign) : 0;
 }
 
-Planned plan_product(const Shape& s, std::initializer_list<Stored> mats) {
-    Planned p{s, {choose(s, false), choose(s, true)}, false, 0, 0};
+Planned plan_product(Shape s, std::initializer_list<Stored> mats) {
     int64_t all = 0, bad = 0;
     for (const Stored& m : mats) {
         all += up(m.bytes(), kAlign);
         if (!m.aligned()) bad += m.bytes();
+        s.crooked |= m.row_bytes % 128 != 0;
     }
+    // rows on odd bytes only reach the direct copies laid out again
+    if (bad > 0) s.crooked = false;
+    Planned p{s, {choose(s, false), choose(s, true)}, false, 0, 0};
     p.pack = bad > 0 && p.t[0].us + 3.0 + 2.0 * (double)bad / 4.5e6 < p.t[1].us;
     p.parts = std::max(part_bytes(s, p.t[0]), part_bytes(s, p.t[1]));
     p.packed = p.pack ? all : 0;
@@ -151,7 +161,7 @@ struct Operands {
     int64_t total = 0;
     char* at;           // where the next copy goes
     explicit Operands(void* ws) : at((char*)ws) {}
-    void copy(const Stored& m, const char*& p, int64_t& pitch) {
+    void copy(const Stored& m, const char*& p, uint32_t& pitch) {
         pk.src[n] = p;
         pk.dst[n] = at;
         pk.row[n] = m.row_bytes;
@@ -159,7 +169,7 @@ struct Operands {
         pk.chunks[n] = m.bytes() / 16;
         total += pk.chunks[n];
         p = at;
-        pitch = m.pitch();
+        pitch = (uint32_t)m.pitch();
         at += up(m.bytes(), kAlign);
         ++n;
     }
@@ -191,8 +201,8 @@ Merged merge(const Planned& x, const Planned& w, bool reg) {
             const int64_t part = ceil_div(x.s.kt, split);
             if (split > 1 && (part < 4 || ceil_div(x.s.kt, part) != split)) continue;
             const int64_t nx = tiles_of(x.s, t) * split, nw = tiles_of(w.s, t);
-            const double k = tile_us(t, reg, nx + nw);
-            const double cx = k * (double)part + start_us(t, reg), cw = k * (double)w.s.kt + start_us(t, reg);
+            const double k = tile_us(t, reg, x.s.crooked || w.s.crooked, nx + nw);
+            const double s0 = start_us(t, reg, nx + nw), cx = k * (double)part + s0, cw = k * (double)w.s.kt + s0;
             const double all = ((double)nx * cx + (double)nw * cw) / slots(t, reg);
             // past one round the last workgroups leave CUs idle: half of one's time
             double us = std::max(std::max(cx, cw), nx + nw > slots(t, reg) ? all + 0.5 * std::max(cx, cw) : 0.0);
@@ -232,19 +242,18 @@ void launch_tiled(int product, int et, bool reg, int tile, const ProductArgs& a,
 
 // Fill in the tile grid of a product; returns its workgroups.
 int64_t set_grid(ProductArgs& a, const Shape& s, int tile, int split, int64_t kt_part, void* parts) {
-    a.zm = s.zm;
-    a.zn = s.zn;
+    a.zm = (uint8_t)s.zm;
+    a.zn = (uint8_t)s.zn;
     a.tiles_m = (int32_t)ceil_div(s.M, spg::kTileM[tile]);
     a.tiles_n = (int32_t)ceil_div(s.N, spg::kTileN[tile] / s.mats);
     // rows of tiles rastered together: 4 (measured at M = 8192, N = 12288: 2, 4, 8 and 16
     // take 1198, 1186, 1200 and 1215 us), all of them when there are few, else even groups,
     // so that no short last group reads every weight again
     const int64_t rows = (int64_t)a.tiles_m * a.zm;
-    a.group_m = (int32_t)(rows <= 8 ? rows : ceil_div(rows, ceil_div(rows, 4)));
-    a.split = split;
+    a.group_m = (uint8_t)(rows <= 8 ? rows : ceil_div(rows, ceil_div(rows, 4)));
+    a.split = (uint8_t)split;
     a.kt_part = (int32_t)kt_part;
     a.part = split > 1 ? (float*)parts : nullptr;
-    a.ldp = part_ld(s);
     return rows * a.tiles_n * a.zn * split;
 }
 
@@ -299,7 +308,7 @@ gemm_status run_merged(bool nk, int et, bool reg, const Merged& m, const Shape& 
 template <int ET, bool DUAL>
 void stream_rows(const ProductArgs& a, hipStream_t st) {
     const dim3 grid((unsigned)ceil_div(a.N, 16)), wg(512);
-    const uintptr_t all = (uintptr_t)a.A[0] | (uintptr_t)a.B[0] | (DUAL ? (uintptr_t)a.B[1] : 0) | (uintptr_t)a.lda | (uintptr_t)a.ldb;
+    const uintptr_t all = (uintptr_t)a.A | (uintptr_t)a.B[0] | (DUAL ? (uintptr_t)a.B[1] : 0) | (uintptr_t)a.lda | (uintptr_t)a.ldb;
     if (all % 4 == 0) hipLaunchKernelGGL((spg::stream_kernel<ET, DUAL, true, 8, 4>), grid, wg, 0, st, a);
     else hipLaunchKernelGGL((spg::stream_kernel<ET, DUAL, false, 8, 4>), grid, wg, 0, st, a);
 }
@@ -375,11 +384,11 @@ gemm_status gemm_gated_create(gemm_gated_handle* out, int64_t M, int64_t N, int6
     const double grad_bytes = 2 * (2 * m * n + 2 * n * k + m * k);
     p->fwd = p->dx = p->dw = Planned{};
     if (!p->simple && !streams(p))
-        p->fwd = plan_product(Shape{M, N, ceil_div(K, 64), 1, 1, 2, 2 * (m * k + 2 * n * k + m * n)}, {p->x, p->w, p->w});
+        p->fwd = plan_product(Shape{M, N, ceil_div(K, 64), 1, 1, 2, 2 * (m * k + 2 * n * k + m * n), false}, {p->x, p->w, p->w});
     if (!p->simple_back) {
-        p->dx = plan_product(Shape{M, K, 2 * ceil_div(N, 64), 1, 1, 1, grad_bytes}, {p->w, p->w});
-        p->dw = plan_product(p->nk ? Shape{N, K, ceil_div(M, 64), 2, 1, 1, grad_bytes}
-                                   : Shape{K, N, ceil_div(M, 64), 1, 2, 1, grad_bytes}, {p->x});
+        p->dx = plan_product(Shape{M, K, 2 * ceil_div(N, 64), 1, 1, 1, grad_bytes, false}, {p->w, p->w});
+        p->dw = plan_product(p->nk ? Shape{N, K, ceil_div(M, 64), 2, 1, 1, grad_bytes, false}
+                                   : Shape{K, N, ceil_div(M, 64), 1, 2, 1, grad_bytes, false}, {p->x});
     }
     int64_t merged = 0;
     for (int r = 0; r < 2; ++r) {
@@ -388,7 +397,7 @@ gemm_status gemm_gated_create(gemm_gated_handle* out, int64_t M, int64_t N, int6
     }
     p->ws_fwd = p->fwd.bytes();
     p->off_part = up(M * p->np * 4, kAlign);
-    p->ws_back = p->off_part + std::max(merged, std::max(p->dx.bytes(), p->dw.bytes()));
+    p->ws_back = p->off_part + std::max(merged, std::max(p->dx.parts, p->dw.parts) + p->dx.packed + p->dw.packed);
     *out = p;
     return GEMM_OK;
 }
@@ -401,20 +410,20 @@ gemm_status gemm_gated_run(gemm_gated_handle h, const void* X, const void* Wg, c
     if (h->M == 0 || h->N == 0) return GEMM_OK;
     if (!H || (h->K > 0 && (!X || !Wg || !Wu))) return GEMM_ERR_INVALID_ARG;
     ProductArgs a{};
-    a.A[0] = (const char*)X;
+    a.A = (const char*)X;
     a.B[0] = (const char*)Wg;
     a.B[1] = (const char*)Wu;
-    a.C[0] = H;
+    a.C = H;
     a.G = G;
     a.U = U;
     a.M = (int32_t)h->M;
     a.N = (int32_t)h->N;
     a.K = (int32_t)h->K;
-    a.lda = h->K * 2;
-    a.ldb = (h->nk ? h->K : h->N) * 2;
+    a.lda = (uint32_t)(h->K * 2);
+    a.ldb = (uint32_t)((h->nk ? h->K : h->N) * 2);
     a.b_cols = (int32_t)h->N;
     a.segments = 1;
-    a.act = h->act;
+    a.act = (uint8_t)h->act;
     if (h->simple) {
         spg::SimpleArgs s{a, h->K, 1, h->nk ? h->K : 1, h->nk ? 1 : h->N, 0};
         return h->et == spg::kElBF16 ? run_simple<spg::kElBF16, true>(s, stream) : run_simple<spg::kElF16, true>(s, stream);
@@ -431,7 +440,7 @@ gemm_status gemm_gated_run(gemm_gated_handle h, const void* X, const void* Wg, c
     if (need > 0 && (!workspace || (uintptr_t)workspace % 16 != 0 || workspace_bytes < h->ws_fwd)) return GEMM_ERR_INVALID_ARG;
     if (pack) {
         Operands o((char*)workspace + h->fwd.parts);
-        if (!xa) o.copy(h->x, a.A[0], a.lda);
+        if (!xa) o.copy(h->x, a.A, a.lda);
         if (!wa) {
             o.copy(h->w, a.B[0], a.ldb);
             o.copy(h->w, a.B[1], a.ldb);
@@ -469,31 +478,31 @@ gemm_status gemm_gated_backward(gemm_gated_handle h, const void* dH, const void*
     }
     // dX = [dG dU] . [Wg; Wu]: one sum over both segments
     ProductArgs x{};
-    x.A[0] = (const char*)D;
+    x.A = (const char*)D;
     x.B[0] = (const char*)Wg;
     x.B[1] = (const char*)Wu;
-    x.C[0] = dX;
+    x.C = dX;
     x.M = (int32_t)M;
     x.N = (int32_t)K;
     x.K = (int32_t)N;
-    x.lda = h->np * 4;
-    x.ldb = (h->nk ? K : N) * 2;
+    x.lda = (uint32_t)(h->np * 4);
+    x.ldb = (uint32_t)((h->nk ? K : N) * 2);
     x.b_cols = (int32_t)K;
     x.segments = 2;
     // dWg, dWu: [N,K] weights dG^T X and dU^T X, [K,N] weights X^T dG and X^T dU
     ProductArgs w{};
-    for (int z = 0; z < 2; ++z) {
-        const char* d = (const char*)(D + z * h->np);
-        w.A[z] = h->nk ? d : (const char*)X;
-        w.B[z] = h->nk ? (const char*)X : d;
-    }
-    w.C[0] = dWg;
-    w.C[1] = dWu;
+    const char* const d[2] = {(const char*)D, (const char*)(D + h->np)};
+    w.A = h->nk ? d[0] : (const char*)X;
+    w.A1 = h->nk ? d[1] : (const char*)X;
+    for (int z = 0; z < 2; ++z) w.B[z] = h->nk ? (const char*)X : d[z];
+    w.C = dWg;
+    w.C1 = dWu;
     w.M = (int32_t)(h->nk ? N : K);
     w.N = (int32_t)(h->nk ? K : N);
     w.K = (int32_t)M;
-    w.lda = h->nk ? h->np * 4 : K * 2;
-    w.ldb = h->nk ? K * 2 : h->np * 4;
+    const int64_t lda = h->nk ? h->np * 4 : K * 2, ldb = h->nk ? K * 2 : h->np * 4;
+    w.lda = (uint32_t)lda;
+    w.ldb = (uint32_t)ldb;
     w.a_cols = (int32_t)(h->nk ? h->np : K);
     w.b_cols = (int32_t)(h->nk ? K : h->np);
     w.segments = 1;
@@ -505,10 +514,10 @@ gemm_status gemm_gated_backward(gemm_gated_handle h, const void* dH, const void*
         }
         for (int z = 0; z < 2 && N > 0; ++z) {
             ProductArgs one = w;
-            one.A[0] = w.A[z];
+            one.A = z ? w.A1 : w.A;
             one.B[0] = w.B[z];
-            one.C[0] = w.C[z];
-            spg::SimpleArgs s{one, 1, w.lda / 2, 1, w.ldb / 2, 0};
+            one.C = z ? w.C1 : w.C;
+            spg::SimpleArgs s{one, 1, lda / 2, 1, ldb / 2, 0};
             const gemm_status e = bf ? run_simple<spg::kElBF16, false>(s, stream) : run_simple<spg::kElF16, false>(s, stream);
             if (e != GEMM_OK) return e;
         }
@@ -519,25 +528,23 @@ gemm_status gemm_gated_backward(gemm_gated_handle h, const void* dH, const void*
     const Merged& both = h->both[!(wa && xa)];
     if (both.on)
         return run_merged(h->nk, h->et, !(wa && xa), both, h->dx.s, h->dw.s, x, w, parts, stream);
+    Operands o((char*)parts + std::max(h->dx.parts, h->dw.parts));
     if (!wa && h->dx.pack) {
-        Operands o((char*)parts + h->dx.parts);
         o.copy(h->w, x.B[0], x.ldb);
         o.copy(h->w, x.B[1], x.ldb);
         x.b_cols = (int32_t)up(K, 8);
-        const gemm_status e = o.launch(2, stream);
-        if (e != GEMM_OK) return e;
     }
-    const gemm_status e = run_tiled(h->nk ? spg::kGradXNK : spg::kGradXKN, h->et, !wa && !h->dx.pack, h->dx, x, parts, stream);
-    if (e != GEMM_OK) return e;
     if (!xa && h->dw.pack) {
-        Operands o((char*)parts + h->dw.parts);
         const char* p = (const char*)X;
         o.copy(h->x, p, h->nk ? w.ldb : w.lda);
-        (h->nk ? w.B : w.A)[0] = (h->nk ? w.B : w.A)[1] = p;
+        if (h->nk) w.B[0] = w.B[1] = p;
+        else w.A = w.A1 = p;
         (h->nk ? w.b_cols : w.a_cols) = (int32_t)up(K, 8);
-        const gemm_status e2 = o.launch(2, stream);
-        if (e2 != GEMM_OK) return e2;
     }
+    gemm_status e = o.launch(2, stream);
+    if (e != GEMM_OK) return e;
+    e = run_tiled(h->nk ? spg::kGradXNK : spg::kGradXKN, h->et, !wa && !h->dx.pack, h->dx, x, parts, stream);
+    if (e != GEMM_OK) return e;
     return run_tiled(spg::kGradW, h->et, !xa && !h->dw.pack, h->dw, w, parts, stream);
 }
 
@@ -571,7 +578,7 @@ gemm_status gemm_quantized_create(gemm_quantized_handle* out, int64_t M, int64_t
     p->b = Stored{N, K};
     p->p = Planned{};
     if (!p->simple && M > kStreamRows) {
-        const Shape s{M, N, ceil_div(K, 128), 1, 1, mats, m * k + mats * n * k + m * n * (out_dtype == GEMM_F32 ? 4 : 2)};
+        const Shape s{M, N, ceil_div(K, 128), 1, 1, mats, m * k + mats * n * k + m * n * (out_dtype == GEMM_F32 ? 4 : 2), false};
         p->p = mats == 2 ? plan_product(s, {p->a, p->b, p->b}) : plan_product(s, {p->a, p->b});
     }
     p->ws = p->p.bytes();
@@ -591,20 +598,20 @@ gemm_status gemm_quantized_run(gemm_quantized_handle h, const int8_t* A, const f
     if (!C || !scale_a || !scale_b || (dual && !scale_b2)) return GEMM_ERR_INVALID_ARG;
     if (h->K > 0 && (!A || !B || (dual && !B2))) return GEMM_ERR_INVALID_ARG;
     ProductArgs a{};
-    a.A[0] = (const char*)A;
+    a.A = (const char*)A;
     a.B[0] = (const char*)B;
     a.B[1] = (const char*)B2;
-    a.C[0] = C;
+    a.C = C;
     a.sa = scale_a;
     a.sb[0] = scale_b;
     a.sb[1] = scale_b2;
     a.M = (int32_t)h->M;
     a.N = (int32_t)h->N;
     a.K = (int32_t)h->K;
-    a.lda = a.ldb = h->K;
+    a.lda = a.ldb = (uint32_t)h->K;
     a.segments = 1;
-    a.out_dtype = h->out;
-    a.act = h->act;
+    a.out_dtype = (uint8_t)h->out;
+    a.act = (uint8_t)h->act;
     if (h->simple) {
         spg::SimpleArgs s{a, h->K, 1, h->K, 1, 0};
         return dual ? run_simple<spg::kElI8, true>(s, stream) : run_simple<spg::kElI8, false>(s, stream);
@@ -621,7 +628,7 @@ gemm_status gemm_quantized_run(gemm_quantized_handle h, const int8_t* A, const f
     if (need > 0 && (!workspace || (uintptr_t)workspace % 16 != 0 || workspace_bytes < h->ws)) return GEMM_ERR_INVALID_ARG;
     if (pack) {
         Operands o((char*)workspace + h->p.parts);
-        if (!aa) o.copy(h->a, a.A[0], a.lda);
+        if (!aa) o.copy(h->a, a.A, a.lda);
         if (!ba) {
             o.copy(h->b, a.B[0], a.ldb);
             if (dual) o.copy(h->b, a.B[1], a.ldb);

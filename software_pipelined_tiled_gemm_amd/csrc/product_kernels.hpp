@@ -26,27 +26,43 @@ enum { kActNone = 0, kActSilu = 1, kActGelu = 2, kActRelu = 3 };
 
 typedef int32_t intx4 __attribute__((ext_vector_type(4)));
 
+// Kept small: the host writes a launch's arguments through PCIe, about 4 ns a byte (an empty
+// kernel with 40 bytes of them launches in 2.8 us, with 232 in 3.6).
 struct ProductArgs {
-    const char* A[2];   // A[1]: the second result's A (weight gradients of [N,K] weights)
+    const char* A;
     const char* B[2];   // B[1]: the up projection; the second segment; the second result's B
-    void* C[2];
-    void* G;            // gated: the pre-activations, or null
-    void* U;
+    void* C;
+    union {
+        struct {        // int8: row scales of A, column scales of B[0] and B[1]
+            const float* sa;
+            const float* sb[2];
+        };
+        struct {        // gated: the pre-activations, or null
+            void* G;
+            void* U;
+        };
+        struct {        // weight gradients: the second result and (for [N,K] weights) its A
+            const char* A1;
+            void* C1;
+        };
+    };
     float* part;        // split reduction: fp32 (int8: int32) partial sums, or null
-    const float* sa;    // int8: row scales of A, column scales of B[0] and B[1]
-    const float* sb[2];
-    int64_t lda, ldb;   // bytes between the stored rows of A and of B
-    int64_t ldp;        // partial sums: elements between rows
+    uint32_t lda, ldb;  // bytes between the stored rows of A and of B
     int32_t M, N, K;    // rows and columns of one result, length of one segment of the sum
     int32_t a_cols, b_cols;   // operands stored reduction-major: columns that may be read
     int32_t tiles_m, tiles_n; // of one result
-    int32_t zm, zn;     // results stacked along the rows or columns of the tile grid (1 or 2)
-    int32_t group_m;
-    int32_t split;      // parts of the reduction (the grid is split times the tiles)
     int32_t kt_part;    // k-tiles of one part
-    int32_t segments;   // 1, or 2: B[1] continues the sum where B[0] ends
-    int32_t out_dtype, act;
+    uint8_t zm, zn;     // results stacked along the rows or columns of the tile grid (1 or 2)
+    uint8_t group_m;
+    uint8_t split;      // parts of the reduction (the grid is split times the tiles)
+    uint8_t segments;   // 1, or 2: B[1] continues the sum where B[0] ends
+    uint8_t out_dtype, act;
 };
+
+// elements between the rows of partial sums
+__device__ __forceinline__ int64_t part_pitch(const ProductArgs& a, bool dual) {
+    return (int64_t)((a.N + 3) & ~3) * (dual ? 2 : 1) * a.zn;
+}
 
 __device__ __forceinline__ float silu(float x) {
     // x / (1 + exp(-x)), exp as 2^(x log2 e); saturates to -0 and to x
@@ -196,9 +212,9 @@ __device__ __forceinline__ void finish4(const AccOf<ET>& s0, const AccOf<ET>& s1
 #pragma unroll
             for (int e = 0; e < 4; ++e) h[e] = act_t<decltype(ac)::value>(v[e]) * w[e];
         });
-        put(args.C[0], h);
+        put(args.C, h);
     } else {
-        put(args.C[z], v);
+        put(z ? args.C1 : args.C, v);
     }
 }
 
@@ -367,7 +383,7 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, 
     const uint32_t row_bytes = REG ? (uint32_t)(K * ES) : ((uint32_t)(K * ES) + 3u) & ~3u;
 
     // ---- copy sources ----
-    const char* a_ptr = args.A[!DUAL && args.zm == 2 ? z : 0];
+    const char* a_ptr = A_T && args.zm == 2 && z ? args.A1 : args.A;
     const char* b_ptr0 = args.B[!DUAL && args.zn == 2 ? z : 0];
     const char* b_ptr1 = args.B[1];
     // DUAL: waves of the lower half copy B[0], the others B[1]
@@ -384,7 +400,7 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, 
     // last row.  Reduction-major: 64 rows further, as many of them as exist; columns past the
     // last are masked by offset.  Written as selects: a branch here would cut the k-step that
     // carries the copies in two.
-    const uint32_t lda = (uint32_t)args.lda, ldb = (uint32_t)args.ldb;
+    const uint32_t lda = args.lda, ldb = args.ldb;
     const uint64_t a_at = (uint64_t)(uintptr_t)a_ptr + (A_T ? 0 : (uint64_t)m0 * lda - kBack);
     const uint64_t b_at[2] = {(uint64_t)(uintptr_t)b_mine + (B_N ? 0 : (uint64_t)n0 * ldb - kBack),
                               (uint64_t)(uintptr_t)(SEG ? b_ptr1 : b_mine) + (B_N ? 0 : (uint64_t)n0 * ldb - kBack)};
@@ -428,8 +444,8 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, 
     if (DUAL && firstB >= BNS / 8) firstB -= BNS / 8;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        kcA[h] = (uint32_t)((firstA + h) * 8 + lane / 8) * (uint32_t)args.lda + (uint32_t)kc_pos(firstA + h) + kBack;
-        kcB[h] = (uint32_t)((firstB + h) * 8 + lane / 8) * (uint32_t)args.ldb + (uint32_t)kc_pos(firstB + h) + kBack;
+        kcA[h] = (uint32_t)((firstA + h) * 8 + lane / 8) * args.lda + (uint32_t)kc_pos(firstA + h) + kBack;
+        kcB[h] = (uint32_t)((firstB + h) * 8 + lane / 8) * args.ldb + (uint32_t)kc_pos(firstB + h) + kBack;
     }
     const int posA = kc_pos(firstA), posB = kc_pos(firstB);
     // reduction-major: op d holds 64 / CPR rows; over: columns of the chunk past the last
@@ -466,11 +482,11 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, 
         constexpr int j = decltype(jc)::value;
         if constexpr (j < A_OPS) {
             if constexpr (A_T) return trA[j];
-            else return kc_off(kcA[j & 1] + (uint32_t)(j >> 1) * 16u * (uint32_t)args.lda, posA ^ ((j & 1) * 64), lim);
+            else return kc_off(kcA[j & 1] + (uint32_t)(j >> 1) * 16u * args.lda, posA ^ ((j & 1) * 64), lim);
         } else {
             constexpr int i = j - A_OPS;
             if constexpr (B_N) return trB[i];
-            else return kc_off(kcB[i & 1] + (uint32_t)(i >> 1) * 16u * (uint32_t)args.ldb, posB ^ ((i & 1) * 64), lim);
+            else return kc_off(kcB[i & 1] + (uint32_t)(i >> 1) * 16u * args.ldb, posB ^ ((i & 1) * 64), lim);
         }
     };
     // REG: bits to shift the loaded chunk down by
@@ -808,7 +824,8 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, 
         // a part of the sum: raw accumulators, row-major, 16 bytes per lane
         const int np4 = (N + 3) & ~3;
         const int zrow = args.zm == 2 ? z * M : 0, zcol = args.zn == 2 ? z * np4 : 0;
-        float* base = args.part + ((size_t)sp * M * args.zm + zrow) * args.ldp + zcol;
+        const int64_t ldp = part_pitch(args, DUAL);
+        float* base = args.part + ((size_t)sp * M * args.zm + zrow) * ldp + zcol;
 #pragma unroll
         for (int bm = 0; bm < TM; ++bm) {
             const int m = m_base + bm * 16 + (lane & 15);
@@ -817,7 +834,7 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, 
                 const bool second = DUAL && bn >= TN / 2;
                 const int n = n_base + (second ? bn - TN / 2 : bn) * 16 + 4 * (lane >> 4);
                 if (m < M && n < N)
-                    *(AccOf<ET>*)(base + (size_t)m * args.ldp + (second ? np4 : 0) + n) = acc[bn][bm];
+                    *(AccOf<ET>*)(base + (size_t)m * ldp + (second ? np4 : 0) + n) = acc[bn][bm];
             }
         }
         wait_vmcnt<0>();   // the zero-fill copies past the last k-tile land before the LDS is given up
@@ -856,10 +873,10 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, 
                     store_block<OD, TM, TN / 2, WNS>(
                         [&](int bn, int bm, int e) __attribute__((always_inline)) {
                             return act_t<decltype(ac)::value>(scaled(bn, bm, e)) * scaled(bn + TN / 2, bm, e);
-                        }, stg, args.C[0], M, N, m_base, n_base, lane);
+                        }, stg, args.C, M, N, m_base, n_base, lane);
                 });
             else
-                store_block<OD, TM, TN, WNS>(scaled, stg, args.C[0], M, N, m_base, n_base, lane);
+                store_block<OD, TM, TN, WNS>(scaled, stg, args.C, M, N, m_base, n_base, lane);
         });
     } else {
         constexpr int OD = ET == kElBF16 ? kOutBF16 : kOutF16;
@@ -874,11 +891,11 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, 
                 store_block<OD, TM, TN / 2, WNS>(
                     [&](int bn, int bm, int e) __attribute__((always_inline)) {
                         return act_t<decltype(ac)::value>(acc[bn][bm][e]) * acc[bn + TN / 2][bm][e];
-                    }, stg, args.C[0], M, N, m_base, n_base, lane);
+                    }, stg, args.C, M, N, m_base, n_base, lane);
             });
         } else {
             store_block<OD, TM, TN, WNS>([&](int bn, int bm, int e) __attribute__((always_inline)) { return acc[bn][bm][e]; },
-                                         stg, args.C[z], M, N, m_base, n_base, lane);
+                                         stg, A_T && z ? args.C1 : args.C, M, N, m_base, n_base, lane);
         }
     }
 }
@@ -935,7 +952,7 @@ __global__ void __launch_bounds__(NW * 64) stream_kernel(ProductArgs args) {
     const int kb = args.K * ES;                       // bytes of a row
     const int n0 = blockIdx.x * 16;
     const int rows = N - n0 < 16 ? N - n0 : 16;
-    const uint32_t ldb = (uint32_t)args.ldb, lda = (uint32_t)args.lda;
+    const uint32_t ldb = args.ldb, lda = args.lda;
     // a matrix: its resource from the word its first row starts in, this lane's row from
     // there, and how many bytes past a word the row starts
     struct Rows {
@@ -948,7 +965,7 @@ __global__ void __launch_bounds__(NW * 64) stream_kernel(ProductArgs args) {
         const uint32_t at = skip + (uint32_t)(lane & 15) * ld;
         return Rows{make_rsrc_b(p - skip, WORDS ? bytes : (bytes + 3u) & ~3u), WORDS ? at : at & ~3u, WORDS ? 0u : at & 3u};
     };
-    const Rows x = rows_of(args.A[0], lda, M);
+    const Rows x = rows_of(args.A, lda, M);
     const Rows b0 = rows_of(args.B[0] + (size_t)n0 * ldb, ldb, rows);
     const Rows b1 = rows_of((DUAL ? args.B[1] : args.B[0]) + (size_t)n0 * ldb, ldb, rows);
     const bool ragged = (kb & 15) != 0;
@@ -1092,8 +1109,9 @@ __global__ void __launch_bounds__(256) sum_parts(ProductArgs args) {
     if (i >= rows * quads) return;
     int64_t m = i / quads;
     int n = (int)(i - m * quads) * 4;
-    const AccOf<ET>* p = (const AccOf<ET>*)(args.part + (size_t)m * args.ldp + n);
-    const size_t step = (size_t)rows * args.ldp / 4;
+    const int64_t ldp = part_pitch(args, DUAL);
+    const AccOf<ET>* p = (const AccOf<ET>*)(args.part + (size_t)m * ldp + n);
+    const size_t step = (size_t)rows * ldp / 4;
     AccOf<ET> s0 = p[0], s1 = s0;
     if constexpr (DUAL) s1 = p[np4 / 4];
     // eight parts' loads in flight at a time, added in order
@@ -1144,7 +1162,7 @@ __global__ void __launch_bounds__(256) simple_product(SimpleArgs a) {
         };
         for (int seg = 0; seg < args.segments; ++seg)
             for (int64_t k = 0; k < args.K; ++k) {
-                const V x = at(args.A[0], m * a.sam + k * a.sak + seg * a.seg_a);
+                const V x = at(args.A, m * a.sam + k * a.sak + seg * a.seg_a);
                 s0 += x * at(args.B[seg], n * a.sbn + k * a.sbk);
                 if constexpr (DUAL) s1 += x * at(args.B[1], n * a.sbn + k * a.sbk);
             }
