@@ -48,30 +48,31 @@ struct Tiling {
 
 // Microseconds of a tile class: a k-tile, and a workgroup's start and store, with direct
 // copies and register-staged (which has no 256x256 and no pair tile); see choose()
-constexpr double kTileUs[spg::kTiles] = {1.18, 0.77, 0.45, 0.33, 0.26, 0.68};
-constexpr double kStartUs[spg::kTiles] = {5.5, 5.6, 2.6, 2.75, 3.2, 2.9};
+constexpr double kTileUs[spg::kTiles] = {1.27, 0.76, 0.51, 0.32, 0.26, 0.70};
+constexpr double kStartUs[spg::kTiles] = {5.3, 5.6, 2.5, 2.75, 2.75, 2.9};
 constexpr double kStagedUs[spg::kTiles] = {0.0, 1.30, 0.65, 0.48, 0.42, 0.0};
-constexpr double kStagedStartUs[spg::kTiles] = {0.0, 5.3, 3.8, 2.9, 3.2, 0.0};
+constexpr double kStagedStartUs[spg::kTiles] = {0.0, 5.3, 3.8, 2.9, 3.3, 0.0};
 // direct copies of rows that are not whole 128-byte lines: each 128-byte chunk of a k-tile is
 // two lines' halves
-constexpr double kCrooked[spg::kTiles] = {1.16, 1.0, 1.17, 1.17, 1.0, 1.17};
+constexpr double kCrooked[spg::kTiles] = {1.08, 1.10, 1.05, 1.20, 1.14, 1.18};
 // two workgroups on a CU: the pair tile, and the register-staged 64x128 one; alone on their
-// CUs the first starts faster and the second multiplies faster
+// CUs the first starts faster and both multiply faster, and a single round in pairs has
+// nothing to overlap the starts and stores with
 bool paired(int t, bool reg) { return t == (reg ? (int)spg::kTileSmall : (int)spg::kTilePair); }
 double slots(int t, bool reg) { return paired(t, reg) ? 512.0 : 256.0; }
 double tile_us(int t, bool reg, bool crooked, int64_t wgs) {
     const bool two = paired(t, reg) && wgs > 256;
     if (reg) return two ? 0.84 : kStagedUs[t];
-    return (two ? 0.82 : kTileUs[t]) * (crooked ? kCrooked[t] : 1.0);
+    return (two ? (wgs > 512 ? 0.81 : 1.30) : kTileUs[t]) * (crooked ? kCrooked[t] : 1.0);
 }
 double start_us(int t, bool reg, int64_t wgs) {
-    if (!reg && paired(t, reg) && wgs <= 256) return 1.2;
+    if (!reg && paired(t, reg) && wgs <= 256) return 1.0;
     return reg ? kStagedStartUs[t] : kStartUs[t];
 }
 constexpr double kLaunchUs = 1.5;
 
 double sum_us(const Shape& s, int64_t split) {
-    return split > 1 ? 3.5 + 2.0 * 4.0 * (double)split * s.M * s.zm * s.N * s.zn * s.mats / 5.0e6 : 0.0;
+    return split > 1 ? 4.5 + 2.0 * 4.0 * (double)split * s.M * s.zm * s.N * s.zn * s.mats / 5.5e6 : 0.0;
 }
 int64_t tiles_of(const Shape& s, int t) {
     return ceil_div(s.M, spg::kTileM[t]) * s.zm * ceil_div(s.N, spg::kTileN[t] / s.mats) * s.zn;
