@@ -1272,13 +1272,17 @@ struct RowVec {
     static constexpr int E = DT == kOutF32 ? 4 : 8;
 };
 
-// One workgroup per row, the row held in registers between the maximum and the rounding
-// (V vectors of 16 bytes a thread); V = 0 reads it twice, for any K.
-template <int DT, int V>
-__global__ void __launch_bounds__(256) quantize_rows(const char* X, int8_t* A, float* scale, int64_t K) {
+// W waves per row (a workgroup has four: one row or four), the row held in registers between
+// the maximum and the rounding (V vectors of 16 bytes a thread); V = 0 reads it twice, for
+// any K.
+template <int DT, int V, int W>
+__global__ void __launch_bounds__(256) quantize_rows(const char* X, int8_t* A, float* scale, int64_t K, int64_t rows) {
+    constexpr int L = W * 64;
+    const int tid = threadIdx.x & (L - 1);
     constexpr int E = RowVec<DT>::E, XB = DT == kOutF32 ? 4 : 2;
-    __shared__ float wmax[4];
-    const int64_t row = blockIdx.x;
+    const int64_t wg = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    const int64_t row = W == 1 ? wg * 4 + (threadIdx.x >> 6) : wg;
+    if (row >= rows) return;                          // whole waves, with W = 4 whole workgroups
     const char* x = X + row * K * XB;
     int8_t* a = A + row * K;
     auto load = [&](int64_t v) -> u32x4 {
@@ -1311,29 +1315,29 @@ __global__ void __launch_bounds__(256) quantize_rows(const char* X, int8_t* A, f
     if constexpr (V > 0) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int64_t v = threadIdx.x + j * 256;
+            const int64_t v = tid + j * L;
             keep[j] = v < nv ? load(v) : u32x4{};
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) take(keep[j]);
     } else {
-        for (int64_t v = threadIdx.x; v < nv; v += 256) take(load(v));
+        for (int64_t v = tid; v < nv; v += L) take(load(v));
     }
 #pragma unroll
     for (int s = 32; s > 0; s >>= 1) {
         const uint32_t o = (uint32_t)__shfl_xor((int)top, s);
         top = o > top ? o : top;
     }
-    if ((threadIdx.x & 63) == 0) wmax[threadIdx.x >> 6] = __builtin_bit_cast(float, top);
-    __syncthreads();
+    if constexpr (W > 1) {
+        __shared__ uint32_t wmax[W];
+        if ((tid & 63) == 0) wmax[tid >> 6] = top;
+        __syncthreads();
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        const uint32_t o = __builtin_bit_cast(uint32_t, wmax[w]);
-        top = o > top ? o : top;
+        for (int w = 0; w < W; ++w) top = wmax[w] > top ? wmax[w] : top;
     }
     float amax = __builtin_bit_cast(float, top);
     const bool finite = top < 0x7f800000u;
-    if (threadIdx.x == 0) scale[row] = amax / 127.0f;
+    if (tid == 0) scale[row] = amax / 127.0f;
     // amax near the ends of the range: scaled so that 127 / amax and 254 x stay inside it
     const float pow = amax < 0x1p-80f ? 0x1p80f : amax > 0x1p80f ? 0x1p-80f : 1.0f;
     amax *= pow;
@@ -1359,11 +1363,11 @@ __global__ void __launch_bounds__(256) quantize_rows(const char* X, int8_t* A, f
     if constexpr (V > 0) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int64_t v = threadIdx.x + j * 256;
+            const int64_t v = tid + j * L;
             if (v < nv) put(v, keep[j]);
         }
     } else {
-        for (int64_t v = threadIdx.x; v < nv; v += 256) put(v, load(v));
+        for (int64_t v = tid; v < nv; v += L) put(v, load(v));
     }
 }
 

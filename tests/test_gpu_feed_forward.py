@@ -380,6 +380,45 @@ def test_quantize_rows(dtype):
             assert a.intact() and s.intact() and xb.intact()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_quantize_rows_of_every_length(dtype):
+    # many short rows (a wave each, the last workgroup not full), and lengths on both sides of
+    # what 2, 4, 8 and 16 vectors of 16 bytes a thread hold
+    torch = _t()
+    dt = _dt(dtype)
+    e = 4 if dtype == "f32" else 8
+    sizes = [(M, K) for M in (2047, 2048, 2049, 2051) for K in (1, 9, 64 * e + 3, 128 * e, 128 * e + 1)]
+    sizes += [(3, v * 256 * e + d) for v in (2, 4, 8, 16) for d in (-1, 0, 1)]
+    for M, K in sizes:
+        for off in (0, 1):
+            gen = _gen(700 + K)
+            x = _normal(gen, (M, K), 1.0)
+            x[1] = 0.0
+            x[M - 1] *= 30.0
+            xb = Buf((M, K), dt, off, x.to(dt))
+            a, s = Buf((M, K), torch.int8, off), Buf((M,), torch.float32)
+            spg.gemm_quantize_rows(xb.t, a.t, s.t)
+            torch.cuda.synchronize()
+            qa, qs = _rounded_rows(xb.t)
+            assert bool((a.t == qa).all()), (M, K, off, int((a.t != qa).sum()))
+            assert bool((s.t == qs).all()), (M, K, off)
+            assert a.intact() and s.intact() and xb.intact()
+
+
+def test_quantize_rows_past_one_grid_dimension():
+    # four rows a workgroup and 2^23 workgroups in the grid's first dimension: the last five rows
+    # are in the next
+    torch = _t()
+    M, K = (1 << 25) + 5, 2
+    x = _normal(_gen(71), (M, K), 1.0).bfloat16()
+    a = torch.full((M, K), 77, dtype=torch.int8, device="cuda")
+    s = torch.full((M,), -1.0, device="cuda")
+    spg.gemm_quantize_rows(x, a, s)
+    for i in range(0, M, 1 << 23):
+        qa, qs = _rounded_rows(x[i:i + (1 << 23)])
+        assert bool((a[i:i + (1 << 23)] == qa).all()) and bool((s[i:i + (1 << 23)] == qs).all()), i
+
+
 def test_quantize_rows_halves_of_fp32():
     # fp32 neighbours of every half: the rounding side is decided exactly
     torch = _t()
