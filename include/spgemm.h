@@ -248,7 +248,7 @@ typedef enum {
     GEMM_ACT_NONE = 0,       /* quantized products only: no gate, one B */
     GEMM_ACT_SILU = 1,       /* x / (1 + exp(-x)) */
     GEMM_ACT_GELU_TANH = 2,  /* the tanh approximation above */
-    GEMM_ACT_RELU = 3        /* max(x, 0) */
+    GEMM_ACT_RELU = 3        /* max(x, 0); NaN stays NaN */
 } gemm_activation;
 
 typedef struct gemm_gated_plan* gemm_gated_handle;

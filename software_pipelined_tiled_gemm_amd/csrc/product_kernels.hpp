@@ -74,7 +74,7 @@ template <int ACT>
 __device__ __forceinline__ float act_t(float x) {
     if constexpr (ACT == kActSilu) return silu(x);
     else if constexpr (ACT == kActGelu) return gelu_tanh(x);
-    else if constexpr (ACT == kActRelu) return relu(x);
+    else if constexpr (ACT == kActRelu) return x <= 0.0f ? 0.0f : x;   // NaN stays NaN
     else return x;
 }
 
@@ -190,8 +190,8 @@ __device__ __forceinline__ void finish4(const AccOf<ET>& s0, const AccOf<ET>& s1
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int c = e < left ? n + e : n;
-            v[e] = (float)s0[e] * (rs * args.sb[0][c]);
-            if constexpr (DUAL) w[e] = (float)s1[e] * (rs * args.sb[1][c]);
+            v[e] = (float)s0[e] * rs * args.sb[0][c];
+            if constexpr (DUAL) w[e] = (float)s1[e] * rs * args.sb[1][c];
         }
     } else {
 #pragma unroll
@@ -864,7 +864,8 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, 
             }
         }
         auto scaled = [&](int bn, int bm, int e) __attribute__((always_inline)) {
-            return (float)acc[bn][bm][e] * (rs[bm] * cs[bn][e]);
+            // in this order: the product of two small scales may leave fp32's range where the result does not
+            return (float)acc[bn][bm][e] * rs[bm] * cs[bn][e];
         };
         with_out(args.out_dtype, [&](auto od) __attribute__((always_inline)) {
             constexpr int OD = decltype(od)::value;
@@ -1182,8 +1183,8 @@ __global__ void __launch_bounds__(256) simple_product(SimpleArgs a) {
 // Written side by side in one [M, 2 np] matrix, np = N rounded up to a whole k-tile and the
 // columns past N zero: rows are 128-byte aligned whatever N is, and both gradients of the
 // weights and the one sum over both segments (dX) read it without masks.  dG and dU are
-// rounded to the operands' type, as the products need them (a relative 2^-9 of each term
-// in bf16, averaged down by the sums).  Bound by memory: 3 reads, 2 writes of M N values.
+// rounded to the operands' type, as the products need them (a relative 2^-8 of each term
+// in bf16 at most, averaged down by the sums).  Bound by memory: 3 reads, 2 writes of M N values.
 template <bool BF16>
 __global__ void __launch_bounds__(256) gated_slopes(const uint16_t* dH, const uint16_t* G, const uint16_t* U,
                                                     uint16_t* D, int M, int N, int np, int act) {
@@ -1216,12 +1217,13 @@ __global__ void __launch_bounds__(256) gated_slopes(const uint16_t* dH, const ui
         const float uv = bits_to_f32((uint16_t)(u[e >> 1] >> sh), BF16);
         float a, sl;
         if (act == kActRelu) {
-            sl = gv > 0.0f ? 1.0f : 0.0f;
-            a = gv > 0.0f ? gv : 0.0f;
+            sl = gv <= 0.0f ? 0.0f : 1.0f;
+            a = gv <= 0.0f ? 0.0f : gv;
         } else {
             float z = gv, dz = 1.0f;
             if (act == kActGelu) {
-                const float g2 = gv * gv;
+                // past |G| = 1e15 s is 0 or 1 and its slope's zero must not meet an infinity
+                const float g2 = __builtin_fminf(gv * gv, 1e30f);
                 z = 1.5957691216f * gv * __builtin_fmaf(0.044715f, g2, 1.0f);
                 dz = 1.5957691216f * __builtin_fmaf(0.134145f, g2, 1.0f);
             }

@@ -165,27 +165,43 @@ def test_gated_forward(size, layout):
         assert all(b.intact() for b in (x, wg, wu, h, g, u))
 
 
-def _check_backward(dh, x, wg, wu, g, u, dx, dwg, dwu, dtype, layout, act):
-    M, K = x.shape
-    N = g.shape[1]
+def _slopes(dh, g, u, dtype, act):
+    """dG and dU, and what the rounded ones may be off by."""
     e, tiny = _half_ulp(dtype), _tiny(dtype)
-    D, X, G, U = dh.double(), x.double(), g.double(), u.double()
-    gd, ud = _as_kn(wg, layout), _as_kn(wu, layout)
-    A, S = _act(G, act), _slope(G, act)
-    dG, dU = D * U * S, D * A
-    # what the rounded dG and dU may be off by
+    D, G, U = dh.double(), g.double(), u.double()
+    dG, dU = D * U * _slope(G, act), D * _act(G, act)
     tg = e * dG.abs() + 1.01 * 2.0 ** -19 * D.abs() * U.abs() * (1 + G.abs()) + tiny
     tu = e * dU.abs() + 1.01 * 2.0 ** -20 * D.abs() * G.abs() + tiny
+    return dG, dU, tg, tu
+
+
+def _check_dx(dh, wg, wu, g, u, dx, dtype, layout, act):
+    N = g.shape[1]
+    e, tiny = _half_ulp(dtype), _tiny(dtype)
+    gd, ud = _as_kn(wg, layout), _as_kn(wu, layout)
+    dG, dU, tg, tu = _slopes(dh, g, u, dtype, act)
     want = dG @ gd.t() + dU @ ud.t()
     tol = e * want.abs() + 1.01 * (tg @ gd.abs().t() + tu @ ud.abs().t()) + tiny
     tol += 2 * N * U32 * ((dG.abs() + tg) @ gd.abs().t() + (dU.abs() + tu) @ ud.abs().t())
     _within(dx, want, tol, "dX")
+
+
+def _check_dw(dh, x, g, u, dwg, dwu, dtype, layout, act):
+    M = x.shape[0]
+    e, tiny = _half_ulp(dtype), _tiny(dtype)
+    X = x.double()
+    dG, dU, tg, tu = _slopes(dh, g, u, dtype, act)
     for name, got, d, t in (("dWg", dwg, dG, tg), ("dWu", dwu, dU, tu)):
         w = X.t() @ d
         tol = e * w.abs() + 1.01 * (X.abs().t() @ t) + M * U32 * (X.abs().t() @ (d.abs() + t)) + tiny
         if layout == "nk":
             w, tol = w.t(), tol.t()
         _within(got, w, tol, name)
+
+
+def _check_backward(dh, x, wg, wu, g, u, dx, dwg, dwu, dtype, layout, act):
+    _check_dx(dh, wg, wu, g, u, dx, dtype, layout, act)
+    _check_dw(dh, x, g, u, dwg, dwu, dtype, layout, act)
 
 
 @pytest.mark.parametrize("layout", ["nk", "kn"])
@@ -263,6 +279,70 @@ def test_gated_infinities_stay_in_their_row_and_column():
             cols = [n for n in range(N) if n not in (7, N - 1)]
             assert bool(ok[rows][:, cols].all()), (layout, M, N, K)
             assert bool(torch.isnan(h[:, 7].float()).all()) and bool(torch.isnan(h[M - 1].float()).all())
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh", "relu"])
+def test_slopes_of_extreme_preactivations(act):
+    # one row and X = 1: dWg and dWu are dG and dU
+    torch = _t()
+    vals = [0.0, -0.0]
+    for v in (1e-38, 1e-20, 1e-3, 0.5, 1.0, 5.0, 20.0, 90.0, 100.0, 1e4, 1e10, 1e19, 2e19, 1e20, 1e30, 3e38):
+        vals += [v, -v]
+    N, K = len(vals), 8
+    g = torch.tensor([vals], dtype=torch.bfloat16, device="cuda")
+    one = torch.ones(1, N, dtype=torch.bfloat16, device="cuda")
+    x = torch.ones(1, K, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(N, K, dtype=torch.bfloat16, device="cuda")
+    dx, dwg, dwu = torch.empty_like(x), torch.empty_like(w), torch.empty_like(w)
+    with spg.Gated(1, N, K, "bf16", "nk", act) as plan:
+        ws = _workspace(plan.workspace_bytes())
+        plan.backward(one, x, w, w, g, one, dx, dwg, dwu, workspace=ws)
+        d = g[0].double()
+        e, tiny = _half_ulp("bf16"), _tiny("bf16")
+        A, S = _act(d, act), _slope(d, act)
+        # fp32 in between: the smallest results may be flushed
+        _within(dwg[:, 0], S, 2 * e * S.abs() + 2.0 ** -19 * (1 + d.abs().clamp(max=100)) + tiny, "dG")
+        _within(dwu[:, 0], A, 2 * e * A.abs() + 2.0 ** -20 * d.abs().clamp(max=100) + 2.0 ** -126, "dU")
+        assert bool((dx == 0).all())
+        g[0, 3] = float("nan")
+        plan.backward(one, x, w, w, g, one, dx, dwg, dwu, workspace=ws)
+        assert bool(torch.isnan(dwu[3]).all()) and bool(torch.isfinite(dwu[:3]).all())
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh", "relu"])
+def test_nan_gates_give_nan(act):
+    torch = _t()
+    for layout in ("nk", "kn"):
+        for M, N, K in ((1, 40, 64), (40, 72, 64), (40, 72, 4), (30, 264, 2048)):
+            x, wg, wu = (b.t for b in _gated_case(M, N, K, "f16", layout, 81))
+            (wg if layout == "nk" else wg.t())[5] = float("nan")
+            h = torch.empty(M, N, dtype=torch.float16, device="cuda")
+            with spg.Gated(M, N, K, "f16", layout, act) as plan:
+                plan(x, wg, wu, h, workspace=_workspace(plan.workspace_bytes()))
+            nan = torch.isnan(h)
+            assert bool(nan[:, 5].all()) and int(nan.sum()) == M, (layout, M, N, K)
+    for M, N, K in ((1, 40, 64), (40, 72, 64), (40, 72, 4), (30, 264, 4096)):
+        a, b = _ints(_gen(82), (M, K)), _ints(_gen(83), (N, K))
+        sa, sb, sn = torch.ones(M, device="cuda"), torch.full((N,), 1e-6, device="cuda"), torch.full((N,), 1e-6, device="cuda")
+        sn[5] = float("nan")
+        c = torch.empty(M, N, device="cuda")
+        with spg.QuantizedGemm(M, N, K, "f32", act) as plan:
+            plan(a, sa, b, sn, c, B2=b, scale_b2=sb, workspace=_workspace(plan.workspace_bytes()))
+        nan = torch.isnan(c)
+        assert bool(nan[:, 5].all()) and int(nan.sum()) == M, (M, N, K)
+
+
+def test_small_scales_whose_product_leaves_the_range():
+    # 1e-30 * 1e-12 is subnormal in fp32, times sums of about 10^6 the results are not
+    torch = _t()
+    for M, N, K in ((3, 40, 640), (40, 72, 640), (40, 72, 12), (30, 264, 8192)):
+        a, b = _ints(_gen(84), (M, K)), _ints(_gen(85), (N, K))
+        sa, sb = torch.full((M,), 1e-30, device="cuda"), torch.full((N,), 1e-12, device="cuda")
+        c = torch.empty(M, N, device="cuda")
+        with spg.QuantizedGemm(M, N, K, "f32") as plan:
+            plan(a, sa, b, sb, c, workspace=_workspace(plan.workspace_bytes()))
+        p = (a.double() @ b.double().t()) * sa.double()[:, None] * sb.double()
+        _within(c, p, 3.01 * U32 * p.abs() + 2.0 ** -149, "C")
 
 
 @pytest.mark.parametrize("layout", ["nk", "kn"])
@@ -449,6 +529,84 @@ def test_quantized_rows_that_are_not_finite():
         plan(a, s, b, sb, c, workspace=_workspace(plan.workspace_bytes()))
     for m in range(6):
         assert bool(torch.isnan(c[m]).all()) if m in (1, 4) else bool(torch.isfinite(c[m]).all())
+
+
+def _big(shape, dtype, seed):
+    torch = _t()
+    t = torch.empty(shape, dtype=dtype, device="cuda").normal_(0.0, 1.0, generator=_gen(seed))
+    assert bool((t[-1] != 0).any()) and bool((t[shape[0] // 2] != 0).any())
+    return t
+
+
+def _some(n):
+    """The first and last indices of n, and some in between on both sides of its middle."""
+    torch = _t()
+    i = list(range(3)) + [n // 3, n // 2 - 1, n // 2, 2 * n // 3] + list(range(n - 70, n))
+    return torch.tensor(sorted({j for j in i if 0 <= j < n}), device="cuda")
+
+
+def test_rows_past_32_bits():
+    # operands of more than 2^32 bytes: many rows of X, many rows of [N,K] weights (streamed
+    # and tiled), long rows of [K,N] weights
+    torch = _t()
+    for M, N, K, layout in ((540000, 40, 4096, "nk"), (9, 1100000, 2048, "nk"), (70, 1100000, 2048, "nk"),
+                            (70, 1100000, 2048, "kn"), (540001, 24, 4097, "nk")):
+        x = _big((M, K), torch.bfloat16, 91)
+        wg, wu = (_big((N, K) if layout == "nk" else (K, N), torch.bfloat16, s) for s in (92, 93))
+        wg *= K ** -0.5
+        wu *= K ** -0.5
+        h = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+        with spg.Gated(M, N, K, "bf16", layout, "silu") as plan:
+            plan(x, wg, wu, h, workspace=_workspace(plan.workspace_bytes()))
+        r, c = _some(M), _some(N)
+        if layout == "nk":
+            _check_forward(x[r], wg[c], wu[c], h[r][:, c], None, None, "bf16", "nk", "silu")
+        else:
+            _check_forward(x[r], wg[:, c], wu[:, c], h[r][:, c], None, None, "bf16", "kn", "silu")
+        del x, wg, wu, h
+        torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("layout", ["nk", "kn"])
+def test_results_past_32_bits(layout):
+    # H, G, U, dH of more than 2^31 elements, dG and dU of more than 2^32
+    torch = _t()
+    M, N, K = 50000, 45000, 64
+    x, wg, wu = (b.t for b in _gated_case(M, N, K, "bf16", layout, 94))
+    h, g, u = (torch.empty(M, N, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    dx, dwg, dwu = torch.empty_like(x), torch.empty_like(wg), torch.empty_like(wu)
+    with spg.Gated(M, N, K, "bf16", layout, "silu") as plan:
+        ws = torch.empty(plan.workspace_bytes(), dtype=torch.uint8, device="cuda")
+        plan(x, wg, wu, h, G=g, U=u, workspace=ws)
+        r, c = _some(M), _some(N)
+        pick = (lambda w: w[c]) if layout == "nk" else (lambda w: w[:, c])
+        _check_forward(x[r], pick(wg), pick(wu), h[r][:, c], g[r][:, c], u[r][:, c], "bf16", layout, "silu")
+        dh = _big((M, N), torch.bfloat16, 95)
+        plan.backward(dh, x, wg, wu, g, u, dx, dwg, dwu, workspace=ws)
+    # dX of some rows, and the weights' gradients of some columns
+    _check_dx(dh[r], wg, wu, g[r], u[r], dx[r], "bf16", layout, "silu")
+    _check_dw(dh[:, c], x, g[:, c], u[:, c], pick(dwg), pick(dwu), "bf16", layout, "silu")
+
+
+def test_int8_rows_past_32_bits():
+    torch = _t()
+    for M, N, K in ((70000, 40, 65537), (40, 70000, 65540), (9, 70000, 65540)):
+        x = _big((M, K), torch.bfloat16, 96)
+        a, sa = torch.empty(M, K, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+        spg.gemm_quantize_rows(x, a, sa)
+        r, c = _some(M), _some(N)
+        qa, qs = _rounded_rows(x[r])
+        assert bool((a[r] == qa).all()) and bool((sa[r] == qs).all())
+        del x
+        b = torch.randint(-128, 128, (N, K), generator=_gen(97), device="cuda", dtype=torch.int8)
+        sb = torch.full((N,), 1e-4, device="cuda")
+        y = torch.empty(M, N, device="cuda")
+        with spg.QuantizedGemm(M, N, K, "f32") as plan:
+            plan(a, sa, b, sb, y, workspace=_workspace(plan.workspace_bytes()))
+        p = (a[r].double() @ b[c].double().t()) * sa[r].double()[:, None] * sb[c].double()
+        _within(y[r][:, c], p, 3.01 * U32 * p.abs(), "C")
+        del a, b, y
+        torch.cuda.empty_cache()
 
 
 def test_other_stream_and_graph_replays():
