@@ -259,20 +259,18 @@ int64_t set_grid(ProductArgs& a, const Shape& s, int tile, int split, int64_t kt
 }
 
 // The sum of a split reduction's parts.
+template <int ET, bool DUAL>
+void launch_sum(int64_t quads, const ProductArgs& a, hipStream_t st) {
+    if (a.split > 8) hipLaunchKernelGGL((spg::sum_parts<ET, DUAL, 4>), dim3((unsigned)ceil_div(quads, 64)), dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((spg::sum_parts<ET, DUAL, 1>), dim3((unsigned)ceil_div(quads, 256)), dim3(256), 0, st, a);
+}
+
 gemm_status run_sum(int et, const Shape& s, const ProductArgs& a, hipStream_t st) {
     const int64_t quads = s.M * s.zm * (up(s.N, 4) / 4) * s.zn;
-    const dim3 grid((unsigned)ceil_div(quads, 256));
     const bool dual = s.mats == 2;
-    if (et == spg::kElI8) {
-        if (dual) hipLaunchKernelGGL((spg::sum_parts<spg::kElI8, true>), grid, dim3(256), 0, st, a);
-        else hipLaunchKernelGGL((spg::sum_parts<spg::kElI8, false>), grid, dim3(256), 0, st, a);
-    } else if (et == spg::kElBF16) {
-        if (dual) hipLaunchKernelGGL((spg::sum_parts<spg::kElBF16, true>), grid, dim3(256), 0, st, a);
-        else hipLaunchKernelGGL((spg::sum_parts<spg::kElBF16, false>), grid, dim3(256), 0, st, a);
-    } else {
-        if (dual) hipLaunchKernelGGL((spg::sum_parts<spg::kElF16, true>), grid, dim3(256), 0, st, a);
-        else hipLaunchKernelGGL((spg::sum_parts<spg::kElF16, false>), grid, dim3(256), 0, st, a);
-    }
+    if (et == spg::kElI8) dual ? launch_sum<spg::kElI8, true>(quads, a, st) : launch_sum<spg::kElI8, false>(quads, a, st);
+    else if (et == spg::kElBF16) dual ? launch_sum<spg::kElBF16, true>(quads, a, st) : launch_sum<spg::kElBF16, false>(quads, a, st);
+    else dual ? launch_sum<spg::kElF16, true>(quads, a, st) : launch_sum<spg::kElF16, false>(quads, a, st);
     return launched();
 }
 

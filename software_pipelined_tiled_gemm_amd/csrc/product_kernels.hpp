@@ -1099,38 +1099,56 @@ __global__ void __launch_bounds__(256) pack_rows(PackArgs a) {
 // the sum over the parts of a split reduction
 // ---------------------------------------------------------------------------
 //
-// Part sums are row-major [split][zm M][ldp]; a thread adds 4 consecutive columns over the
-// parts in order (so the result does not depend on timing) and applies the epilogue.
-template <int ET, bool DUAL>
+// Part sums are row-major [split][zm M][ldp]; a thread adds 4 consecutive columns over every
+// W-th part, and the W waves' sums meet in LDS, in an order that does not depend on timing;
+// then the epilogue.  Bound by the loads' latency, other XCDs having written the parts: eight
+// are in flight, and with more parts than that four waves share them.
+template <int ET, bool DUAL, int W>
 __global__ void __launch_bounds__(256) sum_parts(ProductArgs args) {
     const int np4 = (args.N + 3) & ~3;
     const int quads = np4 / 4 * args.zn;
     const int64_t rows = (int64_t)args.M * args.zm;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= rows * quads) return;
-    int64_t m = i / quads;
-    int n = (int)(i - m * quads) * 4;
+    const int lane = W == 1 ? threadIdx.x : threadIdx.x & 63;
+    const int first = W == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t i = (int64_t)blockIdx.x * (256 / W) + lane;
+    const bool in = i < rows * quads;
+    int64_t m = in ? i / quads : 0;
+    int n = in ? (int)(i - m * quads) * 4 : 0;
     const int64_t ldp = part_pitch(args, DUAL);
-    const AccOf<ET>* p = (const AccOf<ET>*)(args.part + (size_t)m * ldp + n);
     const size_t step = (size_t)rows * ldp / 4;
-    AccOf<ET> s0 = p[0], s1 = s0;
-    if constexpr (DUAL) s1 = p[np4 / 4];
-    // eight parts' loads in flight at a time, added in order
-    for (int k = 1; k < args.split; k += 8) {
+    const AccOf<ET>* p = (const AccOf<ET>*)(args.part + (size_t)m * ldp + n);
+    AccOf<ET> s0 = p[first * step], s1 = s0;
+    if constexpr (DUAL) s1 = p[first * step + np4 / 4];
+    for (int k = first + W; k < args.split; k += 8 * W) {
         AccOf<ET> v[8], w[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int q = k + j < args.split ? k + j : k;
+            const int q = k + j * W < args.split ? k + j * W : k;
             v[j] = p[q * step];
             if constexpr (DUAL) w[j] = p[q * step + np4 / 4];
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (k + j < args.split) {
+            if (k + j * W < args.split) {
                 s0 += v[j];
                 if constexpr (DUAL) s1 += w[j];
             }
     }
+    if constexpr (W > 1) {
+        __shared__ AccOf<ET> sums[W - 1][DUAL ? 2 : 1][64];
+        if (first > 0) {
+            sums[first - 1][0][lane] = s0;
+            if constexpr (DUAL) sums[first - 1][1][lane] = s1;
+        }
+        __syncthreads();
+        if (first > 0) return;
+#pragma unroll
+        for (int w = 0; w < W - 1; ++w) {
+            s0 += sums[w][0][lane];
+            if constexpr (DUAL) s1 += sums[w][1][lane];
+        }
+    }
+    if (!in) return;
     int z = 0;
     if (m >= args.M) { m -= args.M; z = 1; }
     if (n >= np4) { n -= np4; z = 1; }
