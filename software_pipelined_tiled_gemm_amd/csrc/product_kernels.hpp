@@ -18,6 +18,7 @@
 #pragma once
 
 #include "gemm_kernels.hpp"
+#include "tile_copy.hpp"
 
 namespace spg {
 
@@ -378,6 +379,10 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, 
     const int nk = (kt1 - kt0 + KG - 1) / KG;         // k-tiles of this part a group takes (>= 1)
     auto kt_of = [&](int t) { return kt0 + t * KG + kg; };
     const int tail = K * ES - (seg_kt - 1) * 128;     // bytes of a segment's last k-tile
+    // SEG: A is dG and dU, padded to whole k-tiles
+    using RowsA = RowCopy<REG, SEG>;
+    using RowsB = RowCopy<REG, false>;
+    using Columns = ColumnCopy<REG>;
     // bytes of a K-contiguous row that may be read: whole words for direct copies (rows of
     // whole words, or laid out again and padded with zeros)
     const uint32_t row_bytes = REG ? (uint32_t)(K * ES) : ((uint32_t)(K * ES) + 3u) & ~3u;
@@ -391,43 +396,33 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, 
     const char* b_mine = up ? b_ptr1 : b_ptr0;
     const int a_rows = M - m0 < BM ? M - m0 : BM;
     const int b_rows = N - n0 < BNS ? N - n0 : BNS;
-    struct Win { uint64_t p; uint32_t n; };
-    // REG: the chunk that straddles K is loaded from the 16 bytes that end at K, which may
-    // begin before the k-tile: the resource of K-contiguous rows starts 16 bytes early
-    constexpr uint32_t kBack = REG ? 16u : 0u;
     // Start and size of an operand's resource for a k-tile (0 past this part's last one: reads
     // zero).  K-contiguous rows: 128 bytes further per k-tile, up to the end of the tile's
     // last row.  Reduction-major: 64 rows further, as many of them as exist; columns past the
-    // last are masked by offset.  Written as selects: a branch here would cut the k-step that
-    // carries the copies in two.
+    // last are masked by offset.
     const uint32_t lda = args.lda, ldb = args.ldb;
-    const uint64_t a_at = (uint64_t)(uintptr_t)a_ptr + (A_T ? 0 : (uint64_t)m0 * lda - kBack);
-    const uint64_t b_at[2] = {(uint64_t)(uintptr_t)b_mine + (B_N ? 0 : (uint64_t)n0 * ldb - kBack),
-                              (uint64_t)(uintptr_t)(SEG ? b_ptr1 : b_mine) + (B_N ? 0 : (uint64_t)n0 * ldb - kBack)};
-    const uint32_t a_all = (uint32_t)(a_rows - 1) * lda + (SEG ? lda : row_bytes) + kBack;
-    const uint32_t b_all = (uint32_t)(b_rows - 1) * ldb + row_bytes + kBack;
-    auto tr_win = [&](uint64_t p, uint32_t ld, int k, bool in) __attribute__((always_inline)) -> Win {
-        const int left = K - k * 64;
-        int rows = left < 64 ? left : 64;
-        rows = in ? rows : 0;
-        return Win{p + (uint64_t)(uint32_t)(k * 64) * ld, (uint32_t)rows * ld};
-    };
+    const uint64_t a_at = (uint64_t)(uintptr_t)a_ptr + (A_T ? 0 : (uint64_t)m0 * lda - RowsA::kBack);
+    const uint64_t b_at[2] = {(uint64_t)(uintptr_t)b_mine + (B_N ? 0 : (uint64_t)n0 * ldb - RowsB::kBack),
+                              (uint64_t)(uintptr_t)(SEG ? b_ptr1 : b_mine) + (B_N ? 0 : (uint64_t)n0 * ldb - RowsB::kBack)};
+    const uint32_t a_all = (uint32_t)(a_rows - 1) * lda + (SEG ? lda : row_bytes) + RowsA::kBack;
+    const uint32_t b_all = (uint32_t)(b_rows - 1) * ldb + row_bytes + RowsB::kBack;
     auto a_win = [&](int kt) __attribute__((always_inline)) -> Win {
-        if constexpr (A_T) return tr_win(a_at, lda, kt, kt < kt1);
-        else return Win{a_at + (uint32_t)kt * 128u, kt < kt1 ? a_all - (uint32_t)kt * 128u : 0u};
+        if constexpr (A_T) return Columns::window(a_at, lda, K, kt, kt < kt1);
+        else return RowsA::window(a_at, a_all, kt, kt < kt1);
     };
     auto b_win = [&](int kt) __attribute__((always_inline)) -> Win {
         const bool second = SEG && kt >= seg_kt;
         const int k = second ? kt - seg_kt : kt;
         const uint64_t p = second ? b_at[1] : b_at[0];
-        if constexpr (B_N) return tr_win(p, ldb, k, kt < kt1);
-        else return Win{p + (uint32_t)k * 128u, kt < kt1 ? b_all - (uint32_t)k * 128u : 0u};
+        if constexpr (B_N) return Columns::window(p, ldb, K, k, kt < kt1);
+        else return RowsB::window(p, b_all, k, kt < kt1);
     };
     // bytes of a K-contiguous row's part of k-tile kt that exist
-    auto klim = [&](int kt) __attribute__((always_inline)) -> int {
+    auto lim_a = [&](int kt) __attribute__((always_inline)) -> int { return RowsA::limit(kt, seg_kt, tail); };
+    auto lim_b = [&](int kt) __attribute__((always_inline)) -> int {
         int k = kt;
         if constexpr (SEG) k = kt >= seg_kt ? kt - seg_kt : kt;
-        return k == seg_kt - 1 ? tail : 128;
+        return RowsB::limit(k, seg_kt, tail);
     };
 
     // ---- per-lane copy offsets: op j writes 1 KiB of the slot, lane i 16 bytes at 16 i ----
@@ -444,8 +439,8 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, 
     if (DUAL && firstB >= BNS / 8) firstB -= BNS / 8;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        kcA[h] = (uint32_t)((firstA + h) * 8 + lane / 8) * args.lda + (uint32_t)kc_pos(firstA + h) + kBack;
-        kcB[h] = (uint32_t)((firstB + h) * 8 + lane / 8) * args.ldb + (uint32_t)kc_pos(firstB + h) + kBack;
+        kcA[h] = (uint32_t)((firstA + h) * 8 + lane / 8) * args.lda + (uint32_t)kc_pos(firstA + h) + RowsA::kBack;
+        kcB[h] = (uint32_t)((firstB + h) * 8 + lane / 8) * args.ldb + (uint32_t)kc_pos(firstB + h) + RowsB::kBack;
     }
     const int posA = kc_pos(firstA), posB = kc_pos(firstB);
     // reduction-major: op d holds 64 / CPR rows; over: columns of the chunk past the last
@@ -455,13 +450,8 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, 
                       __attribute__((always_inline)) {
         constexpr int CPR = decltype(cpr_c)::value, RP = 64 / CPR;
         const int r = d * RP + lane / CPR, c = (lane % CPR) ^ nswz_t<CPR>(r);
-        over = col0 + c * 8 + 8 - cols;
-        off = (uint32_t)r * (uint32_t)ld + (uint32_t)(col0 + c * 8) * 2u;
-        // columns past the last of a chunk: REG loads the 16 bytes that end at the last column
-        // (and shifts them); a direct copy takes what follows, the next row's first columns
-        // or zeros past the end, which only reach results that are not stored
-        if (over >= 8) off = kOOB;
-        else if (REG && over > 0) off -= 2u * (uint32_t)over;
+        over = Columns::over(col0 + c * 8, cols);
+        off = Columns::offset(r, (uint32_t)ld, col0 + c * 8, over);
     };
     if constexpr (A_T) {
 #pragma unroll
@@ -474,37 +464,27 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, 
             tr_off(std::integral_constant<int, BNS / 8>{}, firstB + j, n0, args.ldb, args.b_cols, trB[j], overB[j]);
     }
     // offset of op j for a k-tile of which `lim` bytes exist along a K-contiguous row
-    auto kc_off = [&](uint32_t off, int pos, int lim) __attribute__((always_inline)) -> uint32_t {
-        if constexpr (REG) off -= pos + 16 > lim ? (uint32_t)(pos + 16 - lim) : 0u;
-        return pos >= lim ? kOOB : off;
-    };
     auto src_off = [&](auto jc, int lim) __attribute__((always_inline)) -> uint32_t {
         constexpr int j = decltype(jc)::value;
         if constexpr (j < A_OPS) {
             if constexpr (A_T) return trA[j];
-            else return kc_off(kcA[j & 1] + (uint32_t)(j >> 1) * 16u * args.lda, posA ^ ((j & 1) * 64), lim);
+            else return RowsA::offset(kcA[j & 1] + (uint32_t)(j >> 1) * 16u * args.lda, posA ^ ((j & 1) * 64), lim);
         } else {
             constexpr int i = j - A_OPS;
             if constexpr (B_N) return trB[i];
-            else return kc_off(kcB[i & 1] + (uint32_t)(i >> 1) * 16u * args.ldb, posB ^ ((i & 1) * 64), lim);
+            else return RowsB::offset(kcB[i & 1] + (uint32_t)(i >> 1) * 16u * args.ldb, posB ^ ((i & 1) * 64), lim);
         }
     };
     // REG: bits to shift the loaded chunk down by
-    auto kc_shift = [&](int pos, int lim) __attribute__((always_inline)) -> uint32_t {
-        return pos < lim && pos + 16 > lim ? 8u * (uint32_t)(pos + 16 - lim) : 0u;
-    };
-    auto tr_shift = [&](int over) __attribute__((always_inline)) -> uint32_t {
-        return over > 0 && over < 8 ? 16u * (uint32_t)over : 0u;
-    };
     auto src_shift = [&](auto jc, int lim) __attribute__((always_inline)) -> uint32_t {
         constexpr int j = decltype(jc)::value;
         if constexpr (j < A_OPS) {
-            if constexpr (A_T) return tr_shift(overA[j]);
-            else return kc_shift(posA ^ ((j & 1) * 64), lim);
+            if constexpr (A_T) return Columns::shift(overA[j]);
+            else return RowsA::shift(posA ^ ((j & 1) * 64), lim);
         } else {
             constexpr int i = j - A_OPS;
-            if constexpr (B_N) return tr_shift(overB[i]);
-            else return kc_shift(posB ^ ((i & 1) * 64), lim);
+            if constexpr (B_N) return Columns::shift(overB[i]);
+            else return RowsB::shift(posB ^ ((i & 1) * 64), lim);
         }
     };
     auto lds_dst = [&](const Slot& s, auto jc) __attribute__((always_inline)) -> SPG_LDS char* {
@@ -516,18 +496,18 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, 
     auto src_ab = [&](int kta, int ktb) __attribute__((always_inline)) -> Src {
         const Win a = a_win(kta), b = b_win(ktb);
         return Src{make_rsrc((const void*)(uintptr_t)a.p, a.n), make_rsrc((const void*)(uintptr_t)b.p, b.n),
-                   klim(kta), klim(ktb)};
+                   lim_a(kta), lim_b(ktb)};
     };
     auto dma_op = [&](const Slot& s, const Src& src, auto jc) __attribute__((always_inline)) {
         constexpr bool ISA = decltype(jc)::value < A_OPS;
         dma16(ISA ? src.a : src.b, lds_dst(s, jc), src_off(jc, ISA ? src.lim_a : src.lim_b));
     };
-    // A K-contiguous row's last chunk of a segment that ends inside it: what follows K there
+    // A K-contiguous row's last chunk of a segment that ends inside it (dG and dU end in zeros): what follows K there
     // is the next row's and is cleared in LDS, by the lane that copied it, once this wave's
     // copies of the k-tile have landed and before the barrier that publishes it.
     auto clear_tail = [&](const Slot& s, int kt) __attribute__((always_inline)) {
-        if constexpr (TAIL && !REG && (!A_T || !B_N)) {
-            const int lim = klim(kt);
+        if constexpr (TAIL && !REG && ((!A_T && !SEG) || !B_N)) {
+            const int lim = lim_b(kt);
             if ((lim & 15) == 0) return;
             // loops, not unrolled: the code stands behind every k-tile of the unrolled pattern
             auto clear = [&](SPG_LDS char* at, int ops, int pos) __attribute__((always_inline)) {
@@ -539,7 +519,7 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, 
                     }
                 }
             };
-            if constexpr (!A_T) clear(s.a + firstA * 1024, A_OPS, posA);
+            if constexpr (!A_T && !SEG) clear(s.a + firstA * 1024, A_OPS, posA);
             if constexpr (!B_N) clear(s.b + wave * B_OPS * 1024, B_OPS, posB);
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         }
@@ -564,21 +544,21 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, 
         constexpr int p = decltype(pc)::value % PD;
         const Win a = a_win(kt), b = b_win(kt);
         const auto ra = make_rsrc_b((const void*)(uintptr_t)a.p, a.n), rb = make_rsrc_b((const void*)(uintptr_t)b.p, b.n);
-        const int lim = klim(kt);
+        const int lb = lim_b(kt), la = SEG ? lim_a(kt) : lb;
         static_for<0, L>([&](auto jc) {
             constexpr int j = decltype(jc)::value;
-            staged[p][j] = __builtin_amdgcn_raw_buffer_load_b128(j < A_OPS ? ra : rb, (int)src_off(jc, lim), 0, 0);
+            staged[p][j] = __builtin_amdgcn_raw_buffer_load_b128(j < A_OPS ? ra : rb, (int)src_off(jc, j < A_OPS ? la : lb), 0, 0);
         });
     };
     // columns past the last reach into this workgroup's tile
     const bool cut = (A_T && m0 + BM > args.a_cols) || (B_N && n0 + BNS > args.b_cols);
     auto lwrite = [&](const Slot& s, auto pc, int kt) __attribute__((always_inline)) {
         constexpr int p = decltype(pc)::value % PD;
-        const int lim = klim(kt);
+        const int lb = lim_b(kt), la = SEG ? lim_a(kt) : lb;
         // only the last k-tile and the last column tile have chunks to realign: a 128-bit
         // shift by a lane's own amount is about 20 instructions, and doing it for every
         // chunk took longer than the multiplications of the small tiles
-        if (lim == 128 && !cut) {
+        if (lb == 128 && !cut) {
             static_for<0, L>([&](auto jc) {
                 *(SPG_LDS u32x4*)(lds_dst(s, jc) + lane * 16) = staged[p][decltype(jc)::value];
             });
@@ -586,7 +566,7 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, 
         }
         static_for<0, L>([&](auto jc) {
             constexpr int j = decltype(jc)::value;
-            *(SPG_LDS u32x4*)(lds_dst(s, jc) + lane * 16) = shr128(staged[p][j], src_shift(jc, lim));
+            *(SPG_LDS u32x4*)(lds_dst(s, jc) + lane * 16) = shr128(staged[p][j], src_shift(jc, j < A_OPS ? la : lb));
         });
     };
 

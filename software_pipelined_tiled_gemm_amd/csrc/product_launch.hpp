@@ -53,7 +53,8 @@ void launch_kernel(const ProductArgs& a, dim3 grid, hipStream_t st) {
 template <int ET, int P, bool REG, int BM, int BN, int WM, int WN, int S, bool DEEP, int KG, int WPS = 1>
 void launch_tile(const ProductArgs& a, dim3 grid, hipStream_t st) {
     constexpr int ES = ET == kElI8 ? 1 : 2;
-    if constexpr (P == kGradW) {
+    if constexpr (P == kGradW || P == kGradXNK) {
+        // no operand's rows end inside a chunk: both across the reduction, or dG and dU padded
         launch_kernel<ET, P, REG, BM, BN, WM, WN, S, DEEP, KG, false, WPS>(a, grid, st);
     } else if constexpr (BM == 256 && !REG) {
         if (a.K * ES % 16 == 0) launch_kernel<ET, P, REG, BM, BN, WM, WN, S, DEEP, KG, false, WPS>(a, grid, st);
