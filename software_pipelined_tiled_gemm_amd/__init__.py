@@ -282,17 +282,17 @@ def gemm_gated_workspace(handle: int) -> int:
 
 def gemm_gated_run(handle: int, X, Wg, Wu, H, G=None, U=None, workspace=None,
                    workspace_bytes: Optional[int] = None, stream=None) -> None:
+    ws = _scratch("gemm_gated_run", workspace, workspace_bytes)
     st = lib().gemm_gated_run(handle, _ptr(X), _ptr(Wg), _ptr(Wu), _ptr(H), _ptr(G), _ptr(U),
-                              _ptr(workspace), _nbytes(workspace, workspace_bytes),
-                              _stream(stream, X, H))
+                              *ws, _stream(stream, X, H))
     _check(st, "gemm_gated_run")
 
 
 def gemm_gated_backward(handle: int, dH, X, Wg, Wu, G, U, dX, dWg, dWu, workspace=None,
                         workspace_bytes: Optional[int] = None, stream=None) -> None:
+    ws = _scratch("gemm_gated_backward", workspace, workspace_bytes)
     st = lib().gemm_gated_backward(handle, _ptr(dH), _ptr(X), _ptr(Wg), _ptr(Wu), _ptr(G), _ptr(U),
-                                   _ptr(dX), _ptr(dWg), _ptr(dWu), _ptr(workspace),
-                                   _nbytes(workspace, workspace_bytes), _stream(stream, dH, X, dX))
+                                   _ptr(dX), _ptr(dWg), _ptr(dWu), *ws, _stream(stream, dH, X, dX))
     _check(st, "gemm_gated_backward")
 
 
@@ -313,9 +313,9 @@ def gemm_quantized_workspace(handle: int) -> int:
 
 def gemm_quantized_run(handle: int, A, scale_a, B, scale_b, C, B2=None, scale_b2=None, workspace=None,
                        workspace_bytes: Optional[int] = None, stream=None) -> None:
+    ws = _scratch("gemm_quantized_run", workspace, workspace_bytes)
     st = lib().gemm_quantized_run(handle, _ptr(A), _ptr(scale_a), _ptr(B), _ptr(scale_b), _ptr(B2),
-                                  _ptr(scale_b2), _ptr(C), _ptr(workspace),
-                                  _nbytes(workspace, workspace_bytes), _stream(stream, A, C))
+                                  _ptr(scale_b2), _ptr(C), *ws, _stream(stream, A, C))
     _check(st, "gemm_quantized_run")
 
 
@@ -351,12 +351,20 @@ def gemm_quantize_rows(X, A, scale, stream=None, dtype: Optional[str] = None,
         _check(st, "gemm_quantize_rows")
 
 
-def _nbytes(workspace, given: Optional[int]) -> int:
-    if given is not None:
-        return given
+def _scratch(what: str, workspace, given: Optional[int] = None, device: Optional[int] = None) -> tuple:
+    """Pointer and bytes of a workspace.  A tensor has to be dense memory of the operands' GPU
+    (`device`, where they tell): the kernels write as many bytes as its size promises."""
     if workspace is None or isinstance(workspace, int):
-        return 0
-    return workspace.nbytes
+        return workspace, given or 0
+    if not workspace.is_contiguous():
+        raise GemmError(1, f"{what}: workspace is not contiguous")
+    if not workspace.is_cuda:
+        raise GemmError(1, f"{what}: workspace is not on a GPU")
+    if device is not None and workspace.get_device() != device:
+        raise GemmError(1, f"{what}: workspace is on another device")
+    if given is not None and given > workspace.nbytes:
+        raise GemmError(1, f"{what}: workspace has {workspace.nbytes} bytes, not {given}")
+    return workspace.data_ptr(), workspace.nbytes if given is None else given
 
 
 _names = _types = None
@@ -525,7 +533,7 @@ class Gated:
         d, x, w, h = self._type, self._x, self._w, self._h
         dev, p = _dense("Gated", ("X", X, d, x), ("Wg", Wg, d, w), ("Wu", Wu, d, w), ("H", H, d, h),
                         ("G", G, d, h), ("U", U, d, h))
-        st = self._run(self.handle, *p, _ptr(workspace), _nbytes(workspace, None), _stream_on(stream, dev))
+        st = self._run(self.handle, *p, *_scratch("Gated", workspace, device=dev), _stream_on(stream, dev))
         if st:
             _check(st, "gemm_gated_run")
         return H
@@ -542,7 +550,7 @@ class Gated:
         dev, p = _dense("Gated.backward", ("dH", dH, d, h), ("X", X, d, x), ("Wg", Wg, d, w),
                         ("Wu", Wu, d, w), ("G", G, d, h), ("U", U, d, h), ("dX", dX, d, x),
                         ("dWg", dWg, d, w), ("dWu", dWu, d, w))
-        st = self._back(self.handle, *p, _ptr(workspace), _nbytes(workspace, None), _stream_on(stream, dev))
+        st = self._back(self.handle, *p, *_scratch("Gated.backward", workspace, device=dev), _stream_on(stream, dev))
         if st:
             _check(st, "gemm_gated_backward")
         return dX, dWg, dWu
@@ -598,7 +606,7 @@ class QuantizedGemm:
         dev, p = _dense("QuantizedGemm", ("A", A, i8, self._a), ("scale_a", scale_a, f32, m), ("B", B, i8, b),
                         ("scale_b", scale_b, f32, n), ("B2", B2, i8, b), ("scale_b2", scale_b2, f32, n),
                         ("C", C, self._out, self._c))
-        st = self._run(self.handle, *p, _ptr(workspace), _nbytes(workspace, None), _stream_on(stream, dev))
+        st = self._run(self.handle, *p, *_scratch("QuantizedGemm", workspace, device=dev), _stream_on(stream, dev))
         if st:
             _check(st, "gemm_quantized_run")
         return C

@@ -1,0 +1,128 @@
+"""What the Python wrappers of the feed-forward operators pass on and what they refuse, with the
+C entry points replaced by recorders: nothing is launched, no GPU is needed."""
+
+import pytest
+
+import software_pipelined_tiled_gemm_amd as spg
+
+torch = pytest.importorskip("torch")
+
+P = 1 << 20      # a raw device pointer
+
+
+class Recorder:
+    """Stands for a C entry point: keeps the arguments, succeeds."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __call__(self, *args):
+        self.calls.append(args)
+        return 0
+
+
+class OnDevice:
+    """The attributes of a dense uint8 device tensor that the wrappers read."""
+
+    dtype, is_cuda = torch.uint8, True
+
+    def __init__(self, n, device=0):
+        self.shape, self.nbytes, self.device = (n,), n, device
+
+    def get_device(self):
+        return self.device
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return P
+
+
+class Like(OnDevice):
+    """... of an operand."""
+
+    def __init__(self, shape, dtype, device=0):
+        self.shape, self.dtype, self.device = torch.Size(shape), dtype, device
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    """The library with recorders in place of the entry points that launch, behind the Python
+    call path."""
+    real = spg.lib()
+
+    class Lib:
+        def __getattr__(self, name):
+            return getattr(real, name)
+
+    fake = Lib()
+    for name in ("gemm_gated_run", "gemm_gated_backward", "gemm_quantized_run", "gemm_quantize_rows"):
+        setattr(fake, name, Recorder())
+    monkeypatch.setattr(spg, "_lib", fake)
+    monkeypatch.setattr(spg, "_calls", None)
+    monkeypatch.setattr(spg, "_address", lambda fn: 0)
+    return fake
+
+
+M, N, K = 96, 256, 8192
+
+
+def calls(lib):
+    """(entry point, call with a workspace) of every operator that takes one: the classes, then
+    the functions of the entry points' names."""
+    gated, q = spg.Gated(M, N, K), spg.QuantizedGemm(M, N, K)
+    return [
+        (lib.gemm_gated_run, gated.workspace_bytes(), lambda **kw: gated(P, P, P, P, stream=0, **kw)),
+        (lib.gemm_gated_backward, gated.workspace_bytes(), lambda **kw: gated.backward(*[P] * 9, stream=0, **kw)),
+        (lib.gemm_quantized_run, q.workspace_bytes(), lambda **kw: q(P, P, P, P, P, stream=0, **kw)),
+        (lib.gemm_gated_run, gated.workspace_bytes(),
+         lambda **kw: spg.gemm_gated_run(gated.handle, P, P, P, P, stream=0, **kw)),
+        (lib.gemm_gated_backward, gated.workspace_bytes(),
+         lambda **kw: spg.gemm_gated_backward(gated.handle, *[P] * 9, stream=0, **kw)),
+        (lib.gemm_quantized_run, q.workspace_bytes(),
+         lambda **kw: spg.gemm_quantized_run(q.handle, P, P, P, P, P, stream=0, **kw)),
+    ]
+
+
+@pytest.mark.parametrize("which", range(6))
+def test_workspaces_that_the_kernels_could_not_write(lib, which):
+    fn, n, call = calls(lib)[which]
+    assert n > 0
+    for bad, why in ((torch.empty(n, dtype=torch.uint8), "not on a GPU"),
+                     (torch.empty(1, dtype=torch.uint8).expand(n), "not contiguous"),
+                     (torch.empty(2 * n, dtype=torch.uint8)[::2], "not contiguous")):
+        with pytest.raises(spg.GemmError, match="workspace is " + why) as e:
+            call(workspace=bad)
+        assert e.value.status == 1 and not fn.calls
+    call(workspace=OnDevice(n))
+    call(workspace=None)
+    assert [c[-3:-1] for c in fn.calls] == [(P, n), (None, 0)]
+
+
+def test_a_size_beyond_the_workspace(lib):
+    for fn, n, call in calls(lib)[3:]:
+        with pytest.raises(spg.GemmError, match="workspace has") as e:
+            call(workspace=OnDevice(n), workspace_bytes=n + 1)
+        assert e.value.status == 1 and not fn.calls
+        call(workspace=OnDevice(n + 16), workspace_bytes=n)
+        call(workspace=P, workspace_bytes=n)
+        assert [c[-3:-1] for c in fn.calls] == [(P, n), (P, n)]
+        fn.calls.clear()
+
+
+def test_a_workspace_on_another_device(lib):
+    b, i8, f32 = torch.bfloat16, torch.int8, torch.float32
+    x, w, h = Like((M, K), b), Like((N, K), b), Like((M, N), b)
+    with spg.Gated(M, N, K) as plan, spg.QuantizedGemm(M, N, K) as q:
+        for fn, n, call in (
+                (lib.gemm_gated_run, plan.workspace_bytes(), lambda ws: plan(x, w, w, h, workspace=ws, stream=0)),
+                (lib.gemm_gated_backward, plan.workspace_bytes(),
+                 lambda ws: plan.backward(h, x, w, w, h, h, x, w, w, workspace=ws, stream=0)),
+                (lib.gemm_quantized_run, q.workspace_bytes(),
+                 lambda ws: q(Like((M, K), i8), Like((M,), f32), Like((N, K), i8), Like((N,), f32), h, workspace=ws, stream=0))):
+            with pytest.raises(spg.GemmError, match="workspace is on another device"):
+                call(OnDevice(n, device=1))
+            assert not fn.calls
+            call(OnDevice(n))
+            assert len(fn.calls) == 1

@@ -733,3 +733,29 @@ def test_example_block_trains_and_serves():
     losses, err = feed_forward.main(tokens=96, model=136, hidden=264, steps=6, rate=0.2)
     assert all(b < a for a, b in zip(losses, losses[1:])), losses
     assert 0.0 < err < 0.05, err
+
+
+def test_workspaces_are_checked_on_both_call_paths(monkeypatch):
+    # refusals before any launch; only the workspace is wrong
+    torch = _t()
+    M, N, K = 96, 256, 8192
+    x, wg, wu = (b.t for b in _gated_case(M, N, K, "bf16", "nk", 101))
+    h = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    a8, sa = _ints(_gen(102), (M, K)), torch.ones(M, device="cuda")
+    b8, sb, c = _ints(_gen(103), (N, K)), torch.ones(N, device="cuda"), torch.zeros(M, N, device="cuda")
+    for compiled in (True, False):
+        if not compiled:
+            monkeypatch.setattr(spg, "_calls", None)
+        with spg.Gated(M, N, K, "bf16", "nk", "silu") as plan, spg.QuantizedGemm(M, N, K, "f32") as q:
+            n = max(plan.workspace_bytes(), q.workspace_bytes())
+            for bad in (torch.empty(n, dtype=torch.uint8), torch.empty(1, dtype=torch.uint8, device="cuda").expand(n),
+                        torch.empty(2 * n, dtype=torch.uint8, device="cuda")[::2],
+                        torch.empty(16, dtype=torch.uint8, device="cuda"), None):
+                for call in (lambda: plan(x, wg, wu, h, workspace=bad),
+                             lambda: plan.backward(h, x, wg, wu, h, h, x, wg, wu, workspace=bad),
+                             lambda: q(a8, sa, b8, sb, c, workspace=bad)):
+                    with pytest.raises(spg.GemmError) as e:
+                        call()
+                    assert e.value.status == 1
+    torch.cuda.synchronize()
+    assert not bool(h.any()) and not bool(c.any())
