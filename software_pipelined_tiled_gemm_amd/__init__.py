@@ -13,6 +13,7 @@ If the shared library has not been built, importing works but every call raises
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import struct
 from typing import Optional
@@ -345,7 +346,15 @@ def gemm_quantize_rows(X, A, scale, stream=None, dtype: Optional[str] = None,
     else:
         if dtype is None or shape is None:
             raise GemmError(1, "gemm_quantize_rows: a raw X needs dtype and shape")
-        device, X_, A_, s_ = None, X, _ptr(A), _ptr(scale)
+        rows, K = shape
+
+        def any_shape(t, want):
+            # tensors of any number of dimensions, as many values
+            return t.shape if hasattr(t, "shape") and t.shape.numel() == math.prod(want) else want
+
+        device, (A_, s_) = _dense("gemm_quantize_rows", ("A", A, _torch_type("i8"), any_shape(A, (rows, K))),
+                                  ("scale", scale, _torch_type("f32"), any_shape(scale, (rows,))))
+        X_ = X
     st = lib().gemm_quantize_rows(X_, DTYPES[dtype], shape[0], shape[1], A_, s_, _stream_on(stream, device))
     if st:
         _check(st, "gemm_quantize_rows")

@@ -126,3 +126,20 @@ def test_a_workspace_on_another_device(lib):
             assert not fn.calls
             call(OnDevice(n))
             assert len(fn.calls) == 1
+
+
+def test_quantising_from_a_raw_pointer_checks_the_tensors(lib, monkeypatch):
+    fn = lib.gemm_quantize_rows
+    i8, f32 = torch.int8, torch.float32
+    a, s = Like((4, 16), i8), Like((4,), f32)
+    args = dict(dtype="bf16", shape=(4, 16))
+    for A, scale in ((torch.zeros(4, 16, dtype=i8), s), (a, torch.zeros(4)), (Like((4, 15), i8), s), (Like((4, 16), f32), s),
+                     (a, Like((3,), f32)), (a, Like((4,), i8)), (a, Like((4,), f32, device=1))):
+        with pytest.raises(spg.GemmError) as e:
+            spg.gemm_quantize_rows(P, A, scale, stream=0, **args)
+        assert e.value.status == 1 and not fn.calls
+    # the tensors' device gives the stream, as for every other call
+    monkeypatch.setattr(spg, "_raw_stream", lambda device: 1000 + device)
+    spg.gemm_quantize_rows(P, Like((2, 2, 16), i8, device=3), Like((2, 2), f32, device=3), **args)
+    spg.gemm_quantize_rows(P, P, P, **args)
+    assert [c[-1] for c in fn.calls] == [1003, None] and all(c[:4] == (P, 1, 4, 16) for c in fn.calls)
