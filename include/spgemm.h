@@ -271,6 +271,8 @@ gemm_status gemm_gated_run(gemm_gated_handle h, const void* X, const void* Wg, c
 /* From dH [M,N] and the forward pass's operands, G and U:
  *     dU = dH * act(G), dG = dH * U * act'(G)      (act'(0) = 0 for ReLU)
  *     dX = dG Wg^T + dU Wu^T, dWg = X^T dG, dWu = X^T dU   (stored as X, Wg and Wu are)
+ * An infinity in G or U counts as the largest finite value of the type (the forward pass
+ * stores it for a finite sum beyond that); NaN stays NaN.
  * dG and dU are rounded to the plan's type; the sums are fp32, each gradient rounded once;
  * results do not vary from run to run.  Sums over nothing (M = 0: the weights' gradients,
  * N = 0: dX) write zeros. */

@@ -1183,6 +1183,10 @@ __global__ void __launch_bounds__(256) simple_product(SimpleArgs a) {
 // weights and the one sum over both segments (dX) read it without masks.  dG and dU are
 // rounded to the operands' type, as the products need them (a relative 2^-8 of each term
 // in bf16 at most, averaged down by the sums).  Bound by memory: 3 reads, 2 writes of M N values.
+//
+// An infinite G or U is read as the largest finite value of its type: the forward pass made it
+// of a finite sum when it rounded it for storage (fp16 ends at 65504), and zero slopes and zero
+// dH times infinity would be NaN in a whole row of dX and a whole column of dWg or dWu.
 template <bool BF16>
 __global__ void __launch_bounds__(256) gated_slopes(const uint16_t* dH, const uint16_t* G, const uint16_t* U,
                                                     uint16_t* D, int M, int N, int np, int act) {
@@ -1206,13 +1210,15 @@ __global__ void __launch_bounds__(256) gated_slopes(const uint16_t* dH, const ui
                 u[e >> 1] |= (uint32_t)U[o + e] << ((e & 1) * 16);
             }
     }
+    constexpr float kLargest = BF16 ? 0x1.fep127f : 65504.0f;
+    auto finite = [](float v) { return __builtin_fabsf(v) > kLargest ? __builtin_copysignf(kLargest, v) : v; };
     u32x4 dg = {}, du = {};
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const int sh = (e & 1) * 16;
         const float hv = bits_to_f32((uint16_t)(h[e >> 1] >> sh), BF16);
-        const float gv = bits_to_f32((uint16_t)(g[e >> 1] >> sh), BF16);
-        const float uv = bits_to_f32((uint16_t)(u[e >> 1] >> sh), BF16);
+        const float gv = finite(bits_to_f32((uint16_t)(g[e >> 1] >> sh), BF16));
+        const float uv = finite(bits_to_f32((uint16_t)(u[e >> 1] >> sh), BF16));
         float a, sl;
         if (act == kActRelu) {
             sl = gv <= 0.0f ? 0.0f : 1.0f;

@@ -759,3 +759,61 @@ def test_workspaces_are_checked_on_both_call_paths(monkeypatch):
                     assert e.value.status == 1
     torch.cuda.synchronize()
     assert not bool(h.any()) and not bool(c.any())
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh", "relu"])
+def test_slopes_of_infinite_preactivations(act, dtype):
+    # a stored infinity is a sum beyond the type's range: it counts as the largest finite
+    # value.  One row and X = 1: dWg and dWu are dG and dU, rounded to the type twice.
+    torch = _t()
+    inf, dt = float("inf"), _dt(dtype)
+    big = torch.finfo(dt).max
+    # (bf16: dH U has to stay inside fp32)
+    gates = [(g, u, d) for g in (inf, -inf, 2.0, -2.0, 0.0) for u in (inf, -inf, 1.0, -0.5, 0.0) for d in (0.0, 0.01, -1.0)]
+    G, U, D = (torch.tensor([[t[i] for t in gates]], dtype=dt, device="cuda") for i in range(3))
+    N, K = len(gates), 8
+    x, w = torch.ones(1, K, dtype=dt, device="cuda"), torch.zeros(N, K, dtype=dt, device="cuda")
+    dx, dwg, dwu = torch.empty_like(x), torch.empty_like(w), torch.empty_like(w)
+    with spg.Gated(1, N, K, dtype, "nk", act) as plan:
+        ws = _workspace(plan.workspace_bytes())
+        plan.backward(D, x, w, w, G, U, dx, dwg, dwu, workspace=ws)
+        g, u, d = G[0].double().clamp(-big, big), U[0].double().clamp(-big, big), D[0].double()
+        e, tiny = _half_ulp(dtype), _tiny(dtype)
+        A, S = _act(g, act), _slope(g, act)
+        small = g.abs().clamp(max=100)
+        want = d * u * S
+        # slopes pass 1: where a result leaves the type's range, its rounding is infinite
+        over = torch.isinf(want.to(dt))
+        assert torch.equal(dwg[over, 0], want[over].to(dt))
+        tol = 2.01 * e * want.abs() + 2.0 ** -19 * (d * u).abs() * (1 + small) + 2 * tiny
+        _within(dwg[~over, 0], want[~over], tol[~over], "dG")
+        _within(dwu[:, 0], d * A, 2.01 * e * (d * A).abs() + 2.0 ** -20 * d.abs() * small + 2.0 ** -126 + 2 * tiny, "dU")
+        assert bool(over.any()) or bool((dx == 0).all())      # inf * 0 in the products
+        # what is not a number stays so
+        G[0, 0], U[0, 20] = float("nan"), float("nan")
+        plan.backward(D, x, w, w, G, U, dx, dwg, dwu, workspace=ws)
+        assert bool(torch.isnan(dwu[0]).all()) and bool(torch.isfinite(dwu[1:]).all())
+        assert bool(torch.isnan(dwg[20]).all()) and not bool(torch.isnan(dwg[21:]).any())
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh", "relu"])
+def test_gates_beyond_fp16_train(act):
+    # gates of +-70000 are infinite in fp16; H and every gradient of the formula in fp32 are not
+    torch = _t()
+    M, N, K = 3, 24, 16
+    for layout in ("nk", "kn"):
+        x = torch.full((M, K), 1.0, dtype=torch.float16, device="cuda")
+        wg, wu = torch.full((N, K), 0.01, device="cuda"), torch.full((N, K), 1e-5, device="cuda")
+        wg[3], wg[7] = 70000.0 / K, -70000.0 / K
+        wg, wu = (w.half() if layout == "nk" else w.half().t().contiguous() for w in (wg, wu))
+        h, g, u = (torch.empty(M, N, dtype=torch.float16, device="cuda") for _ in range(3))
+        dh = torch.full_like(h, 0.125)
+        dh[1] = 0.0
+        grads = [torch.empty_like(t) for t in (x, wg, wu)]
+        with spg.Gated(M, N, K, "f16", layout, act) as plan:
+            ws = _workspace(plan.workspace_bytes())
+            plan(x, wg, wu, h, G=g, U=u, workspace=ws)
+            assert bool((g[:, 3] == float("inf")).all()) and bool((g[:, 7] == -float("inf")).all())
+            plan.backward(dh, x, wg, wu, g, u, *grads, workspace=ws)
+        assert all(bool(torch.isfinite(t).all()) for t in (h, *grads)), layout
