@@ -155,7 +155,10 @@ PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
         return nullptr;
     }
     const DLPackExchangeAPI* api = (const DLPackExchangeAPI*)PyCapsule_GetPointer(a[0], "dlpack_exchange_api");
-    if (!api) return nullptr;
+    if (!api) {   // not the interface this file knows
+        PyErr_Clear();
+        Py_RETURN_FALSE;
+    }
     if (api->header.version.major != DLPACK_MAJOR_VERSION || !api->dltensor_from_py_object_no_sync ||
         !api->current_work_stream)
         Py_RETURN_FALSE;

@@ -143,3 +143,18 @@ def test_quantising_from_a_raw_pointer_checks_the_tensors(lib, monkeypatch):
     spg.gemm_quantize_rows(P, Like((2, 2, 16), i8, device=3), Like((2, 2), f32, device=3), **args)
     spg.gemm_quantize_rows(P, P, P, **args)
     assert [c[-1] for c in fn.calls] == [1003, None] and all(c[:4] == (P, 1, 4, 16) for c in fn.calls)
+
+
+def test_an_exchange_interface_of_another_kind(monkeypatch):
+    # a torch whose interface cannot be read: the Python path, not an error out of a plan
+    import ctypes
+    import os
+    if not os.path.exists(os.path.join(os.path.dirname(spg.__file__), "_calls.so")):
+        pytest.fail("_calls.so is not built; run __graft_entry__.build()")
+    new = ctypes.pythonapi.PyCapsule_New
+    new.restype, new.argtypes = ctypes.py_object, [ctypes.c_void_p, ctypes.c_char_p, ctypes.c_void_p]
+    for other in (new(P, b"dlpack_exchange_api_of_another_version", None), new(P, None, None), object()):
+        monkeypatch.setattr(torch.Tensor, "__dlpack_c_exchange_api__", other, raising=False)
+        monkeypatch.setattr(spg, "_calls", False)
+        with spg.Gated(4, 32, 16) as plan:
+            assert plan._calls is None
