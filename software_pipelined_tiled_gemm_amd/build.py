@@ -19,6 +19,7 @@ import sys
 import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
+from typing import Optional
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -94,12 +95,22 @@ def build(out: str = OUT, extra=(), poison: bool = False) -> str:
     return out
 
 
-def build_calls(out: str = CALLS_OUT) -> str:
+def build_calls(out: str = CALLS_OUT) -> Optional[str]:
     """Compile csrc/binding.cpp, the wrappers' call path for torch tensors (host code; the
-    Python and DLPack headers only, nothing linked)."""
-    import torch
-    inc = ["-I", sysconfig.get_paths()["include"],
-           "-I", os.path.join(os.path.dirname(torch.__file__), "include")]
+    Python and DLPack headers only, nothing linked).  Without torch or one of the headers it is
+    left out (None, and a line on stderr): the library's C users need none of them, and the
+    wrappers make the same checks and calls in Python."""
+    try:
+        import torch
+    except ImportError:
+        print("no torch: the compiled call path of the Python wrappers is not built", file=sys.stderr)
+        return None
+    dirs = [sysconfig.get_paths()["include"], os.path.join(os.path.dirname(torch.__file__), "include")]
+    for d, header in zip(dirs, ("Python.h", os.path.join("ATen", "dlpack.h"))):
+        if not os.path.exists(os.path.join(d, header)):
+            print(f"no {header} in {d}: the compiled call path of the Python wrappers is not built", file=sys.stderr)
+            return None
+    inc = [a for d in dirs for a in ("-I", d)]
     tmp_out = out + ".tmp"
     subprocess.run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", *inc,
                     os.path.join(CSRC, "binding.cpp"), "-o", tmp_out], check=True)

@@ -158,3 +158,20 @@ def test_an_exchange_interface_of_another_kind(monkeypatch):
         monkeypatch.setattr(spg, "_calls", False)
         with spg.Gated(4, 32, 16) as plan:
             assert plan._calls is None
+
+
+def test_the_build_without_torch_or_headers(monkeypatch, tmp_path, capsys):
+    # the library itself needs neither: its C users build without the wrappers' call path
+    import sys
+    from software_pipelined_tiled_gemm_amd import build
+    out = tmp_path / "_calls.so"
+    with monkeypatch.context() as m:
+        m.setitem(sys.modules, "torch", None)
+        assert build.build_calls(str(out)) is None
+        assert "torch" in capsys.readouterr().err
+    with monkeypatch.context() as m:
+        m.setattr(build.sysconfig, "get_paths", lambda: {"include": str(tmp_path)})
+        assert build.build_calls(str(out)) is None
+        assert "Python.h" in capsys.readouterr().err
+    assert not list(tmp_path.iterdir())
+    assert build.build_calls(str(out)) == str(out) and out.exists()
