@@ -360,11 +360,14 @@ def gemm_quantize_rows(X, A, scale, stream=None, dtype: Optional[str] = None,
         _check(st, "gemm_quantize_rows")
 
 
-def _scratch(what: str, workspace, given: Optional[int] = None, device: Optional[int] = None) -> tuple:
+def _scratch(what: str, workspace, given: Optional[int] = None, device: Optional[int] = None, raw: int = 0) -> tuple:
     """Pointer and bytes of a workspace.  A tensor has to be dense memory of the operands' GPU
-    (`device`, where they tell): the kernels write as many bytes as its size promises."""
-    if workspace is None or isinstance(workspace, int):
-        return workspace, given or 0
+    (`device`, where they tell): the kernels write as many bytes as its size promises.  A raw
+    pointer without a given size has `raw` bytes: the plan's need, as raw operands have its shapes."""
+    if workspace is None:
+        return None, given or 0
+    if isinstance(workspace, int):
+        return workspace, raw if given is None else given
     if not workspace.is_contiguous():
         raise GemmError(1, f"{what}: workspace is not contiguous")
     if not workspace.is_cuda:
@@ -512,13 +515,15 @@ class Gated:
 
     X [M,K]; Wg, Wu [N,K] ("nk") or [K,N] ("kn"); H, G, U [M,N].  Pass G and U to keep the
     pre-activations for ``backward``.  ``workspace`` is a uint8 tensor of at least
-    ``workspace_bytes()``; calls in flight on different streams need one each."""
+    ``workspace_bytes()``, or a raw pointer to that much memory; calls in flight on different
+    streams need one each."""
 
     def __init__(self, M, N, K, dtype="bf16", layout="nk", act="silu"):
         self.handle = 0
         self.M, self.N, self.K = M, N, K
         self.dtype, self.layout, self.act = dtype, layout, act
         self.handle = gemm_gated_create(M, N, K, dtype, layout, act)
+        self._ws = gemm_gated_workspace(self.handle)
         self._x, self._h = (M, K), (M, N)
         self._w = (N, K) if layout == "nk" else (K, N)
         self._run, self._back = lib().gemm_gated_run, lib().gemm_gated_backward
@@ -542,7 +547,7 @@ class Gated:
         d, x, w, h = self._type, self._x, self._w, self._h
         dev, p = _dense("Gated", ("X", X, d, x), ("Wg", Wg, d, w), ("Wu", Wu, d, w), ("H", H, d, h),
                         ("G", G, d, h), ("U", U, d, h))
-        st = self._run(self.handle, *p, *_scratch("Gated", workspace, device=dev), _stream_on(stream, dev))
+        st = self._run(self.handle, *p, *_scratch("Gated", workspace, device=dev, raw=self._ws), _stream_on(stream, dev))
         if st:
             _check(st, "gemm_gated_run")
         return H
@@ -559,7 +564,7 @@ class Gated:
         dev, p = _dense("Gated.backward", ("dH", dH, d, h), ("X", X, d, x), ("Wg", Wg, d, w),
                         ("Wu", Wu, d, w), ("G", G, d, h), ("U", U, d, h), ("dX", dX, d, x),
                         ("dWg", dWg, d, w), ("dWu", dWu, d, w))
-        st = self._back(self.handle, *p, *_scratch("Gated.backward", workspace, device=dev), _stream_on(stream, dev))
+        st = self._back(self.handle, *p, *_scratch("Gated.backward", workspace, device=dev, raw=self._ws), _stream_on(stream, dev))
         if st:
             _check(st, "gemm_gated_backward")
         return dX, dWg, dWu
@@ -586,13 +591,15 @@ class QuantizedGemm:
     """C = (A B^T) scaled by row and by column, int8 operands (gemm_quantized_* in
     include/spgemm.h); with an activation C = act(C1) * C2 from B and B2.
 
-    A [M,K] int8 with scale_a [M]; B, B2 [N,K] int8 with scale_b, scale_b2 [N]; C [M,N]."""
+    A [M,K] int8 with scale_a [M]; B, B2 [N,K] int8 with scale_b, scale_b2 [N]; C [M,N];
+    ``workspace`` as in ``Gated``."""
 
     def __init__(self, M, N, K, out_dtype="bf16", act="none"):
         self.handle = 0
         self.M, self.N, self.K = M, N, K
         self.out_dtype, self.act = out_dtype, act
         self.handle = gemm_quantized_create(M, N, K, out_dtype, act)
+        self._ws = gemm_quantized_workspace(self.handle)
         self._a, self._b, self._c, self._m, self._n = (M, K), (N, K), (M, N), (M,), (N,)
         self._run = lib().gemm_quantized_run
         self._calls = _calls_module()
@@ -615,7 +622,7 @@ class QuantizedGemm:
         dev, p = _dense("QuantizedGemm", ("A", A, i8, self._a), ("scale_a", scale_a, f32, m), ("B", B, i8, b),
                         ("scale_b", scale_b, f32, n), ("B2", B2, i8, b), ("scale_b2", scale_b2, f32, n),
                         ("C", C, self._out, self._c))
-        st = self._run(self.handle, *p, *_scratch("QuantizedGemm", workspace, device=dev), _stream_on(stream, dev))
+        st = self._run(self.handle, *p, *_scratch("QuantizedGemm", workspace, device=dev, raw=self._ws), _stream_on(stream, dev))
         if st:
             _check(st, "gemm_quantized_run")
         return C

@@ -175,3 +175,14 @@ def test_the_build_without_torch_or_headers(monkeypatch, tmp_path, capsys):
         assert "Python.h" in capsys.readouterr().err
     assert not list(tmp_path.iterdir())
     assert build.build_calls(str(out)) == str(out) and out.exists()
+
+
+def test_raw_workspaces_through_the_classes(lib):
+    # a raw pointer is taken at its word, as raw operands are: workspace_bytes() of memory
+    for fn, n, call in calls(lib)[:3]:
+        call(workspace=P)
+        assert fn.calls[-1][-3:-1] == (P, n)
+    # the functions of the entry points' names take the size
+    for fn, n, call in calls(lib)[3:]:
+        call(workspace=P)
+        assert fn.calls[-1][-3:-1] == (P, 0)

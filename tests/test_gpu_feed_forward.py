@@ -817,3 +817,23 @@ def test_gates_beyond_fp16_train(act):
             assert bool((g[:, 3] == float("inf")).all()) and bool((g[:, 7] == -float("inf")).all())
             plan.backward(dh, x, wg, wu, g, u, *grads, workspace=ws)
         assert all(bool(torch.isfinite(t).all()) for t in (h, *grads)), layout
+
+
+def test_raw_pointers_with_a_workspace():
+    # operands and workspace as raw pointers, where the reduction is split, against tensors
+    torch = _t()
+    M, N, K = 96, 256, 8192
+    x, wg, wu = (b.t for b in _gated_case(M, N, K, "bf16", "nk", 105))
+    out = []
+    with spg.Gated(M, N, K, "bf16", "nk", "silu") as plan:
+        ws = _workspace(plan.workspace_bytes())
+        stream = torch.cuda.current_stream().cuda_stream
+        for raw in (False, True):
+            h, g, u = (torch.zeros(M, N, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+            grads = [torch.zeros_like(t) for t in (x, wg, wu)]
+            p = (lambda t: t.data_ptr()) if raw else (lambda t: t)
+            plan(p(x), p(wg), p(wu), p(h), G=p(g), U=p(u), workspace=p(ws), stream=stream)
+            plan.backward(*(p(t) for t in (h, x, wg, wu, g, u, *grads)), workspace=p(ws), stream=stream)
+            torch.cuda.synchronize()
+            out.append([h, g, u, *grads])
+    assert all(torch.equal(a, b) and bool(a.any()) for a, b in zip(*out))
