@@ -264,6 +264,9 @@ gemm_status gemm_gated_create(gemm_gated_handle* out, int64_t M, int64_t N, int6
                               gemm_b_layout layout, gemm_activation act);
 /* Bytes of workspace that gemm_gated_run and gemm_gated_backward need (-1: NULL handle). */
 int64_t gemm_gated_workspace(gemm_gated_handle h);
+/* Bytes that gemm_gated_run alone needs (serving): parts of a split reduction and copies of
+ * misaligned operands, without the backward pass's dG and dU; often 0. */
+int64_t gemm_gated_run_workspace(gemm_gated_handle h);
 /* H [M,N]; G and U [M,N] receive the pre-activations that the backward pass reads, rounded
  * to the plan's type; both NULL (serving) or both given (training). */
 gemm_status gemm_gated_run(gemm_gated_handle h, const void* X, const void* Wg, const void* Wu, void* H, void* G,

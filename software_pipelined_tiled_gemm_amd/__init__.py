@@ -81,7 +81,8 @@ EXPORTED = ("gemm_create", "gemm_run", "gemm_destroy", "gemm_get_config", "gemm_
             "gemm_autotune",
             "gemm_num_configs", "gemm_list_config", "gemm_lds_bytes", "gemm_status_string",
             "gemm_last_hip_error", "gemm_wait_timeouts", "gelu_run",
-            "gemm_gated_create", "gemm_gated_workspace", "gemm_gated_run", "gemm_gated_backward",
+            "gemm_gated_create", "gemm_gated_workspace", "gemm_gated_run_workspace",
+            "gemm_gated_run", "gemm_gated_backward",
             "gemm_gated_destroy", "gemm_quantized_create", "gemm_quantized_workspace",
             "gemm_quantized_run", "gemm_quantized_destroy", "gemm_quantize_rows")
 
@@ -148,6 +149,7 @@ def _load(path):
     for name, res, args in (
             ("gemm_gated_create", en, [ctypes.POINTER(vp), i64, i64, i64, en, en, en]),
             ("gemm_gated_workspace", i64, [vp]),
+            ("gemm_gated_run_workspace", i64, [vp]),
             ("gemm_gated_run", en, [vp] * 8 + [i64, vp]),
             ("gemm_gated_backward", en, [vp] * 11 + [i64, vp]),
             ("gemm_gated_destroy", en, [vp]),
@@ -279,6 +281,10 @@ def gemm_gated_create(M: int, N: int, K: int, dtype: str = "bf16", layout: str =
 
 def gemm_gated_workspace(handle: int) -> int:
     return int(lib().gemm_gated_workspace(handle))
+
+
+def gemm_gated_run_workspace(handle: int) -> int:
+    return int(lib().gemm_gated_run_workspace(handle))
 
 
 def gemm_gated_run(handle: int, X, Wg, Wu, H, G=None, U=None, workspace=None,
@@ -515,8 +521,9 @@ class Gated:
 
     X [M,K]; Wg, Wu [N,K] ("nk") or [K,N] ("kn"); H, G, U [M,N].  Pass G and U to keep the
     pre-activations for ``backward``.  ``workspace`` is a uint8 tensor of at least
-    ``workspace_bytes()``, or a raw pointer to that much memory; calls in flight on different
-    streams need one each."""
+    ``workspace_bytes()``, or a raw pointer to that much memory; where only the projection is
+    called, ``workspace_bytes(backward=False)`` is enough.  Calls in flight on different streams
+    need one each."""
 
     def __init__(self, M, N, K, dtype="bf16", layout="nk", act="silu"):
         self.handle = 0
@@ -524,6 +531,7 @@ class Gated:
         self.dtype, self.layout, self.act = dtype, layout, act
         self.handle = gemm_gated_create(M, N, K, dtype, layout, act)
         self._ws = gemm_gated_workspace(self.handle)
+        self._ws_run = gemm_gated_run_workspace(self.handle)
         self._x, self._h = (M, K), (M, N)
         self._w = (N, K) if layout == "nk" else (K, N)
         self._run, self._back = lib().gemm_gated_run, lib().gemm_gated_backward
@@ -533,8 +541,9 @@ class Gated:
         self._run_spec = _address(self._run), _specs(x, w, w, h, h, h)
         self._back_spec = _address(self._back), _specs(h, x, w, w, h, h, x, w, w)
 
-    def workspace_bytes(self) -> int:
-        return gemm_gated_workspace(self.handle)
+    def workspace_bytes(self, backward: bool = True) -> int:
+        """Bytes for the plan's calls; without ``backward`` for the projection alone."""
+        return gemm_gated_workspace(self.handle) if backward else gemm_gated_run_workspace(self.handle)
 
     def __call__(self, X, Wg, Wu, H, G=None, U=None, workspace=None, stream=None):
         if self._calls is not None:
@@ -547,7 +556,7 @@ class Gated:
         d, x, w, h = self._type, self._x, self._w, self._h
         dev, p = _dense("Gated", ("X", X, d, x), ("Wg", Wg, d, w), ("Wu", Wu, d, w), ("H", H, d, h),
                         ("G", G, d, h), ("U", U, d, h))
-        st = self._run(self.handle, *p, *_scratch("Gated", workspace, device=dev, raw=self._ws), _stream_on(stream, dev))
+        st = self._run(self.handle, *p, *_scratch("Gated", workspace, device=dev, raw=self._ws_run), _stream_on(stream, dev))
         if st:
             _check(st, "gemm_gated_run")
         return H

@@ -405,6 +405,7 @@ gemm_status gemm_gated_create(gemm_gated_handle* out, int64_t M, int64_t N, int6
 }
 
 int64_t gemm_gated_workspace(gemm_gated_handle h) { return h ? std::max(h->ws_fwd, h->ws_back) : -1; }
+int64_t gemm_gated_run_workspace(gemm_gated_handle h) { return h ? h->ws_fwd : -1; }
 
 gemm_status gemm_gated_run(gemm_gated_handle h, const void* X, const void* Wg, const void* Wu, void* H, void* G,
                            void* U, void* workspace, int64_t workspace_bytes, hipStream_t stream) {

@@ -139,3 +139,18 @@ def test_wrappers_check_tensors():
         spg.gemm_quantize_rows(x, torch.zeros(4, 15, dtype=torch.int8), torch.zeros(4))
     with pytest.raises(KeyError):
         spg.Gated(4, 32, 16, "f64")
+
+
+def test_serving_needs_no_room_for_the_backward_pass(L):
+    assert L.gemm_gated_run_workspace(None) == -1
+    with spg.Gated(8192, 12288, 4096, "bf16", "nk", "silu") as plan:
+        assert plan.workspace_bytes(backward=False) == 0
+        assert plan.workspace_bytes() >= 8192 * 12288 * 2 * 2
+    p = 4096
+    for layout, K in (("kn", 8192), ("nk", 8192), ("kn", 1001), ("nk", 1001)):
+        h = spg.gemm_gated_create(96, 256, K, "bf16", layout, "silu")
+        run, both = spg.gemm_gated_run_workspace(h), spg.gemm_gated_workspace(h)
+        assert 0 <= run <= both
+        if K == 8192:      # split: the projection asks for its own part and for no more
+            assert run > 0 and L.gemm_gated_run(h, p, p, p, p, 0, 0, p, run - 1, 0) == 1
+        spg.gemm_gated_destroy(h)

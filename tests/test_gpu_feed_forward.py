@@ -837,3 +837,20 @@ def test_raw_pointers_with_a_workspace():
             torch.cuda.synchronize()
             out.append([h, g, u, *grads])
     assert all(torch.equal(a, b) and bool(a.any()) for a, b in zip(*out))
+
+
+@pytest.mark.parametrize("layout", ["nk", "kn"])
+def test_serving_in_its_own_workspace(layout):
+    # split reductions and operands laid out again, in exactly what the projection asks for
+    torch = _t()
+    for M, N, K in ((96, 256, 8192), (1300, 2051, 1003), (300, 1024, 448)):
+        x, wg, wu = (b.t for b in _gated_case(M, N, K, "bf16", layout, 107))
+        h = Buf((M, N), torch.bfloat16)
+        with spg.Gated(M, N, K, "bf16", layout, "silu") as plan:
+            n = plan.workspace_bytes(backward=False)
+            assert n <= plan.workspace_bytes()
+            ws = Buf((max(n, 16),), torch.uint8, 0)
+            plan(x, wg, wu, h.t, workspace=ws.t)
+        torch.cuda.synchronize()
+        _check_forward(x, wg, wu, h.t, None, None, "bf16", layout, "silu")
+        assert h.intact() and ws.intact()
