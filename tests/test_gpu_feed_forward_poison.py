@@ -1,8 +1,9 @@
 """The feed-forward operators on the poisoned library: in it every ring slot starts as NaN
 patterns and becomes NaN again the moment its release barrier has passed, so a fragment read
 that the barriers do not cover gives NaN (int8: -1) in the result.  Results have to be finite
-and bitwise those of the production library, over every tile class, both copy modes, split
-and merged launches, and k-tile counts around the rings' depths."""
+and bitwise those of the production library, over both copy modes, split and merged launches,
+and k-tile counts around the rings' depths; test_gpu_feed_forward_forms.py does the same for
+every kernel that the choice of tiles launches."""
 
 import pytest
 
