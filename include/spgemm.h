@@ -259,7 +259,7 @@ typedef struct gemm_quantized_plan* gemm_quantized_handle;
  * X [M,K], Wg and Wu [N,K] (GEMM_B_NK) or [K,N] (GEMM_B_KN), all fp16 or all bf16; sums
  * and the activation in fp32, each output rounded once.  M, N, K >= 0.
  * Errors: INVALID_ARG (out NULL, negative size, fp32 or unknown dtype, unknown layout, act
- * NONE or unknown), UNSUPPORTED (a size above 2^30). */
+ * NONE or unknown), UNSUPPORTED (a size above 2^30 - 513). */
 gemm_status gemm_gated_create(gemm_gated_handle* out, int64_t M, int64_t N, int64_t K, gemm_dtype dtype,
                               gemm_b_layout layout, gemm_activation act);
 /* Bytes of workspace that gemm_gated_run and gemm_gated_backward need (-1: NULL handle). */
@@ -267,8 +267,9 @@ int64_t gemm_gated_workspace(gemm_gated_handle h);
 /* Bytes that gemm_gated_run alone needs (serving): parts of a split reduction and copies of
  * misaligned operands, without the backward pass's dG and dU; often 0. */
 int64_t gemm_gated_run_workspace(gemm_gated_handle h);
-/* H [M,N]; G and U [M,N] receive the pre-activations that the backward pass reads, rounded
- * to the plan's type; both NULL (serving) or both given (training). */
+/* H [M,N], from the fp32 sums; G and U [M,N] receive the pre-activations that the backward pass
+ * reads, rounded to the plan's type (half the memory that training keeps, and three of the
+ * backward pass's reads); both NULL (serving) or both given (training). */
 gemm_status gemm_gated_run(gemm_gated_handle h, const void* X, const void* Wg, const void* Wu, void* H, void* G,
                            void* U, void* workspace, int64_t workspace_bytes, hipStream_t stream);
 /* From dH [M,N] and the forward pass's operands, G and U:
@@ -276,8 +277,10 @@ gemm_status gemm_gated_run(gemm_gated_handle h, const void* X, const void* Wg, c
  *     dX = dG Wg^T + dU Wu^T, dWg = X^T dG, dWu = X^T dU   (stored as X, Wg and Wu are)
  * An infinity in G or U counts as the largest finite value of the type (the forward pass
  * stores it for a finite sum beyond that); NaN stays NaN.
- * dG and dU are rounded to the plan's type; the sums are fp32, each gradient rounded once;
- * results do not vary from run to run.  Sums over nothing (M = 0: the weights' gradients,
+ * dG and dU are rounded to the plan's type, the operands' of the products that sum them; the
+ * sums are fp32, each gradient rounded once; results do not vary from run to run.  Together the
+ * four roundings leave a bf16 gradient 0.003 off (of its norm), an exact one rounded once 0.0017.
+ * fp16 steps are 2^-24 below 2^-14: losses are to be scaled so that dG and dU stay above it.  Sums over nothing (M = 0: the weights' gradients,
  * N = 0: dX) write zeros. */
 gemm_status gemm_gated_backward(gemm_gated_handle h, const void* dH, const void* X, const void* Wg, const void* Wu,
                                 const void* G, const void* U, void* dX, void* dWg, void* dWu, void* workspace,
@@ -287,8 +290,10 @@ gemm_status gemm_gated_destroy(gemm_gated_handle h);
 /* Plan of a product of 8-bit integers,
  *     C[m,n] = (sum_k A[m,k] B[n,k]) * scale_a[m] * scale_b[n]
  * A [M,K] with a scale per row (token), B [N,K] with a scale per row (output channel),
- * exact int32 sums, C [M,N] fp16, bf16 or fp32, rounded once.  With an activation:
- * C = act(C1) * C2, C1 from (B, scale_b) and C2 from (B2, scale_b2).
+ * exact int32 sums; the sum's conversion to fp32 (exact up to 2^24), the product with scale_a
+ * and the product with scale_b are rounded once each (3 * 2^-24 of the value at most), then the
+ * result to C's type (C [M,N] fp16, bf16 or fp32).  With an activation: C = act(C1) * C2 in
+ * fp32, C1 from (B, scale_b) and C2 from (B2, scale_b2).
  * Errors: INVALID_ARG, UNSUPPORTED (K > 131071, where the sums could overflow). */
 gemm_status gemm_quantized_create(gemm_quantized_handle* out, int64_t M, int64_t N, int64_t K, gemm_dtype out_dtype,
                                   gemm_activation act);
