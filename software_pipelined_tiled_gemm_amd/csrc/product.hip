@@ -83,7 +83,9 @@ int64_t tiles_of(const Shape& s, int t) {
 // store, plus a launch; never less than the operands take to read.  Parts add a kernel and
 // their sums' traffic.  The constants are fitted to the measured times of every tile class
 // and up to 16 parts at 360 shapes of the seven products, 1 to 12288 rows, columns and
-// reductions: the choice takes 1% longer than the fastest on average, 30% at worst.  What
+// reductions.  Of whole calls, the sums among them and up to 32 parts, the choice takes 1.6%
+// longer than the fastest on average, 40% at worst, more than 10% at 17 of 357 shapes (nine
+// of them of at most 64 rows, most of which want more parts).  What
 // bounds the small tiles is that a CU copies about 105 bytes a nanosecond into its LDS; what
 // bounds short reductions, the start and the store.  Pairs: 4096 x 8192 outputs of 64, 256
 // and 1024 reductions take 36, 55 and 140 us against 54, 73 and 164 with one 128x128 tile a
