@@ -7,7 +7,7 @@ in parallel.  csrc/gemm.hip holds the GEMM's host side (C ABI, variant table) an
 csrc/gelu.hip the standalone elementwise GELU (include/spgelu.h).  The feed-forward
 operators are csrc/product.hip (host side) and csrc/product_unit.hip, compiled once per
 element type, product and copy mode.  csrc/binding.cpp becomes a module of its own,
-_calls.so.
+_calls.so, where torch is installed.
 """
 
 from __future__ import annotations
