@@ -374,6 +374,8 @@ def _scratch(what: str, workspace, given: Optional[int] = None, device: Optional
         return None, given or 0
     if isinstance(workspace, int):
         return workspace, raw if given is None else given
+    if workspace.nbytes == 0 and not given:
+        return None, 0
     if not workspace.is_contiguous():
         raise GemmError(1, f"{what}: workspace is not contiguous")
     if not workspace.is_cuda:

@@ -186,3 +186,10 @@ def test_raw_workspaces_through_the_classes(lib):
     for fn, n, call in calls(lib)[3:]:
         call(workspace=P)
         assert fn.calls[-1][-3:-1] == (P, 0)
+
+
+def test_empty_workspaces(lib):
+    # workspace_bytes() may be 0: a tensor without bytes is no workspace, wherever it is
+    for fn, n, call in calls(lib):
+        call(workspace=torch.empty(0, dtype=torch.uint8))
+        assert fn.calls[-1][-3:-1] == (None, 0)
