@@ -1242,8 +1242,11 @@ __global__ void __launch_bounds__(256) gated_slopes(const uint16_t* dH, const ui
             a = gv * s;
             sl = __builtin_fmaf(a * (1.0f - s), dz, s);
         }
+        // dH U may pass fp32's range (bf16's is as wide) where the slope brings it back
+        float d = hv * uv;
+        d = BF16 && __builtin_fabsf(d) > 0x1.fffffep127f ? hv * sl * uv : d * sl;
         if (n + e < N) {
-            dg[e >> 1] |= (uint32_t)f32_to_bits(hv * uv * sl, BF16) << sh;
+            dg[e >> 1] |= (uint32_t)f32_to_bits(d, BF16) << sh;
             du[e >> 1] |= (uint32_t)f32_to_bits(hv * a, BF16) << sh;
         }
     }

@@ -854,3 +854,28 @@ def test_serving_in_its_own_workspace(layout):
         torch.cuda.synchronize()
         _check_forward(x, wg, wu, h.t, None, None, "bf16", layout, "silu")
         assert h.intact() and ws.intact()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh", "relu"])
+def test_slopes_where_dh_times_u_leaves_the_range(act):
+    # bf16 holds values whose product fp32 does not; with the slope it does.  One row and X = 1:
+    # dWg is dG, rounded to the type twice
+    torch = _t()
+    vals = [(g, u, d) for g in (-200.0, -20.0, -3.0, 0.5, 30.0) for u in (1e20, -3e38, 1e-3) for d in (1e20, -1e25, 2.0)]
+    G, U, D = (torch.tensor([[t[i] for t in vals]], dtype=torch.bfloat16, device="cuda") for i in range(3))
+    N, K = len(vals), 8
+    x = torch.ones(1, K, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(N, K, dtype=torch.bfloat16, device="cuda")
+    dx, dwg, dwu = torch.empty_like(x), torch.empty_like(w), torch.empty_like(w)
+    with spg.Gated(1, N, K, "bf16", "nk", act) as plan:
+        plan.backward(D, x, w, w, G, U, dx, dwg, dwu, workspace=_workspace(plan.workspace_bytes()))
+    g, u, d = (t[0].double() for t in (G, U, D))
+    want = d * u * _slope(g, act)
+    tol = 2.01 * _half_ulp("bf16") * want.abs() + 2.0 ** -19 * (d * u).abs() * (1 + g.abs()) + 2 * _tiny("bf16")
+    got = dwg[:, 0]
+    assert not bool(torch.isnan(got).any())
+    # clear of the range's end on either side: finite, or the infinity
+    inside, outside = want.abs() + tol < 3e38, want.abs() - tol > 3.5e38
+    _within(got[inside], want[inside], tol[inside], "dG")
+    assert torch.equal(got[outside].double(), torch.sign(want[outside]) * float("inf"))
+    assert bool(inside.any()) and bool(outside.any())
