@@ -1218,38 +1218,45 @@ __global__ void __launch_bounds__(256) gated_slopes(const uint16_t* dH, const ui
             }
     }
     constexpr float kLargest = BF16 ? 0x1.fep127f : 65504.0f;
-    auto finite = [](float v) { return __builtin_fabsf(v) > kLargest ? __builtin_copysignf(kLargest, v) : v; };
+    auto finite = [](float v) {   // NaN stays NaN
+        return __builtin_elementwise_minimum(__builtin_elementwise_maximum(v, -kLargest), kLargest);
+    };
     u32x4 dg = {}, du = {};
+    // the activation chosen once, not for every value: with the two limits above, 511 x 1365 took
+    // 4.5 us with a branch a value, 4.3 so (and 4.3 without the limits, with the branches)
+    with_act(act, [&](auto ac) {
+        constexpr int ACT = decltype(ac)::value;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int sh = (e & 1) * 16;
-        const float hv = bits_to_f32((uint16_t)(h[e >> 1] >> sh), BF16);
-        const float gv = finite(bits_to_f32((uint16_t)(g[e >> 1] >> sh), BF16));
-        const float uv = finite(bits_to_f32((uint16_t)(u[e >> 1] >> sh), BF16));
-        float a, sl;
-        if (act == kActRelu) {
-            sl = gv <= 0.0f ? 0.0f : 1.0f;
-            a = gv <= 0.0f ? 0.0f : gv;
-        } else {
-            float z = gv, dz = 1.0f;
-            if (act == kActGelu) {
-                // past |G| = 1e15 s is 0 or 1 and its slope's zero must not meet an infinity
-                const float g2 = __builtin_fminf(gv * gv, 1e30f);
-                z = 1.5957691216f * gv * __builtin_fmaf(0.044715f, g2, 1.0f);
-                dz = 1.5957691216f * __builtin_fmaf(0.134145f, g2, 1.0f);
+        for (int e = 0; e < 8; ++e) {
+            const int sh = (e & 1) * 16;
+            const float hv = bits_to_f32((uint16_t)(h[e >> 1] >> sh), BF16);
+            const float gv = finite(bits_to_f32((uint16_t)(g[e >> 1] >> sh), BF16));
+            const float uv = finite(bits_to_f32((uint16_t)(u[e >> 1] >> sh), BF16));
+            float a, sl;
+            if constexpr (ACT == kActRelu) {
+                sl = gv <= 0.0f ? 0.0f : 1.0f;
+                a = gv <= 0.0f ? 0.0f : gv;
+            } else {
+                float z = gv, dz = 1.0f;
+                if constexpr (ACT == kActGelu) {
+                    // past |G| = 1e15 s is 0 or 1 and its slope's zero must not meet an infinity
+                    const float g2 = __builtin_fminf(gv * gv, 1e30f);
+                    z = 1.5957691216f * gv * __builtin_fmaf(0.044715f, g2, 1.0f);
+                    dz = 1.5957691216f * __builtin_fmaf(0.134145f, g2, 1.0f);
+                }
+                const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
+                a = gv * s;
+                sl = __builtin_fmaf(a * (1.0f - s), dz, s);
             }
-            const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
-            a = gv * s;
-            sl = __builtin_fmaf(a * (1.0f - s), dz, s);
+            // dH U may pass fp32's range (bf16's is as wide) where the slope brings it back
+            float d = hv * uv;
+            d = BF16 && __builtin_fabsf(d) > 0x1.fffffep127f ? hv * sl * uv : d * sl;
+            if (n + e < N) {
+                dg[e >> 1] |= (uint32_t)f32_to_bits(d, BF16) << sh;
+                du[e >> 1] |= (uint32_t)f32_to_bits(hv * a, BF16) << sh;
+            }
         }
-        // dH U may pass fp32's range (bf16's is as wide) where the slope brings it back
-        float d = hv * uv;
-        d = BF16 && __builtin_fabsf(d) > 0x1.fffffep127f ? hv * sl * uv : d * sl;
-        if (n + e < N) {
-            dg[e >> 1] |= (uint32_t)f32_to_bits(d, BF16) << sh;
-            du[e >> 1] |= (uint32_t)f32_to_bits(hv * a, BF16) << sh;
-        }
-    }
+    });
     uint16_t* d = D + (size_t)m * 2 * np + n;
     *(u32x4*)d = dg;
     *(u32x4*)(d + np) = du;
