@@ -312,6 +312,137 @@ gemm_status gemm_quantized_destroy(gemm_quantized_handle h);
 gemm_status gemm_quantize_rows(const void* X, gemm_dtype dtype, int64_t rows, int64_t K, int8_t* A, float* scale,
                                hipStream_t stream);
 
+/* ---------------------------------------------------------------------------------
+ * Operators of a mixture-of-experts block: the norm before it, the routing of its tokens,
+ * the experts' products, and the combination of their rows.  The conventions above hold:
+ * dense row-major matrices, device pointers owned by the caller, any element alignment,
+ * status codes, checks before any HIP call, asynchronous on `stream`, no allocation and no
+ * synchronization, results that do not vary from run to run; workspaces as for the
+ * feed-forward operators.  Outputs must not overlap inputs (not checked).
+ *
+ * Groups.  Rows that belong to the same expert lie together: group e is rows offsets[e] to
+ * offsets[e+1] - 1 of `rows`, offsets [groups + 1] int32 on the device, read there (no call
+ * waits for them).  Groups may be empty, and rows may be left over in front of the first
+ * group and behind the last: no call reads or writes them.  Offsets outside 0 .. rows count
+ * as the nearest of the two, and a group that would end before it starts is empty; where that
+ * makes groups overlap, rows may be left out, but nothing outside the operands is touched. */
+
+typedef struct gemm_norm_plan* gemm_norm_handle;
+typedef struct gemm_route_plan* gemm_route_handle;
+typedef struct gemm_grouped_plan* gemm_grouped_handle;
+typedef struct gemm_experts_plan* gemm_experts_handle;
+typedef struct gemm_combine_plan* gemm_combine_handle;
+
+/* Plan of a layer norm over rows of K values,
+ *     mean = sum x / K,  rstd = 1 / sqrt(sum (x - mean)^2 / K + eps)
+ *     Y = (X - mean) * rstd * weight + bias
+ * X, Y [rows,K] of dtype (fp16, bf16, fp32); weight, bias [K] of param_dtype (dtype or fp32),
+ * either NULL for 1 and 0.  Statistics in fp32, the mean subtracted before the squares are
+ * summed; each result rounded once.  A row with an infinity or a NaN gives NaN.
+ * Errors: INVALID_ARG (out NULL, negative size, unknown types, eps negative or not finite),
+ * UNSUPPORTED (a size above 2^30 - 513). */
+gemm_status gemm_norm_create(gemm_norm_handle* out, int64_t rows, int64_t K, gemm_dtype dtype, gemm_dtype param_dtype,
+                             float eps);
+/* Bytes of workspace that gemm_norm_backward needs (-1: NULL handle). */
+int64_t gemm_norm_workspace(gemm_norm_handle h);
+/* mean and rstd [rows] fp32, for the backward pass; both NULL (serving) or both given. */
+gemm_status gemm_norm_run(gemm_norm_handle h, const void* X, const void* weight, const void* bias, void* Y, float* mean,
+                          float* rstd, hipStream_t stream);
+/* With n = (X - mean) * rstd and g = dY * weight:
+ *     dX = rstd * (g - sum g / K - n * sum(g n) / K),  dweight = sum_rows dY n,  dbias = sum_rows dY
+ * dweight and dbias are of param_dtype, summed in fp32; either may be NULL.  Sums over nothing
+ * (rows = 0) write zeros. */
+gemm_status gemm_norm_backward(gemm_norm_handle h, const void* dY, const void* X, const void* weight, const float* mean,
+                               const float* rstd, void* dX, void* dweight, void* dbias, void* workspace,
+                               int64_t workspace_bytes, hipStream_t stream);
+gemm_status gemm_norm_destroy(gemm_norm_handle h);
+
+/* Plan of a routing of `tokens` tokens to k of `experts` experts each.  From logits
+ * [tokens,experts] of dtype (fp16, bf16, fp32):
+ *   - expert [tokens,k] int32: the k largest logits in falling order, equal ones by rising
+ *     index.  A logit of -inf or NaN is never chosen; where fewer than k are left, expert is
+ *     -1 (a token of -inf alone, such as padding, goes to no expert);
+ *   - gate [tokens,k] fp32: softmax over all logits of the token at the chosen ones, or with
+ *     renormalise over the chosen ones alone; 0 where expert is -1.  A NaN or a +inf among a
+ *     token's logits makes all gates of its experts NaN;
+ *   - the chosen (token, j) grouped by expert, within a group by rising token: offsets
+ *     [experts+1] int32 of the groups, slot [tokens,k] int32 the place of (token, j), -1 where
+ *     expert is, and source [tokens*k] int32 the token at each place; places behind the last
+ *     group stay as they are.
+ * 1 <= k <= min(experts, 64), experts <= 1024.
+ * Errors: INVALID_ARG, UNSUPPORTED (more experts, tokens*k or tokens*experts above 2^30). */
+gemm_status gemm_route_create(gemm_route_handle* out, int64_t tokens, int64_t experts, int64_t k, gemm_dtype dtype,
+                              int32_t renormalise);
+int64_t gemm_route_workspace(gemm_route_handle h);
+gemm_status gemm_route_run(gemm_route_handle h, const void* logits, float* gate, int32_t* expert, int32_t* slot,
+                           int32_t* source, int32_t* offsets, void* workspace, int64_t workspace_bytes,
+                           hipStream_t stream);
+/* The logits' gradient [tokens,experts] of dtype from dgate [tokens,k] and the forward pass's logits
+ * and expert: with p the softmax and d the gradient of each p (0 where not chosen),
+ *     dlogits = p * (d - sum p d),
+ * renormalised over the chosen logits alone, the others' 0.  dgate is not read where expert
+ * is -1.  An expert outside 0 .. experts-1 counts as -1. */
+gemm_status gemm_route_backward(gemm_route_handle h, const void* logits, const int32_t* expert, const float* dgate,
+                                void* dlogits, hipStream_t stream);
+gemm_status gemm_route_destroy(gemm_route_handle h);
+
+/* Plan of one product per group: the rows of group e times matrix e,
+ *     Y[r] = X[r] W[e],   X [rows,K], Y [rows,N], W [groups,N,K] (GEMM_B_NK) or [groups,K,N]
+ * all fp16 or all bf16, sums in fp32, each result rounded once.
+ * tokens >= 0: X is [tokens,K] and row r reads X[source[r]], source [rows] int32 (a row may be
+ * read by any number of them; outside 0 .. tokens-1 it counts as a row of zeros); tokens = -1:
+ * X is [rows,K] and source NULL.  `rows` is the most that the groups hold.
+ * Errors: INVALID_ARG (out NULL, negative size, groups < 1, fp32 or unknown dtype or layout),
+ * UNSUPPORTED (a size above 2^30 - 513, groups > 65535). */
+gemm_status gemm_grouped_create(gemm_grouped_handle* out, int64_t rows, int64_t N, int64_t K, int64_t groups,
+                                int64_t tokens, gemm_dtype dtype, gemm_b_layout layout);
+/* Bytes for both passes, and for gemm_grouped_run alone (-1: NULL handle). */
+int64_t gemm_grouped_workspace(gemm_grouped_handle h);
+int64_t gemm_grouped_run_workspace(gemm_grouped_handle h);
+gemm_status gemm_grouped_run(gemm_grouped_handle h, const void* X, const void* W, const int32_t* offsets,
+                             const int32_t* source, void* Y, void* workspace, int64_t workspace_bytes,
+                             hipStream_t stream);
+/* From dY [rows,N]:  dX[r] = dY[r] W[e]^T (always [rows,K]: with a source, what each row
+ * contributes to its token; gemm_combine_run sums them),  dW[e] = X_e^T dY_e (stored as W is;
+ * zeros for an empty group).  Either of dX and dW may be NULL. */
+gemm_status gemm_grouped_backward(gemm_grouped_handle h, const void* dY, const void* X, const void* W,
+                                  const int32_t* offsets, const int32_t* source, void* dX, void* dW, void* workspace,
+                                  int64_t workspace_bytes, hipStream_t stream);
+gemm_status gemm_grouped_destroy(gemm_grouped_handle h);
+
+/* Plan of the gated projection of every group,
+ *     G = X Wg[e],  U = X Wu[e],  H = act(G) * U
+ * X, source and tokens as above; Wg and Wu as W; roundings, G and U as in gemm_gated_run. */
+gemm_status gemm_experts_create(gemm_experts_handle* out, int64_t rows, int64_t N, int64_t K, int64_t groups,
+                                int64_t tokens, gemm_dtype dtype, gemm_b_layout layout, gemm_activation act);
+int64_t gemm_experts_workspace(gemm_experts_handle h);
+int64_t gemm_experts_run_workspace(gemm_experts_handle h);
+gemm_status gemm_experts_run(gemm_experts_handle h, const void* X, const void* Wg, const void* Wu,
+                             const int32_t* offsets, const int32_t* source, void* H, void* G, void* U, void* workspace,
+                             int64_t workspace_bytes, hipStream_t stream);
+/* As gemm_gated_backward, group by group; dX [rows,K] as in gemm_grouped_backward. */
+gemm_status gemm_experts_backward(gemm_experts_handle h, const void* dH, const void* X, const void* Wg, const void* Wu,
+                                  const void* G, const void* U, const int32_t* offsets, const int32_t* source, void* dX,
+                                  void* dWg, void* dWu, void* workspace, int64_t workspace_bytes, hipStream_t stream);
+gemm_status gemm_experts_destroy(gemm_experts_handle h);
+
+/* Plan of the sum that brings the experts' rows back to their tokens,
+ *     out[t] = sum_j gate[t,j] * Y[slot[t,j]]
+ * Y [rows,N] and out [tokens,N] of dtype (fp16, bf16, fp32), slot [tokens,k] int32, gate
+ * [tokens,k] fp32 or NULL (ones: the sum of the rows' input gradients).  A slot outside
+ * 0 .. rows-1 (-1: no expert) contributes nothing, whatever its gate.  Sums in fp32 in the
+ * order of j, rounded once.  1 <= k <= 64. */
+gemm_status gemm_combine_create(gemm_combine_handle* out, int64_t tokens, int64_t k, int64_t rows, int64_t N,
+                                gemm_dtype dtype);
+gemm_status gemm_combine_run(gemm_combine_handle h, const void* Y, const int32_t* slot, const float* gate, void* out,
+                             hipStream_t stream);
+/* From dout [tokens,N]:  dY[slot[t,j]] = gate[t,j] * dout[t] (rows that no slot names stay as they
+ * are; no row may be named twice),  dgate[t,j] = dout[t] . Y[slot[t,j]] in fp32 (0 where the
+ * slot names no row).  dgate NULL: Y may be NULL too. */
+gemm_status gemm_combine_backward(gemm_combine_handle h, const void* dout, const void* Y, const int32_t* slot,
+                                  const float* gate, void* dY, float* dgate, hipStream_t stream);
+gemm_status gemm_combine_destroy(gemm_combine_handle h);
+
 #ifdef __cplusplus
 }
 #endif

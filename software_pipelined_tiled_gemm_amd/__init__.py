@@ -1,5 +1,5 @@
-"""Python binding of the MI355X software-pipelined tiled GEMM and the feed-forward operators
-(C ABI in include/spgemm.h) and of the standalone elementwise GELU (include/spgelu.h).
+"""Python binding of the MI355X software-pipelined tiled GEMM, the feed-forward operators and the
+operators of a mixture of experts (C ABI in include/spgemm.h) and of the standalone elementwise GELU (include/spgelu.h).
 
 Argument marshalling only: every step of C = epi(A . B) runs in the HIP
 kernels of ``libspgemm.so``.  PyTorch is used by callers for device memory and
@@ -84,7 +84,15 @@ EXPORTED = ("gemm_create", "gemm_run", "gemm_destroy", "gemm_get_config", "gemm_
             "gemm_gated_create", "gemm_gated_workspace", "gemm_gated_run_workspace",
             "gemm_gated_run", "gemm_gated_backward",
             "gemm_gated_destroy", "gemm_quantized_create", "gemm_quantized_workspace",
-            "gemm_quantized_run", "gemm_quantized_destroy", "gemm_quantize_rows")
+            "gemm_quantized_run", "gemm_quantized_destroy", "gemm_quantize_rows",
+            "gemm_norm_create", "gemm_norm_workspace", "gemm_norm_run", "gemm_norm_backward", "gemm_norm_destroy",
+            "gemm_route_create", "gemm_route_workspace", "gemm_route_run", "gemm_route_backward",
+            "gemm_route_destroy",
+            "gemm_grouped_create", "gemm_grouped_workspace", "gemm_grouped_run_workspace", "gemm_grouped_run",
+            "gemm_grouped_backward", "gemm_grouped_destroy",
+            "gemm_experts_create", "gemm_experts_workspace", "gemm_experts_run_workspace", "gemm_experts_run",
+            "gemm_experts_backward", "gemm_experts_destroy",
+            "gemm_combine_create", "gemm_combine_run", "gemm_combine_backward", "gemm_combine_destroy")
 
 _lib = None
 _poison_lib = None
@@ -157,7 +165,33 @@ def _load(path):
             ("gemm_quantized_workspace", i64, [vp]),
             ("gemm_quantized_run", en, [vp] * 9 + [i64, vp]),
             ("gemm_quantized_destroy", en, [vp]),
-            ("gemm_quantize_rows", en, [vp, en, i64, i64, vp, vp, vp])):
+            ("gemm_quantize_rows", en, [vp, en, i64, i64, vp, vp, vp]),
+            ("gemm_norm_create", en, [ctypes.POINTER(vp), i64, i64, en, en, ctypes.c_float]),
+            ("gemm_norm_workspace", i64, [vp]),
+            ("gemm_norm_run", en, [vp] * 8),
+            ("gemm_norm_backward", en, [vp] * 10 + [i64, vp]),
+            ("gemm_norm_destroy", en, [vp]),
+            ("gemm_route_create", en, [ctypes.POINTER(vp), i64, i64, i64, en, i32]),
+            ("gemm_route_workspace", i64, [vp]),
+            ("gemm_route_run", en, [vp] * 8 + [i64, vp]),
+            ("gemm_route_backward", en, [vp] * 6),
+            ("gemm_route_destroy", en, [vp]),
+            ("gemm_grouped_create", en, [ctypes.POINTER(vp), i64, i64, i64, i64, i64, en, en]),
+            ("gemm_grouped_workspace", i64, [vp]),
+            ("gemm_grouped_run_workspace", i64, [vp]),
+            ("gemm_grouped_run", en, [vp] * 7 + [i64, vp]),
+            ("gemm_grouped_backward", en, [vp] * 9 + [i64, vp]),
+            ("gemm_grouped_destroy", en, [vp]),
+            ("gemm_experts_create", en, [ctypes.POINTER(vp), i64, i64, i64, i64, i64, en, en, en]),
+            ("gemm_experts_workspace", i64, [vp]),
+            ("gemm_experts_run_workspace", i64, [vp]),
+            ("gemm_experts_run", en, [vp] * 10 + [i64, vp]),
+            ("gemm_experts_backward", en, [vp] * 13 + [i64, vp]),
+            ("gemm_experts_destroy", en, [vp]),
+            ("gemm_combine_create", en, [ctypes.POINTER(vp), i64, i64, i64, i64, en]),
+            ("gemm_combine_run", en, [vp] * 6),
+            ("gemm_combine_backward", en, [vp] * 8),
+            ("gemm_combine_destroy", en, [vp])):
         f = getattr(L, name)
         f.restype, f.argtypes = res, args
     return L
@@ -395,7 +429,8 @@ def _torch_names():
     global _names, _types
     if _names is None:
         import torch
-        _names = {torch.float16: "f16", torch.bfloat16: "bf16", torch.float32: "f32", torch.int8: "i8"}
+        _names = {torch.float16: "f16", torch.bfloat16: "bf16", torch.float32: "f32", torch.int8: "i8",
+                  torch.int32: "i32"}
         _types = {v: k for k, v in _names.items()}
     return _names
 
@@ -491,11 +526,11 @@ def _raw(stream):
 
 def _specs(*tensors) -> bytes:
     """(dtype, shape) of each tensor of a call as csrc/binding.cpp reads them."""
-    codes = {"f16": (2, 16), "bf16": (4, 16), "f32": (2, 32), "i8": (0, 8)}   # DLPack's
+    codes = {"f16": (2, 16), "bf16": (4, 16), "f32": (2, 32), "i8": (0, 8), "i32": (0, 32)}   # DLPack's
     out = b""
     for dtype, shape in tensors:
         code, bits = codes[dtype]
-        out += struct.pack("4i2q", code, bits, len(shape), 0, *shape, *[0] * (2 - len(shape)))
+        out += struct.pack("4i3q", code, bits, len(shape), 0, *shape, *[0] * (3 - len(shape)))
     return out
 
 
@@ -654,6 +689,248 @@ class QuantizedGemm:
             self.close()
         except Exception:
             pass
+
+
+# ---- the operators of a mixture of experts ----------------------------------------------
+
+class _Entry:
+    """One C entry point of a plan: the tensors it takes, checked and passed on."""
+
+    def __init__(self, name: str, what: str, tensors, scratch: Optional[int] = None):
+        # tensors: (name, dtype, shape) in the C order; scratch: the workspace's bytes, None for
+        # an entry point without one
+        self.name, self.what, self.scratch = name, what, scratch
+        self.fn = getattr(lib(), name)
+        self.names = [(n, _torch_type(d), s) for n, d, s in tensors]
+        self.calls = _calls_module()
+        if self.calls is not None:
+            L = lib()
+            # the HIP runtime's own, found through the library that is linked to it
+            self.raw = _address(self.fn), _specs(*((d, s) for _, d, s in tensors))
+            self.device = _address(L.hipGetDevice), _address(L.hipSetDevice)
+
+    def __call__(self, handle, tensors, workspace, stream):
+        if self.calls is not None:
+            fn, spec = self.raw
+            st = self.calls.call(fn, handle, spec, tensors, False if self.scratch is None else workspace, _raw(stream),
+                                 *self.device)
+            if st >= 0:
+                if st:
+                    _check(st, self.name)
+                return
+        dev, p = _dense(self.what, *((n, t, d, s) for (n, d, s), t in zip(self.names, tensors)))
+        ws = () if self.scratch is None else _scratch(self.what, workspace, device=dev, raw=self.scratch)
+        st = _on_device(dev, lambda: self.fn(handle, *p, *ws, _stream_on(stream, dev)))
+        if st:
+            _check(st, self.name)
+
+
+def _on_device(device: Optional[int], call):
+    """call() with the tensors' device as the current one: kernels start on the current device."""
+    if device is None:
+        return call()
+    import torch
+    if not torch.cuda.is_available() or torch.cuda.current_device() == device:
+        return call()
+    with torch.cuda.device(device):
+        return call()
+
+
+def _create(name: str, *args) -> int:
+    h = ctypes.c_void_p()
+    _check(getattr(lib(), name)(ctypes.byref(h), *args), name)
+    return int(h.value)
+
+
+class _Plan:
+    """A plan's handle and its end."""
+
+    handle, _destroy = 0, ""
+
+    def close(self):
+        if self.handle:
+            h, self.handle = self.handle, 0
+            _check(getattr(lib(), self._destroy)(h), self._destroy)
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class LayerNorm(_Plan):
+    """Layer norm of rows and its backward pass (gemm_norm_* in include/spgemm.h).
+
+    X, Y [rows,K] of ``dtype``; weight, bias [K] of ``param_dtype`` ("f32", or X's type, which is
+    the default), or None.  Pass mean and rstd [rows] fp32 to keep them for ``backward``, whose
+    workspace has ``workspace_bytes()``."""
+
+    _destroy = "gemm_norm_destroy"
+
+    def __init__(self, rows, K, dtype="bf16", param_dtype=None, eps=1e-5):
+        param_dtype = param_dtype or dtype
+        self.rows, self.K, self.dtype, self.param_dtype, self.eps = rows, K, dtype, param_dtype, eps
+        self.handle = _create("gemm_norm_create", rows, K, DTYPES[dtype], DTYPES[param_dtype], eps)
+        x, p, r = (dtype, (rows, K)), (param_dtype, (K,)), ("f32", (rows,))
+        self._run = _Entry("gemm_norm_run", "LayerNorm",
+                           (("X", *x), ("weight", *p), ("bias", *p), ("Y", *x), ("mean", *r), ("rstd", *r)))
+        self._back = _Entry("gemm_norm_backward", "LayerNorm.backward",
+                            (("dY", *x), ("X", *x), ("weight", *p), ("mean", *r), ("rstd", *r), ("dX", *x),
+                             ("dweight", *p), ("dbias", *p)), self.workspace_bytes())
+
+    def workspace_bytes(self) -> int:
+        return int(lib().gemm_norm_workspace(self.handle))
+
+    def __call__(self, X, weight, bias, Y, mean=None, rstd=None, stream=None):
+        self._run(self.handle, (X, weight, bias, Y, mean, rstd), None, stream)
+        return Y
+
+    def backward(self, dY, X, weight, mean, rstd, dX, dweight=None, dbias=None, workspace=None, stream=None):
+        self._back(self.handle, (dY, X, weight, mean, rstd, dX, dweight, dbias), workspace, stream)
+        return dX, dweight, dbias
+
+
+class Router(_Plan):
+    """k of E experts for every token, and the chosen rows grouped by expert (gemm_route_* in
+    include/spgemm.h).
+
+    logits [tokens,experts] of ``dtype``; gate [tokens,k] fp32, expert and slot [tokens,k], source
+    [tokens*k] and offsets [experts+1] int32.  Offsets and source are what ``GroupedGemm`` and
+    ``GroupedGated`` take, slot and gate what ``Combine`` takes.  Logits of -inf are never chosen
+    (expert and slot -1, gate 0): padding has them throughout."""
+
+    _destroy = "gemm_route_destroy"
+
+    def __init__(self, tokens, experts, k, dtype="f32", renormalise=False):
+        self.tokens, self.experts, self.k, self.dtype, self.renormalise = tokens, experts, k, dtype, renormalise
+        self.handle = _create("gemm_route_create", tokens, experts, k, DTYPES[dtype], 1 if renormalise else 0)
+        x, tk = (dtype, (tokens, experts)), (tokens, k)
+        self._run = _Entry("gemm_route_run", "Router",
+                           (("logits", *x), ("gate", "f32", tk), ("expert", "i32", tk), ("slot", "i32", tk),
+                            ("source", "i32", (tokens * k,)), ("offsets", "i32", (experts + 1,))), self.workspace_bytes())
+        self._back = _Entry("gemm_route_backward", "Router.backward",
+                            (("logits", *x), ("expert", "i32", tk), ("dgate", "f32", tk), ("dlogits", *x)))
+
+    def workspace_bytes(self) -> int:
+        return int(lib().gemm_route_workspace(self.handle))
+
+    def __call__(self, logits, gate, expert, slot, source, offsets, workspace=None, stream=None):
+        self._run(self.handle, (logits, gate, expert, slot, source, offsets), workspace, stream)
+        return gate, expert, slot, source, offsets
+
+    def backward(self, logits, expert, dgate, dlogits, stream=None):
+        self._back(self.handle, (logits, expert, dgate, dlogits), None, stream)
+        return dlogits
+
+
+class _Grouped(_Plan):
+    """What the products by group share: sizes, shapes, workspaces."""
+
+    _kind = ""
+
+    def _shapes(self, rows, N, K, groups, dtype, layout, tokens):
+        self.rows, self.N, self.K, self.groups = rows, N, K, groups
+        self.dtype, self.layout, self.tokens = dtype, layout, tokens
+        x = (dtype, (rows if tokens is None else tokens, K))
+        w = (dtype, (groups, N, K) if layout == "nk" else (groups, K, N))
+        return x, w, ("offsets", "i32", (groups + 1,)), ("source", "i32", (rows,)), (dtype, (rows, N)), (dtype, (rows, K))
+
+    def workspace_bytes(self, backward: bool = True) -> int:
+        """Bytes for the plan's calls; without ``backward`` for the products of the forward pass alone."""
+        return int(getattr(lib(), f"gemm_{self._kind}_{'' if backward else 'run_'}workspace")(self.handle))
+
+
+class GroupedGemm(_Grouped):
+    """The rows of every group times the group's matrix, and the backward pass (gemm_grouped_* in
+    include/spgemm.h).
+
+    Group e is rows offsets[e] .. offsets[e+1] - 1; offsets [groups+1] int32 on the GPU.  X
+    [rows,K], W [groups,N,K] ("nk") or [groups,K,N] ("kn"), Y [rows,N].  With ``tokens``, X is
+    [tokens,K] and row r reads X[source[r]], source [rows] int32.  ``workspace`` as in ``Gated``."""
+
+    _kind, _destroy = "grouped", "gemm_grouped_destroy"
+
+    def __init__(self, rows, N, K, groups, dtype="bf16", layout="nk", tokens=None):
+        self.handle = _create("gemm_grouped_create", rows, N, K, groups, -1 if tokens is None else tokens, DTYPES[dtype],
+                              B_LAYOUTS[layout])
+        x, w, off, src, y, dx = self._shapes(rows, N, K, groups, dtype, layout, tokens)
+        self._run = _Entry("gemm_grouped_run", "GroupedGemm", (("X", *x), ("W", *w), off, src, ("Y", *y)),
+                           self.workspace_bytes(backward=False))
+        self._back = _Entry("gemm_grouped_backward", "GroupedGemm.backward",
+                            (("dY", *y), ("X", *x), ("W", *w), off, src, ("dX", *dx), ("dW", *w)), self.workspace_bytes())
+
+    def __call__(self, X, W, offsets, Y, source=None, workspace=None, stream=None):
+        self._run(self.handle, (X, W, offsets, source, Y), workspace, stream)
+        return Y
+
+    def backward(self, dY, X, W, offsets, dX, dW, source=None, workspace=None, stream=None):
+        self._back(self.handle, (dY, X, W, offsets, source, dX, dW), workspace, stream)
+        return dX, dW
+
+
+class GroupedGated(_Grouped):
+    """The gated projection H = act(X Wg[e]) * (X Wu[e]) of every group's rows, and its backward
+    pass (gemm_experts_* in include/spgemm.h): ``Gated`` for a mixture of experts.
+
+    Rows, offsets, source and weights as in ``GroupedGemm``; G, U and ``workspace`` as in
+    ``Gated``.  dX is [rows,K]: ``Combine`` without gates sums it over a token's rows."""
+
+    _kind, _destroy = "experts", "gemm_experts_destroy"
+
+    def __init__(self, rows, N, K, groups, dtype="bf16", layout="nk", act="silu", tokens=None):
+        self.act = act
+        self.handle = _create("gemm_experts_create", rows, N, K, groups, -1 if tokens is None else tokens, DTYPES[dtype],
+                              B_LAYOUTS[layout], ACTIVATIONS[act])
+        x, w, off, src, h, dx = self._shapes(rows, N, K, groups, dtype, layout, tokens)
+        wg, wu = ("Wg", *w), ("Wu", *w)
+        self._run = _Entry("gemm_experts_run", "GroupedGated",
+                           (("X", *x), wg, wu, off, src, ("H", *h), ("G", *h), ("U", *h)),
+                           self.workspace_bytes(backward=False))
+        self._back = _Entry("gemm_experts_backward", "GroupedGated.backward",
+                            (("dH", *h), ("X", *x), wg, wu, ("G", *h), ("U", *h), off, src, ("dX", *dx), ("dWg", *w),
+                             ("dWu", *w)), self.workspace_bytes())
+
+    def __call__(self, X, Wg, Wu, offsets, H, source=None, G=None, U=None, workspace=None, stream=None):
+        self._run(self.handle, (X, Wg, Wu, offsets, source, H, G, U), workspace, stream)
+        return H
+
+    def backward(self, dH, X, Wg, Wu, G, U, offsets, dX, dWg, dWu, source=None, workspace=None, stream=None):
+        self._back(self.handle, (dH, X, Wg, Wu, G, U, offsets, source, dX, dWg, dWu), workspace, stream)
+        return dX, dWg, dWu
+
+
+class Combine(_Plan):
+    """out[t] = sum over j of gate[t,j] Y[slot[t,j]], and its backward pass (gemm_combine_* in
+    include/spgemm.h): the experts' rows back to their tokens.
+
+    Y [rows,N] and out [tokens,N] of ``dtype``, slot [tokens,k] int32 (-1: no row), gate [tokens,k]
+    fp32 or None for ones."""
+
+    _destroy = "gemm_combine_destroy"
+
+    def __init__(self, tokens, k, rows, N, dtype="bf16"):
+        self.tokens, self.k, self.rows, self.N, self.dtype = tokens, k, rows, N, dtype
+        self.handle = _create("gemm_combine_create", tokens, k, rows, N, DTYPES[dtype])
+        y, o, tk = (dtype, (rows, N)), (dtype, (tokens, N)), (tokens, k)
+        self._run = _Entry("gemm_combine_run", "Combine", (("Y", *y), ("slot", "i32", tk), ("gate", "f32", tk), ("out", *o)))
+        self._back = _Entry("gemm_combine_backward", "Combine.backward",
+                            (("dout", *o), ("Y", *y), ("slot", "i32", tk), ("gate", "f32", tk), ("dY", *y),
+                             ("dgate", "f32", tk)))
+
+    def __call__(self, Y, slot, gate, out, stream=None):
+        self._run(self.handle, (Y, slot, gate, out), None, stream)
+        return out
+
+    def backward(self, dout, Y, slot, gate, dY, dgate=None, stream=None):
+        self._back(self.handle, (dout, Y, slot, gate, dY, dgate), None, stream)
+        return dY, dgate
 
 
 class Gemm:

@@ -6,7 +6,8 @@ number (with -DSPG_UNIT_IS_<n>=~,1 selecting that unit's lines), so the units co
 in parallel.  csrc/gemm.hip holds the GEMM's host side (C ABI, variant table) and
 csrc/gelu.hip the standalone elementwise GELU (include/spgelu.h).  The feed-forward
 operators are csrc/product.hip (host side) and csrc/product_unit.hip, compiled once per
-element type, product and copy mode.  csrc/binding.cpp becomes a module of its own,
+element type, product and copy mode.  The operators of a mixture of experts are csrc/norm.hip,
+csrc/route.hip (with the combination) and csrc/grouped.hip.  csrc/binding.cpp becomes a module of its own,
 _calls.so, where torch is installed.
 """
 
@@ -72,7 +73,10 @@ def build(out: str = OUT, extra=(), poison: bool = False) -> str:
     # (source, object name, defines): the host side, the GELU, and one object per unit
     jobs = [(os.path.join(CSRC, "gemm.hip"), "gemm.o", pdef + keep),
             (os.path.join(CSRC, "gelu.hip"), "gelu.o", []),
-            (os.path.join(CSRC, "product.hip"), "product.o", pdef)]
+            (os.path.join(CSRC, "product.hip"), "product.o", pdef),
+            (os.path.join(CSRC, "norm.hip"), "norm.o", []),
+            (os.path.join(CSRC, "route.hip"), "route.o", []),
+            (os.path.join(CSRC, "grouped.hip"), "grouped.o", pdef)]
     jobs += [(os.path.join(CSRC, "product_unit.hip"), f"product_unit_{et}_{p}_{reg}.o",
               pdef + [f"-DSPG_ET={et}", f"-DSPG_PRODUCT={p}", f"-DSPG_REG={reg}"])
              for et, p, reg in product_units()]

@@ -15,15 +15,17 @@
 
 #include <stdint.h>
 
+#include <utility>
+
 namespace {
 
 const DLPackExchangeAPI* g_api = nullptr;
 PyTypeObject* g_types[2] = {nullptr, nullptr};   // torch.Tensor, torch.nn.Parameter
 
-// What a plan expects of one tensor (packed by the wrapper with struct "4i2q")
+// What a plan expects of one tensor (packed by the wrapper with struct "4i3q")
 struct Spec {
     int32_t code, bits, ndim, unused;
-    int64_t dim[2];
+    int64_t dim[3];
 };
 
 // The tensor behind `o`; false with no Python error set if it is not one that can be read here
@@ -121,6 +123,91 @@ PyObject* run(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return PyLong_FromLong(r);
 }
 
+// The pointers of a plan's tensors (null for None); false if one is not what its spec says, or
+// none is a tensor
+bool pointers(PyObject* tuple, const Spec* spec, Py_ssize_t m, void** p, DLDevice* dev) {
+    dev->device_id = -1;
+    DLTensor t;
+    for (Py_ssize_t i = 0; i < m; ++i) {
+        PyObject* o = PyTuple_GET_ITEM(tuple, i);
+        p[i] = nullptr;
+        if (o == Py_None) continue;
+        const Spec& s = spec[i];
+        if (!view(o, &t) || !typed(t, s.code, s.bits) || t.ndim != s.ndim) return false;
+        for (int d = 0; d < s.ndim; ++d)
+            if (t.shape[d] != s.dim[d]) return false;
+        if (!dense(t)) return false;
+        if (dev->device_id < 0) *dev = t.device;
+        else if (dev->device_id != t.device.device_id) return false;
+        p[i] = data_of(t);
+    }
+    return dev->device_id >= 0;
+}
+
+template <size_t I>
+using Ptr = void*;
+
+// fn(h, p[0] .. p[n-1], stream), or with a workspace and its bytes before the stream
+template <size_t... I>
+int invoke(std::index_sequence<I...>, void* fn, void* h, void** p, bool scratch, void* ws, int64_t bytes, void* st) {
+    if (scratch) return ((int (*)(void*, Ptr<I>..., void*, int64_t, void*))fn)(h, p[I]..., ws, bytes, st);
+    return ((int (*)(void*, Ptr<I>..., void*))fn)(h, p[I]..., st);
+}
+
+typedef int (*GetDevice)(int*);
+typedef int (*SetDevice)(int);
+
+// call(fn, handle, specs, tensors, workspace or False, stream, hipGetDevice, hipSetDevice)
+// -> status, or -1: nothing called.  For entry points with 4 to 11 tensors; the launch is made
+// with the tensors' device as the current one.
+PyObject* call(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (n != 8) {
+        PyErr_SetString(PyExc_TypeError, "call takes 8 arguments");
+        return nullptr;
+    }
+    void* fn = PyLong_AsVoidPtr(a[0]);
+    void* h = PyLong_AsVoidPtr(a[1]);
+    const GetDevice get = (GetDevice)PyLong_AsVoidPtr(a[6]);
+    const SetDevice set = (SetDevice)PyLong_AsVoidPtr(a[7]);
+    if (PyErr_Occurred()) return nullptr;
+    const Py_ssize_t m = PyTuple_CheckExact(a[3]) ? PyTuple_GET_SIZE(a[3]) : -1;
+    if (!PyBytes_CheckExact(a[2]) || m < 4 || m > 11 || PyBytes_GET_SIZE(a[2]) != m * (Py_ssize_t)sizeof(Spec)) {
+        PyErr_SetString(PyExc_TypeError, "call: 4 to 11 tensors and a spec for each");
+        return nullptr;
+    }
+    void* p[11];
+    DLDevice dev{kDLCPU, -1};
+    if (!pointers(a[3], (const Spec*)PyBytes_AS_STRING(a[2]), m, p, &dev)) return PyLong_FromLong(-1);
+    const bool scratch = a[4] != Py_False;
+    void* ws = nullptr;
+    int64_t bytes = 0;
+    if (scratch && a[4] != Py_None) {
+        DLTensor t;
+        if (!view(a[4], &t) || !dense(t) || t.device.device_id != dev.device_id) return PyLong_FromLong(-1);
+        bytes = (t.dtype.bits * t.dtype.lanes) / 8;
+        for (int d = 0; d < t.ndim; ++d) bytes *= t.shape[d];
+        if (bytes > 0) ws = data_of(t);
+    }
+    void* st = nullptr;
+    if (!stream_of(a[5], dev, &st)) return PyLong_FromLong(-1);
+    int now = -1;
+    const bool other = get(&now) == 0 && now != dev.device_id;
+    if (other && set(dev.device_id) != 0) return PyLong_FromLong(-1);
+    int r = 0;
+    switch (m) {
+        case 4: r = invoke(std::make_index_sequence<4>{}, fn, h, p, scratch, ws, bytes, st); break;
+        case 5: r = invoke(std::make_index_sequence<5>{}, fn, h, p, scratch, ws, bytes, st); break;
+        case 6: r = invoke(std::make_index_sequence<6>{}, fn, h, p, scratch, ws, bytes, st); break;
+        case 7: r = invoke(std::make_index_sequence<7>{}, fn, h, p, scratch, ws, bytes, st); break;
+        case 8: r = invoke(std::make_index_sequence<8>{}, fn, h, p, scratch, ws, bytes, st); break;
+        case 9: r = invoke(std::make_index_sequence<9>{}, fn, h, p, scratch, ws, bytes, st); break;
+        case 10: r = invoke(std::make_index_sequence<10>{}, fn, h, p, scratch, ws, bytes, st); break;
+        default: r = invoke(std::make_index_sequence<11>{}, fn, h, p, scratch, ws, bytes, st); break;
+    }
+    if (other) set(now);
+    return PyLong_FromLong(r);
+}
+
 typedef int (*FnRows)(const void*, int, int64_t, int64_t, void*, void*, void*);
 
 // rows(fn, X, A, scale, stream) -> status of gemm_quantize_rows, or -1: nothing called
@@ -173,6 +260,7 @@ PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyMethodDef g_methods[] = {
     {"setup", (PyCFunction)(void (*)(void))setup, METH_FASTCALL, nullptr},
     {"run", (PyCFunction)(void (*)(void))run, METH_FASTCALL, nullptr},
+    {"call", (PyCFunction)(void (*)(void))call, METH_FASTCALL, nullptr},
     {"rows", (PyCFunction)(void (*)(void))rows, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

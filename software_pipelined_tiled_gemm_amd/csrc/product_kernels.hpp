@@ -315,7 +315,7 @@ struct ProductGeom {
     static_assert(!DEEP || S == 2, "the B-deep ring has two A and three B slots");
 };
 
-// The tiled kernel.  One workgroup owns a BM x BN tile and one part of the reduction,
+// The tiled kernel.  One workgroup owns a BM x BN tile (tm, tn) and one part (sp) of the reduction,
 // keeps the sums in registers and streams k-tiles through a ring of LDS slots.
 //   A_T   A is stored [K,M] (the weight gradients), read through the transposing LDS read
 //   B_N   B is stored [K,N], else [N,K]
@@ -341,7 +341,7 @@ struct ProductGeom {
 // multiplied: a 0 * inf could not be undone.
 template <int ET, bool A_T, bool B_N, bool DUAL, bool SEG, bool REG, int BM, int BN, int WM, int WN,
           int S, bool DEEP, int KG, bool TAIL>
-__device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, SPG_LDS char* lds) {
+__device__ __forceinline__ void product_tile_of(ProductArgs args, int tm, int tn, int sp, SPG_LDS char* lds) {
     using G = ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP, KG>;
     constexpr int TM = G::TM, TN = G::TN, BNS = G::BNS, WNS = G::WNS, NW = G::NW;
     constexpr int A_OPS = G::A_OPS, B_OPS = G::B_OPS, L = G::L;
@@ -371,8 +371,6 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, const int wg, 
         __syncthreads();
     }
 
-    int tm, tn, sp;
-    product_tile(wg, args, tm, tn, sp);
     int z = 0;
     if (tm >= args.tiles_m) { tm -= args.tiles_m; z = 1; }
     if (tn >= args.tiles_n) { tn -= args.tiles_n; z = 1; }
@@ -892,7 +890,9 @@ template <int ET, bool A_T, bool B_N, bool DUAL, bool SEG, bool REG, int BM, int
 __global__ void __launch_bounds__((ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP, KG>::NT), WPS)
 product_kernel(ProductArgs args) {
     __shared__ __attribute__((aligned(1024))) char lds[ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP, KG>::LDS];
-    product_tile_of<ET, A_T, B_N, DUAL, SEG, REG, BM, BN, WM, WN, S, DEEP, KG, TAIL>(args, blockIdx.x, (SPG_LDS char*)lds);
+    int tm, tn, sp;
+    product_tile(blockIdx.x, args, tm, tn, sp);
+    product_tile_of<ET, A_T, B_N, DUAL, SEG, REG, BM, BN, WM, WN, S, DEEP, KG, TAIL>(args, tm, tn, sp, (SPG_LDS char*)lds);
 }
 
 // The input gradient and the weights' gradients of a small training step in one launch:
@@ -903,8 +903,14 @@ __global__ void __launch_bounds__((ProductGeom<false, BM, BN, WM, WN, S, false, 
 gradients_kernel(ProductArgs x, ProductArgs w, int nx) {
     __shared__ __attribute__((aligned(1024))) char lds[ProductGeom<false, BM, BN, WM, WN, S, false, KG>::LDS];
     const int wg = blockIdx.x;
-    if (wg < nx) product_tile_of<ET, false, NK, false, true, REG, BM, BN, WM, WN, S, false, KG, true>(x, wg, (SPG_LDS char*)lds);
-    else product_tile_of<ET, true, true, false, false, REG, BM, BN, WM, WN, S, false, KG, true>(w, wg - nx, (SPG_LDS char*)lds);
+    int tm, tn, sp;
+    if (wg < nx) {
+        product_tile(wg, x, tm, tn, sp);
+        product_tile_of<ET, false, NK, false, true, REG, BM, BN, WM, WN, S, false, KG, true>(x, tm, tn, sp, (SPG_LDS char*)lds);
+    } else {
+        product_tile(wg - nx, w, tm, tn, sp);
+        product_tile_of<ET, true, true, false, false, REG, BM, BN, WM, WN, S, false, KG, true>(w, tm, tn, sp, (SPG_LDS char*)lds);
+    }
 }
 
 // ---------------------------------------------------------------------------
