@@ -7,7 +7,8 @@ in parallel.  csrc/gemm.hip holds the GEMM's host side (C ABI, variant table) an
 csrc/gelu.hip the standalone elementwise GELU (include/spgelu.h).  The feed-forward
 operators are csrc/product.hip (host side) and csrc/product_unit.hip, compiled once per
 element type, product and copy mode.  The operators of a mixture of experts are csrc/norm.hip,
-csrc/route.hip (with the combination) and csrc/grouped.hip.  csrc/binding.cpp becomes a module of its own,
+csrc/route.hip (with the combination) and csrc/grouped.hip, the last with csrc/grouped_unit.hip,
+again once per element type, product and copy mode.  csrc/binding.cpp becomes a module of its own,
 _calls.so, where torch is installed.
 """
 
@@ -64,6 +65,12 @@ def product_units() -> list:
     return [(et, p, reg) for et, p in pairs for reg in (0, 1)]
 
 
+def grouped_units() -> list:
+    """(element type, product, copy mode) of every grouped_unit.hip object: the enum of
+    csrc/grouped_launch.hpp in fp16 and bf16, with direct copies and register-staged."""
+    return [(et, p, reg) for p in range(7) for et in (0, 1) for reg in (0, 1)]
+
+
 def build(out: str = OUT, extra=(), poison: bool = False) -> str:
     """Compile the library; poison=True builds the poison library from POISON_UNITS."""
     unit_src = os.path.join(CSRC, "gemm_unit.hip")
@@ -80,6 +87,9 @@ def build(out: str = OUT, extra=(), poison: bool = False) -> str:
     jobs += [(os.path.join(CSRC, "product_unit.hip"), f"product_unit_{et}_{p}_{reg}.o",
               pdef + [f"-DSPG_ET={et}", f"-DSPG_PRODUCT={p}", f"-DSPG_REG={reg}"])
              for et, p, reg in product_units()]
+    jobs += [(os.path.join(CSRC, "grouped_unit.hip"), f"grouped_unit_{et}_{p}_{reg}.o",
+              pdef + [f"-DSPG_ET={et}", f"-DSPG_PRODUCT={p}", f"-DSPG_REG={reg}"])
+             for et, p, reg in grouped_units()]
     jobs += [(unit_src, f"gemm_unit{u}.o", pdef + [f"-DSPG_UNIT_IS_{u}=~,1"]) for u in us]
     inc = ["-I", os.path.join(ROOT, "include"), "-I", CSRC]
     with tempfile.TemporaryDirectory(prefix="spgemm_build_") as tmp:

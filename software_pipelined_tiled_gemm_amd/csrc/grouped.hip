@@ -7,11 +7,16 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <cmath>
 #include <new>
 
 #include "errors.hpp"
-#include "grouped_kernels.hpp"
+#include "grouped_launch.hpp"
 #include "spgemm.h"
+#include "tile_cost.hpp"
+
+using spg::GroupArgs;
+using spg::ProductArgs;
 
 namespace {
 
@@ -19,16 +24,33 @@ constexpr int64_t kAlign = 256;   // sections of a workspace
 int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// direct copies read from 4-byte aligned addresses
+bool words(const void* p) { return (uintptr_t)p % 4 == 0; }
+
 gemm_status launched() {
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? GEMM_OK : spg::hip_fail(e);
 }
 
-// Sizes, layouts and workspaces that the plain and the gated products share.
+// a launch has less than 2^32 threads along one axis
+dim3 spread(int64_t wgs) {
+    const int64_t x = std::min<int64_t>(wgs, 1 << 21);
+    return dim3((unsigned)x, (unsigned)ceil_div(wgs, x));
+}
+
+// Rows of operands are addressed by 32-bit offsets below 2^31: 256 of them fit up to here.
+constexpr int64_t kMaxRowBytes = ((int64_t)1 << 23) - 128;
+constexpr int64_t kMaxBytes = (int64_t)1 << 31;
+
+// Sizes and layouts that the plain and the gated products share.
 struct Common {
     int64_t rows, N, K, groups, tokens;   // tokens -1: no source
     bool bf, nk;
     int64_t matrix() const { return N * K * 2; }
+    int64_t live() const { return std::max<int64_t>(1, std::min(groups, rows)); }   // groups that may have rows
+    // the copy of X in the groups' order
+    int64_t pitch() const { return up(K * 2, 128); }
+    int64_t gathered() const { return tokens < 0 ? 0 : up(rows * pitch(), kAlign); }
 };
 
 gemm_status check(const void* out, int64_t rows, int64_t N, int64_t K, int64_t groups, int64_t tokens, gemm_dtype dtype,
@@ -41,19 +63,180 @@ gemm_status check(const void* out, int64_t rows, int64_t N, int64_t K, int64_t g
     return GEMM_OK;
 }
 
-spg::GroupArgs group_args(const Common& c, const int32_t* offsets, const int32_t* source, int64_t b_step) {
-    return spg::GroupArgs{offsets, source, b_step, (int32_t)c.groups, (int32_t)c.rows, (int32_t)std::max<int64_t>(c.tokens, 0)};
+bool wrong_source(const Common& c, const void* source) { return c.rows > 0 && (c.tokens < 0) != (source == nullptr); }
+
+bool small_workspace(const void* workspace, int64_t bytes, int64_t need) {
+    return need > 0 && (!workspace || (uintptr_t)workspace % 16 != 0 || bytes < need);
+}
+
+GroupArgs group_args(const Common& c, const int32_t* offsets, const int32_t* source) {
+    return GroupArgs{offsets, source, c.matrix(), (int32_t)c.groups, (int32_t)c.rows, (int32_t)std::max<int64_t>(c.tokens, 0)};
+}
+
+// ---- the choice of kernel --------------------------------------------------------------
+
+// Products of all groups' rows with their matrices: `mats` B side by side in a tile, `kt` k-tiles.
+struct RowsShape {
+    int64_t rows, live, N, kt;
+    int mats;
+    double bytes;
+    bool crooked;
+};
+
+// Row tiles of BM rows: the last tile of a group is half full on average.
+double row_tiles(const RowsShape& s, int BM) {
+    return std::max((double)s.live, (double)s.rows / BM + 0.5 * (double)s.live);
+}
+
+// Microseconds of a grid of `wgs` workgroups of tile class t, `kt` k-tiles each
+double grid_us(int t, bool reg, bool crooked, double wgs, double kt, double bytes) {
+    const double rounds = std::max(1.0, wgs / spg::slots(t, reg) + 0.3);
+    const double us = rounds * (spg::tile_us(t, reg, crooked, (int64_t)wgs) * kt + spg::start_us(t, reg, (int64_t)wgs));
+    return spg::kLaunchUs + std::max(us, 3.0 + bytes / 5.0e6);
+}
+
+bool staged(int t) { return t != spg::kTileBig && t != spg::kTilePair; }   // tiles that stage through registers
+
+int choose_rows(const RowsShape& s, bool reg) {
+    int best = spg::kTileNarrow;
+    double best_us = 1e30;
+    for (int t = 0; t < spg::kTiles; ++t) {
+        if (reg && !staged(t)) continue;
+        const double wgs = row_tiles(s, spg::kTileM[t]) * (double)ceil_div(s.N, spg::kTileN[t] / s.mats);
+        const double us = grid_us(t, reg, s.crooked, wgs, (double)s.kt, s.bytes);
+        if (us < best_us) {
+            best_us = us;
+            best = t;
+        }
+    }
+    return best;
+}
+
+int choose_weights(const Common& c, int mats, bool reg) {
+    int best = spg::kTileNarrow;
+    double best_us = 1e30;
+    const double kt = (double)c.rows / (double)c.groups / 64.0 + 0.5;
+    const bool crooked = c.N % 64 != 0 || c.K % 64 != 0;
+    for (int t = 0; t < spg::kTiles; ++t) {
+        if (reg && !staged(t)) continue;
+        const int64_t m = c.nk ? c.N : c.K, n = c.nk ? c.K : c.N;
+        const double wgs = (double)c.groups * mats * (double)(ceil_div(m, spg::kTileM[t]) * ceil_div(n, spg::kTileN[t]));
+        const double us = grid_us(t, reg, crooked, wgs, kt, 2.0 * mats * c.N * c.K * c.groups);
+        if (us < best_us) {
+            best_us = us;
+            best = t;
+        }
+    }
+    return best;
+}
+
+// ---- launches --------------------------------------------------------------------------
+
+template <int P>
+void launch_product(bool bf, bool reg, int tile, const ProductArgs& a, const GroupArgs& g, int per, dim3 grid, hipStream_t st) {
+    if (bf) {
+        if (reg) spg::launch_grouped<spg::kElBF16, P, true>(tile, a, g, per, grid, st);
+        else spg::launch_grouped<spg::kElBF16, P, false>(tile, a, g, per, grid, st);
+    } else {
+        if (reg) spg::launch_grouped<spg::kElF16, P, true>(tile, a, g, per, grid, st);
+        else spg::launch_grouped<spg::kElF16, P, false>(tile, a, g, per, grid, st);
+    }
+}
+
+void launch_any(int product, bool bf, bool reg, int tile, const ProductArgs& a, const GroupArgs& g, int per, dim3 grid,
+                hipStream_t st) {
+    switch (product) {
+        case spg::kRowsGatedNK: return launch_product<spg::kRowsGatedNK>(bf, reg, tile, a, g, per, grid, st);
+        case spg::kRowsGatedKN: return launch_product<spg::kRowsGatedKN>(bf, reg, tile, a, g, per, grid, st);
+        case spg::kRowsSumNK: return launch_product<spg::kRowsSumNK>(bf, reg, tile, a, g, per, grid, st);
+        case spg::kRowsSumKN: return launch_product<spg::kRowsSumKN>(bf, reg, tile, a, g, per, grid, st);
+        case spg::kRowsNK: return launch_product<spg::kRowsNK>(bf, reg, tile, a, g, per, grid, st);
+        case spg::kRowsKN: return launch_product<spg::kRowsKN>(bf, reg, tile, a, g, per, grid, st);
+        default: return launch_product<spg::kGroupWeights>(bf, reg, tile, a, g, per, grid, st);
+    }
+}
+
+constexpr int32_t kWhole = 1 << 28;   // k-tiles of a part: the reduction is not split
+
+// rows of tiles rastered together, as set_grid in product.hip
+uint8_t raster_rows(int64_t rows) { return (uint8_t)(rows <= 8 ? std::max<int64_t>(rows, 1) : 4); }
+
+gemm_status run_rows(int product, const Common& c, bool reg, int tile, int mats, ProductArgs a, const int32_t* offsets,
+                     hipStream_t st) {
+    GroupArgs g = group_args(c, offsets, nullptr);
+    a.zm = a.zn = a.split = 1;
+    a.kt_part = kWhole;
+    const int BM = spg::kTileM[tile];
+    // every group with rows has at most one tile that is not full
+    const int64_t tiles = (c.rows - c.live()) / BM + c.live();
+    a.tiles_m = 0;   // found on the device
+    a.tiles_n = (int32_t)ceil_div(a.N, spg::kTileN[tile] / mats);
+    a.group_m = raster_rows(tiles);
+    launch_any(product, c.bf, reg, tile, a, g, 0, dim3((unsigned)up(tiles * a.tiles_n, 8)), st);
+    return launched();
+}
+
+// dW (and with two results dWg, dWu): D rows of `ldd` bytes, two matrices `second` bytes apart
+gemm_status run_weights(const Common& c, int mats, bool reg, int tile, const char* D, int64_t ldd, int64_t d_cols, int64_t second,
+                        const char* X, int64_t ldx, int64_t x_cols, void* dW, void* dW1, const int32_t* offsets, hipStream_t st) {
+    ProductArgs w{};
+    w.A = c.nk ? D : X;
+    if (mats == 2) {
+        w.A1 = c.nk ? D + second : X;
+        w.C1 = dW1;
+    }
+    w.B[0] = c.nk ? X : D;
+    w.B[1] = c.nk ? X : D + second;
+    w.C = dW;
+    w.M = (int32_t)(c.nk ? c.N : c.K);
+    w.N = (int32_t)(c.nk ? c.K : c.N);
+    w.lda = (uint32_t)(c.nk ? ldd : ldx);
+    w.ldb = (uint32_t)(c.nk ? ldx : ldd);
+    w.a_cols = (int32_t)(c.nk ? d_cols : x_cols);
+    w.b_cols = (int32_t)(c.nk ? x_cols : d_cols);
+    w.segments = w.split = 1;
+    w.zm = (uint8_t)(c.nk ? mats : 1);
+    w.zn = (uint8_t)(c.nk ? 1 : mats);
+    w.kt_part = kWhole;
+    w.tiles_m = (int32_t)ceil_div(w.M, spg::kTileM[tile]);
+    w.tiles_n = (int32_t)ceil_div(w.N, spg::kTileN[tile]);
+    w.group_m = raster_rows((int64_t)w.tiles_m * w.zm);
+    const int64_t per = up((int64_t)w.tiles_m * w.tiles_n * mats, 8);
+    launch_any(spg::kGroupWeights, c.bf, reg, tile, w, group_args(c, offsets, nullptr), (int)per, dim3((unsigned)(per * c.groups)), st);
+    return launched();
+}
+
+template <bool BF16, bool DUAL>
+void launch_stream(const Common& c, const ProductArgs& a, const GroupArgs& g, hipStream_t st) {
+    const dim3 grid((unsigned)ceil_div(a.N, 16), (unsigned)c.live()), wg(512);
+    const uintptr_t all = (uintptr_t)a.A | (uintptr_t)a.B[0] | (DUAL ? (uintptr_t)a.B[1] : 0) | (uintptr_t)a.lda | (uintptr_t)a.ldb;
+    if (all % 4 == 0) hipLaunchKernelGGL((spg::grouped_stream<BF16, DUAL, true, 8, 4>), grid, wg, 0, st, a, g);
+    else hipLaunchKernelGGL((spg::grouped_stream<BF16, DUAL, false, 8, 4>), grid, wg, 0, st, a, g);
+}
+
+gemm_status run_stream(const Common& c, bool dual, const ProductArgs& a, const int32_t* offsets, const int32_t* source,
+                       hipStream_t st) {
+    const GroupArgs g = group_args(c, offsets, source);
+    if (c.bf) dual ? launch_stream<true, true>(c, a, g, st) : launch_stream<true, false>(c, a, g, st);
+    else dual ? launch_stream<false, true>(c, a, g, st) : launch_stream<false, false>(c, a, g, st);
+    return launched();
+}
+
+gemm_status run_gather(const Common& c, const void* X, const int32_t* source, void* to, hipStream_t st) {
+    const int64_t per = c.pitch() / 16;
+    const spg::GatherArgs a{(const char*)X, (char*)to, source, c.rows, c.K * 2, (int32_t)per, (int32_t)c.tokens};
+    hipLaunchKernelGGL(spg::gather_rows<2>, spread(ceil_div(c.rows * per, 256)), dim3(256), 0, st, a);
+    return launched();
 }
 
 dim3 simple_grid(int64_t outputs, int64_t groups) {
     return dim3((unsigned)std::min<int64_t>(ceil_div(std::max<int64_t>(outputs, 1), 256), 4096), (unsigned)groups);
 }
 
-// Rows of every group times its matrix, B as [N,K] (nk) or [K,N]; A's rows through `source`
-// where that is not null.  Two B: gated, or (segments 2) one sum over both.
-gemm_status simple_rows(const Common& c, const spg::ProductArgs& p, bool nk, int64_t lda, int64_t seg_a, bool dual,
+// Any sizes: B as [N,K] (nk) or [K,N] of the product at hand.
+gemm_status simple_rows(const Common& c, const ProductArgs& p, bool nk, int64_t lda, int64_t seg_a, bool dual,
                         const int32_t* offsets, const int32_t* source, hipStream_t st) {
-    const spg::SimpleGroupArgs a{p, group_args(c, offsets, source, c.matrix()), lda, 1, nk ? p.K : 1, nk ? 1 : p.N, seg_a};
+    const spg::SimpleGroupArgs a{p, group_args(c, offsets, source), lda, 1, nk ? p.K : 1, nk ? 1 : p.N, seg_a};
     const dim3 grid = simple_grid(ceil_div(c.rows * p.N, c.groups), c.groups);
     if (c.bf) {
         if (dual) hipLaunchKernelGGL((spg::simple_group_rows<true, true>), grid, dim3(256), 0, st, a);
@@ -67,7 +250,7 @@ gemm_status simple_rows(const Common& c, const spg::ProductArgs& p, bool nk, int
 
 gemm_status simple_weights(const Common& c, const void* D, int64_t ldd, const void* X, void* C, const int32_t* offsets,
                            const int32_t* source, hipStream_t st) {
-    const spg::SimpleWeightArgs a{group_args(c, offsets, source, c.matrix()), (const char*)D, (const char*)X, (char*)C,
+    const spg::SimpleWeightArgs a{group_args(c, offsets, source), (const char*)D, (const char*)X, (char*)C,
                                   ldd, c.N, c.K, c.nk ? c.K : 1, c.nk ? 1 : c.N};
     const dim3 grid = simple_grid(c.N * c.K, c.groups);
     if (c.bf) hipLaunchKernelGGL((spg::simple_group_weights<true>), grid, dim3(256), 0, st, a);
@@ -75,21 +258,30 @@ gemm_status simple_weights(const Common& c, const void* D, int64_t ldd, const vo
     return launched();
 }
 
-bool small_workspace(const void* workspace, int64_t bytes, int64_t need) {
-    return need > 0 && (!workspace || (uintptr_t)workspace % 16 != 0 || bytes < need);
+// The streaming kernel: matrices along the reduction, few rows a group.
+bool streams(const Common& c, bool along) {
+    return along && c.rows <= 16 * c.live() && c.rows <= 1024;
 }
+
+// Operands' first row and last byte within 32-bit offsets of the stream
+bool fits(int64_t rows, int64_t row_bytes) { return rows * row_bytes + 64 < kMaxBytes; }
 
 }  // namespace
 
 struct gemm_grouped_plan {
     Common c;
+    bool simple, simple_back, stream, stream_back;
+    int fwd[2], dx[2], dw[2];      // tile classes [register-staged]
+    int64_t ws_run, ws_back;
 };
 
 struct gemm_experts_plan {
     Common c;
     int act;
-    int64_t np;        // columns of dG and of dU in the workspace
-    int64_t ws_back;
+    bool simple, simple_back, stream;
+    int fwd[2], dx[2], dw[2];
+    int64_t np;                    // columns of dG and of dU in the workspace
+    int64_t ws_run, ws_back, off_x;
 };
 
 extern "C" {
@@ -99,62 +291,108 @@ gemm_status gemm_grouped_create(gemm_grouped_handle* out, int64_t rows, int64_t 
     if (out) *out = nullptr;
     const gemm_status e = check(out, rows, N, K, groups, tokens, dtype, layout);
     if (e != GEMM_OK) return e;
-    gemm_grouped_plan* p = new (std::nothrow) gemm_grouped_plan{
-        Common{rows, N, K, groups, tokens, dtype == GEMM_BF16, layout == GEMM_B_NK}};
+    gemm_grouped_plan* p = new (std::nothrow) gemm_grouped_plan{};
     if (!p) return GEMM_ERR_OUT_OF_MEMORY;
+    const Common c = p->c = Common{rows, N, K, groups, tokens, dtype == GEMM_BF16, layout == GEMM_B_NK};
+    // the tiled kernels need 16 bytes of every row they copy, and 32-bit offsets
+    p->simple = K < 8 || (!c.nk && N < 8) || K * 2 > kMaxRowBytes || N * 2 > kMaxRowBytes;
+    p->simple_back = p->simple || N < 8;
+    p->stream = !p->simple && streams(c, c.nk) && fits(std::max(rows, tokens), K * 2);
+    p->stream_back = !p->simple_back && streams(c, !c.nk) && fits(rows, N * 2);
+    const double live = (double)c.live(), io = 2.0 * rows * (N + K) + live * c.matrix();
+    const bool crooked = N % 64 != 0 || K % 64 != 0;
+    for (int r = 0; r < 2; ++r) {
+        p->fwd[r] = choose_rows(RowsShape{rows, c.live(), N, ceil_div(K, 64), 1, io, crooked}, r == 1);
+        p->dx[r] = choose_rows(RowsShape{rows, c.live(), K, ceil_div(N, 64), 1, io, crooked}, r == 1);
+        p->dw[r] = choose_weights(c, 1, r == 1);
+    }
+    p->ws_run = p->simple || p->stream ? 0 : c.gathered();
+    p->ws_back = p->simple_back ? 0 : c.gathered();
     *out = p;
     return GEMM_OK;
 }
 
-int64_t gemm_grouped_workspace(gemm_grouped_handle h) { return h ? 0 : -1; }
-int64_t gemm_grouped_run_workspace(gemm_grouped_handle h) { return h ? 0 : -1; }
+int64_t gemm_grouped_workspace(gemm_grouped_handle h) { return h ? std::max(h->ws_run, h->ws_back) : -1; }
+int64_t gemm_grouped_run_workspace(gemm_grouped_handle h) { return h ? h->ws_run : -1; }
 
 gemm_status gemm_grouped_run(gemm_grouped_handle h, const void* X, const void* W, const int32_t* offsets,
                              const int32_t* source, void* Y, void* workspace, int64_t workspace_bytes,
                              hipStream_t stream) {
-    (void)workspace;
-    (void)workspace_bytes;
     if (!h) return GEMM_ERR_INVALID_ARG;
     const Common& c = h->c;
-    if ((c.tokens < 0) != (source == nullptr) && c.rows > 0) return GEMM_ERR_INVALID_ARG;
+    if (wrong_source(c, source)) return GEMM_ERR_INVALID_ARG;
     if (c.rows == 0 || c.N == 0) return GEMM_OK;
     if (!offsets || !Y || (c.K > 0 && (!W || (!X && c.tokens != 0)))) return GEMM_ERR_INVALID_ARG;
-    spg::ProductArgs a{};
+    ProductArgs a{};
     a.A = (const char*)X;
     a.B[0] = (const char*)W;
     a.C = Y;
     a.M = (int32_t)c.rows;
     a.N = (int32_t)c.N;
     a.K = (int32_t)c.K;
+    a.lda = (uint32_t)(c.K * 2);
+    a.ldb = (uint32_t)((c.nk ? c.K : c.N) * 2);
+    a.b_cols = (int32_t)c.N;
     a.segments = 1;
-    return simple_rows(c, a, c.nk, c.K, 0, false, offsets, source, stream);
+    if (h->simple) return simple_rows(c, a, c.nk, c.K, 0, false, offsets, source, stream);
+    if (h->stream) return run_stream(c, false, a, offsets, source, stream);
+    if (small_workspace(workspace, workspace_bytes, h->ws_run)) return GEMM_ERR_INVALID_ARG;
+    if (source) {
+        const gemm_status e = run_gather(c, X, source, workspace, stream);
+        if (e != GEMM_OK) return e;
+        a.A = (const char*)workspace;
+        a.lda = (uint32_t)c.pitch();
+    }
+    const bool reg = a.lda % 4 != 0 || !words(a.A) || a.ldb % 4 != 0 || !words(W);
+    return run_rows(c.nk ? spg::kRowsNK : spg::kRowsKN, c, reg, h->fwd[reg], 1, a, offsets, stream);
 }
 
 gemm_status gemm_grouped_backward(gemm_grouped_handle h, const void* dY, const void* X, const void* W,
                                   const int32_t* offsets, const int32_t* source, void* dX, void* dW, void* workspace,
                                   int64_t workspace_bytes, hipStream_t stream) {
-    (void)workspace;
-    (void)workspace_bytes;
     if (!h) return GEMM_ERR_INVALID_ARG;
     const Common& c = h->c;
-    if ((c.tokens < 0) != (source == nullptr) && c.rows > 0) return GEMM_ERR_INVALID_ARG;
+    if (wrong_source(c, source)) return GEMM_ERR_INVALID_ARG;
     if (c.K == 0 || (!dX && !dW) || (c.rows == 0 && c.N == 0)) return GEMM_OK;
     if (!offsets) return GEMM_ERR_INVALID_ARG;
     if (c.rows > 0 && c.N > 0 && (!dY || (dX && !W) || (dW && !X && c.tokens != 0))) return GEMM_ERR_INVALID_ARG;
+    if (small_workspace(workspace, workspace_bytes, c.N > 0 ? h->ws_back : 0)) return GEMM_ERR_INVALID_ARG;
     if (dX && c.rows > 0) {
-        spg::ProductArgs a{};
+        ProductArgs a{};
         a.A = (const char*)dY;
         a.B[0] = (const char*)W;
         a.C = dX;
         a.M = (int32_t)c.rows;
         a.N = (int32_t)c.K;
         a.K = (int32_t)c.N;
+        a.lda = (uint32_t)(c.N * 2);
+        a.ldb = (uint32_t)((c.nk ? c.K : c.N) * 2);
+        a.b_cols = (int32_t)c.K;
         a.segments = 1;
-        const gemm_status e = simple_rows(c, a, !c.nk, c.N, 0, false, offsets, nullptr, stream);
+        gemm_status e;
+        if (h->simple_back) {
+            e = simple_rows(c, a, !c.nk, c.N, 0, false, offsets, nullptr, stream);
+        } else if (h->stream_back) {
+            e = run_stream(c, false, a, offsets, nullptr, stream);
+        } else {
+            const bool reg = a.lda % 4 != 0 || !words(dY) || a.ldb % 4 != 0 || !words(W);
+            e = run_rows(c.nk ? spg::kRowsKN : spg::kRowsNK, c, reg, h->dx[reg], 1, a, offsets, stream);
+        }
         if (e != GEMM_OK) return e;
     }
-    if (dW && c.N > 0) return simple_weights(c, dY, c.N, X, dW, offsets, source, stream);
-    return GEMM_OK;
+    if (!dW || c.N == 0) return GEMM_OK;
+    if (h->simple_back) return simple_weights(c, dY, c.N, X, dW, offsets, source, stream);
+    const char* x = (const char*)X;
+    int64_t ldx = c.K * 2, cols = c.K;
+    if (source) {
+        const gemm_status e = run_gather(c, X, source, workspace, stream);
+        if (e != GEMM_OK) return e;
+        x = (const char*)workspace;
+        ldx = c.pitch();
+        cols = up(c.K, 8);
+    }
+    const bool reg = c.N % 2 != 0 || !words(dY) || ldx % 4 != 0 || !words(x);
+    return run_weights(c, 1, reg, h->dw[reg], (const char*)dY, c.N * 2, c.N, 0, x, ldx, cols, dW, nullptr, offsets, stream);
 }
 
 gemm_status gemm_grouped_destroy(gemm_grouped_handle h) {
@@ -168,28 +406,40 @@ gemm_status gemm_experts_create(gemm_experts_handle* out, int64_t rows, int64_t 
     if (act != GEMM_ACT_SILU && act != GEMM_ACT_GELU_TANH && act != GEMM_ACT_RELU) return GEMM_ERR_INVALID_ARG;
     const gemm_status e = check(out, rows, N, K, groups, tokens, dtype, layout);
     if (e != GEMM_OK) return e;
-    gemm_experts_plan* p = new (std::nothrow) gemm_experts_plan{
-        Common{rows, N, K, groups, tokens, dtype == GEMM_BF16, layout == GEMM_B_NK}, (int)act, up(N, 64), 0};
+    gemm_experts_plan* p = new (std::nothrow) gemm_experts_plan{};
     if (!p) return GEMM_ERR_OUT_OF_MEMORY;
-    p->ws_back = up(rows * p->np * 4, kAlign);
+    const Common c = p->c = Common{rows, N, K, groups, tokens, dtype == GEMM_BF16, layout == GEMM_B_NK};
+    p->act = (int)act;
+    p->np = up(N, 64);
+    p->simple = K < 8 || (!c.nk && N < 8) || K * 2 > kMaxRowBytes || N * 2 > kMaxRowBytes;
+    p->simple_back = p->simple || p->np * 4 > kMaxRowBytes;
+    p->stream = !p->simple && streams(c, c.nk) && fits(std::max(rows, tokens), K * 2);
+    const double live = (double)c.live(), io = 2.0 * rows * (N + K) + 2.0 * live * c.matrix();
+    const bool crooked = N % 64 != 0 || K % 64 != 0;
+    for (int r = 0; r < 2; ++r) {
+        p->fwd[r] = choose_rows(RowsShape{rows, c.live(), N, ceil_div(K, 64), 2, io, crooked}, r == 1);
+        p->dx[r] = choose_rows(RowsShape{rows, c.live(), K, 2 * ceil_div(N, 64), 1, io, crooked}, r == 1);
+        p->dw[r] = choose_weights(c, 2, r == 1);
+    }
+    p->ws_run = p->simple || p->stream ? 0 : c.gathered();
+    p->off_x = up(rows * p->np * 4, kAlign);
+    p->ws_back = p->off_x + (p->simple_back ? 0 : c.gathered());
     *out = p;
     return GEMM_OK;
 }
 
-int64_t gemm_experts_workspace(gemm_experts_handle h) { return h ? h->ws_back : -1; }
-int64_t gemm_experts_run_workspace(gemm_experts_handle h) { return h ? 0 : -1; }
+int64_t gemm_experts_workspace(gemm_experts_handle h) { return h ? std::max(h->ws_run, h->ws_back) : -1; }
+int64_t gemm_experts_run_workspace(gemm_experts_handle h) { return h ? h->ws_run : -1; }
 
 gemm_status gemm_experts_run(gemm_experts_handle h, const void* X, const void* Wg, const void* Wu,
                              const int32_t* offsets, const int32_t* source, void* H, void* G, void* U, void* workspace,
                              int64_t workspace_bytes, hipStream_t stream) {
-    (void)workspace;
-    (void)workspace_bytes;
     if (!h || (G == nullptr) != (U == nullptr)) return GEMM_ERR_INVALID_ARG;
     const Common& c = h->c;
-    if ((c.tokens < 0) != (source == nullptr) && c.rows > 0) return GEMM_ERR_INVALID_ARG;
+    if (wrong_source(c, source)) return GEMM_ERR_INVALID_ARG;
     if (c.rows == 0 || c.N == 0) return GEMM_OK;
     if (!offsets || !H || (c.K > 0 && (!Wg || !Wu || (!X && c.tokens != 0)))) return GEMM_ERR_INVALID_ARG;
-    spg::ProductArgs a{};
+    ProductArgs a{};
     a.A = (const char*)X;
     a.B[0] = (const char*)Wg;
     a.B[1] = (const char*)Wu;
@@ -199,9 +449,22 @@ gemm_status gemm_experts_run(gemm_experts_handle h, const void* X, const void* W
     a.M = (int32_t)c.rows;
     a.N = (int32_t)c.N;
     a.K = (int32_t)c.K;
+    a.lda = (uint32_t)(c.K * 2);
+    a.ldb = (uint32_t)((c.nk ? c.K : c.N) * 2);
+    a.b_cols = (int32_t)c.N;
     a.segments = 1;
     a.act = (uint8_t)h->act;
-    return simple_rows(c, a, c.nk, c.K, 0, true, offsets, source, stream);
+    if (h->simple) return simple_rows(c, a, c.nk, c.K, 0, true, offsets, source, stream);
+    if (h->stream) return run_stream(c, true, a, offsets, source, stream);
+    if (small_workspace(workspace, workspace_bytes, h->ws_run)) return GEMM_ERR_INVALID_ARG;
+    if (source) {
+        const gemm_status e = run_gather(c, X, source, workspace, stream);
+        if (e != GEMM_OK) return e;
+        a.A = (const char*)workspace;
+        a.lda = (uint32_t)c.pitch();
+    }
+    const bool reg = a.lda % 4 != 0 || !words(a.A) || a.ldb % 4 != 0 || !words(Wg) || !words(Wu);
+    return run_rows(c.nk ? spg::kRowsGatedNK : spg::kRowsGatedKN, c, reg, h->fwd[reg], 2, a, offsets, stream);
 }
 
 gemm_status gemm_experts_backward(gemm_experts_handle h, const void* dH, const void* X, const void* Wg, const void* Wu,
@@ -209,13 +472,14 @@ gemm_status gemm_experts_backward(gemm_experts_handle h, const void* dH, const v
                                   void* dWg, void* dWu, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
     if (!h) return GEMM_ERR_INVALID_ARG;
     const Common& c = h->c;
-    if ((c.tokens < 0) != (source == nullptr) && c.rows > 0) return GEMM_ERR_INVALID_ARG;
+    if (wrong_source(c, source)) return GEMM_ERR_INVALID_ARG;
     if (c.K == 0 || (c.rows == 0 && c.N == 0)) return GEMM_OK;
     if (!offsets || (c.rows > 0 && !dX) || (c.N > 0 && (!dWg || !dWu))) return GEMM_ERR_INVALID_ARG;
     if (c.rows > 0 && c.N > 0) {
         if (!dH || (!X && c.tokens != 0) || !Wg || !Wu || !G || !U) return GEMM_ERR_INVALID_ARG;
         if (small_workspace(workspace, workspace_bytes, h->ws_back)) return GEMM_ERR_INVALID_ARG;
     }
+    const bool simple = h->simple_back || c.rows == 0 || c.N == 0;
     uint16_t* D = (uint16_t*)workspace;
     if (c.rows > 0 && c.N > 0) {
         const dim3 grid((unsigned)ceil_div(c.rows * (h->np / 8), 256));
@@ -227,7 +491,8 @@ gemm_status gemm_experts_backward(gemm_experts_handle h, const void* dH, const v
         if (e != GEMM_OK) return e;
     }
     if (c.rows > 0) {
-        spg::ProductArgs a{};
+        // dX = [dG dU] . [Wg; Wu]: one sum over both segments
+        ProductArgs a{};
         a.A = (const char*)D;
         a.B[0] = (const char*)Wg;
         a.B[1] = (const char*)Wu;
@@ -235,15 +500,38 @@ gemm_status gemm_experts_backward(gemm_experts_handle h, const void* dH, const v
         a.M = (int32_t)c.rows;
         a.N = (int32_t)c.K;
         a.K = (int32_t)c.N;
+        a.lda = (uint32_t)(h->np * 4);
+        a.ldb = (uint32_t)((c.nk ? c.K : c.N) * 2);
+        a.b_cols = (int32_t)c.K;
         a.segments = 2;
-        const gemm_status e = simple_rows(c, a, !c.nk, 2 * h->np, h->np, false, offsets, nullptr, stream);
+        gemm_status e;
+        if (simple) {
+            e = simple_rows(c, a, !c.nk, 2 * h->np, h->np, false, offsets, nullptr, stream);
+        } else {
+            const bool reg = a.ldb % 4 != 0 || !words(Wg) || !words(Wu);
+            e = run_rows(c.nk ? spg::kRowsSumNK : spg::kRowsSumKN, c, reg, h->dx[reg], 1, a, offsets, stream);
+        }
         if (e != GEMM_OK) return e;
     }
-    for (int z = 0; z < 2 && c.N > 0; ++z) {
-        const gemm_status e = simple_weights(c, D + z * h->np, 2 * h->np, X, z ? dWu : dWg, offsets, source, stream);
-        if (e != GEMM_OK) return e;
+    if (c.N == 0) return GEMM_OK;
+    if (simple) {
+        for (int z = 0; z < 2; ++z) {
+            const gemm_status e = simple_weights(c, D + z * h->np, 2 * h->np, X, z ? dWu : dWg, offsets, source, stream);
+            if (e != GEMM_OK) return e;
+        }
+        return GEMM_OK;
     }
-    return GEMM_OK;
+    const char* x = (const char*)X;
+    int64_t ldx = c.K * 2, cols = c.K;
+    if (source) {
+        x = (const char*)workspace + h->off_x;
+        const gemm_status e = run_gather(c, X, source, (void*)x, stream);
+        if (e != GEMM_OK) return e;
+        ldx = c.pitch();
+        cols = up(c.K, 8);
+    }
+    const bool reg = ldx % 4 != 0 || !words(x);
+    return run_weights(c, 2, reg, h->dw[reg], (const char*)D, h->np * 4, h->np, h->np * 2, x, ldx, cols, dWg, dWu, offsets, stream);
 }
 
 gemm_status gemm_experts_destroy(gemm_experts_handle h) {

@@ -1,0 +1,80 @@
+// Launchers of the tiled products by group: declared for the host unit, defined and explicitly
+// instantiated by grouped_unit.hip, which is compiled once per (element type, product, copy mode).
+#pragma once
+
+#include "grouped_kernels.hpp"
+#include "product_launch.hpp"
+
+namespace spg {
+
+// The products, by how their operands are stored.
+enum {
+    kRowsGatedNK = 0,    // two matrices [N,K], gated epilogue
+    kRowsGatedKN = 1,    // two matrices [K,N]
+    kRowsSumNK = 2,      // [dG dU] with matrices [N,K]: one sum over both, B reduction-major
+    kRowsSumKN = 3,      // [dG dU] with matrices [K,N]
+    kRowsNK = 4,         // one matrix, stored along the reduction
+    kRowsKN = 5,         // one matrix, stored across it
+    kGroupWeights = 6,   // gradients of the matrices
+    kGroupProducts = 7
+};
+
+// Tile classes are those of product_launch.hpp.  `per`: workgroups of a group (kGroupWeights)
+template <int ET, int P, bool REG>
+void launch_grouped(int tile, const ProductArgs& a, const GroupArgs& g, int per, dim3 grid, hipStream_t st);
+
+#ifdef SPG_DEFINE_GROUPED
+template <int ET, int P, bool REG, int BM, int BN, int WM, int WN, int S, bool DEEP, int KG, bool TAIL, int WPS>
+void launch_group_kernel(const ProductArgs& a, const GroupArgs& g, int per, dim3 grid, hipStream_t st) {
+    constexpr bool DUAL = P == kRowsGatedNK || P == kRowsGatedKN, SEG = P == kRowsSumNK || P == kRowsSumKN;
+    constexpr bool BN_ = P == kRowsGatedKN || P == kRowsSumNK || P == kRowsKN;
+    const dim3 wg(ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP, KG>::NT);
+    if constexpr (P == kGroupWeights)
+        hipLaunchKernelGGL((grouped_weights<ET, REG, BM, BN, WM, WN, S, DEEP, KG, WPS>), grid, wg, 0, st, a, g, per);
+    else
+        hipLaunchKernelGGL((grouped_rows<ET, BN_, DUAL, SEG, REG, BM, BN, WM, WN, S, DEEP, KG, TAIL, WPS>), grid, wg, 0, st, a, g);
+}
+
+// Tails as in launch_tile (product_launch.hpp)
+template <int ET, int P, bool REG, int BM, int BN, int WM, int WN, int S, bool DEEP, int KG, int WPS = 1>
+void launch_group_tile(const ProductArgs& a, const GroupArgs& g, int per, dim3 grid, hipStream_t st) {
+    if constexpr (P == kGroupWeights || P == kRowsSumNK) {
+        launch_group_kernel<ET, P, REG, BM, BN, WM, WN, S, DEEP, KG, false, WPS>(a, g, per, grid, st);
+    } else if constexpr (BM == 256 && !REG) {
+        if (a.K % 8 == 0) launch_group_kernel<ET, P, REG, BM, BN, WM, WN, S, DEEP, KG, false, WPS>(a, g, per, grid, st);
+        else launch_group_kernel<ET, P, REG, BM, BN, WM, WN, S, BN == 256, KG, true, WPS>(a, g, per, grid, st);
+    } else {
+        launch_group_kernel<ET, P, REG, BM, BN, WM, WN, S, DEEP, KG, true, WPS>(a, g, per, grid, st);
+    }
+}
+
+template <int ET, int P, bool REG>
+void launch_grouped(int tile, const ProductArgs& a, const GroupArgs& g, int per, dim3 grid, hipStream_t st) {
+    constexpr bool DUAL = P == kRowsGatedNK || P == kRowsGatedKN;
+    // the ping-pong schedule as in launch_product
+    constexpr bool DEEP = P != kRowsGatedKN && P != kGroupWeights;
+    if constexpr (!REG) {
+        if (tile == kTileBig) {
+            if constexpr (DUAL) launch_group_tile<ET, P, REG, 256, 256, 64, 128, 2, DEEP, 1>(a, g, per, grid, st);
+            else launch_group_tile<ET, P, REG, 256, 256, 128, 64, 2, DEEP, 1>(a, g, per, grid, st);
+        } else if (tile == kTileTall) {
+            launch_group_tile<ET, P, REG, 256, 128, 64, 64, 3, false, 1>(a, g, per, grid, st);
+        } else if (tile == kTileMid) {
+            launch_group_tile<ET, P, REG, 128, 128, 32, 64, 4, false, 1>(a, g, per, grid, st);
+        } else if (tile == kTilePair) {
+            launch_group_tile<ET, P, REG, 128, 128, 32, 64, 2, false, 1, 4>(a, g, per, grid, st);
+        } else if (tile == kTileSmall) {
+            launch_group_tile<ET, P, REG, 64, 128, 32, 64, 3, false, 2>(a, g, per, grid, st);
+        } else {
+            launch_group_tile<ET, P, REG, 64, 64, 32, 64, 2, false, 4>(a, g, per, grid, st);
+        }
+    } else {
+        if (tile == kTileTall) launch_group_tile<ET, P, REG, 256, 128, 64, 64, 2, false, 1>(a, g, per, grid, st);
+        else if (tile == kTileMid) launch_group_tile<ET, P, REG, 128, 128, 32, 64, 2, false, 1>(a, g, per, grid, st);
+        else if (tile == kTileSmall) launch_group_tile<ET, P, REG, 64, 128, 32, 64, 2, false, 1>(a, g, per, grid, st);
+        else launch_group_tile<ET, P, REG, 64, 64, 32, 64, 2, false, 4>(a, g, per, grid, st);
+    }
+}
+#endif
+
+}  // namespace spg
