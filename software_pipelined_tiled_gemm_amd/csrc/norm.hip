@@ -36,9 +36,243 @@ struct NormArgs {
     const char *X, *dY, *weight, *bias;
     char *Y, *dX, *dweight, *dbias;
     float *mean, *rstd, *part;
-    int64_t rows, K;
+    int64_t rows, K, pitch;    // pitch: floats between the parts' rows
     float eps;
 };
+
+// Rows of up to 64 * W * EPT values: a team of W waves takes a row, EPT values a thread, all of it
+// in registers between the sums; a workgroup of four teams (W = 1) or one takes every
+// gridDim.x-th row and has the next one's loads in flight while it sums.  weight and bias are
+// read once per workgroup.  TAIL: rows that end inside a vector; its shifts and masks take up to 60
+// registers, which the other rows save.
+template <int DT, int W, int EPT, bool TAIL>
+struct Team {
+    static constexpr int E = Vec<DT>::E, V = EPT / E, TEAMS = W == 1 ? 4 : 1, NT = W * TEAMS * 64;
+    static constexpr int64_t kMost = 64 * W * EPT;
+    u32x4 v[V];
+    // element of vector i that this thread starts at
+    static __device__ __forceinline__ int at(int i) { return (i * W * 64 + (int)(threadIdx.x & (W * 64 - 1))) * E; }
+    __device__ __forceinline__ void load(const char* row, int K, bool in) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = in && at(i) < K ? vec<DT>(row, at(i), K) : u32x4{};
+    }
+    template <int D>
+    static __device__ __forceinline__ u32x4 vec(const char* row, int k, int K) {
+        struct __attribute__((packed, aligned(Vec<D>::EB))) B { u32x4 v; };
+        if constexpr (TAIL) return load_vec<D>(row, k, K);
+        else return ((const B*)(row + (uint32_t)(k * Vec<D>::EB)))->v;
+    }
+    static __device__ __forceinline__ void store(char* row, int k, int K, const float (&x)[E]) {
+        struct __attribute__((packed, aligned(Vec<DT>::EB))) B { u32x4 v; };
+        if constexpr (TAIL) store_vec<DT>(row, k, K, x);
+        else ((B*)(row + (uint32_t)(k * Vec<DT>::EB)))->v = pack_vec<DT>(x);
+    }
+    __device__ __forceinline__ float operator[](int j) const { return elem<DT>(v[j / E], j % E); }
+};
+
+template <int PT, typename T>
+__device__ __forceinline__ void load_params(const char* p, int K, float fill, float (&x)[T::V * T::E]) {
+#pragma unroll
+    for (int i = 0; i < T::V; ++i)
+#pragma unroll
+        for (int h = 0; h < T::E; h += Vec<PT>::E) {
+            const u32x4 v = p && T::at(i) + h < K ? T::template vec<PT>(p, T::at(i) + h, K) : u32x4{};
+#pragma unroll
+            for (int e = 0; e < Vec<PT>::E && h + e < T::E; ++e) x[i * T::E + h + e] = p ? elem<PT>(v, e) : fill;
+        }
+}
+
+// Sums of NS values over a team, in every thread; `turn` alternates between two places in LDS, so
+// that one barrier a sum is enough: when a place is written again, every wave has passed the
+// barrier behind its last reading.
+template <int W, int NS>
+__device__ __forceinline__ void team_sums(float (&s)[NS], float (*lds)[W][NS], int& turn) {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) s[i] = wave_sum(s[i]);
+    if constexpr (W > 1) {
+        if ((threadIdx.x & 63) == 0)
+#pragma unroll
+            for (int i = 0; i < NS; ++i) lds[turn][threadIdx.x >> 6][i] = s[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            if constexpr (W == 16) {
+                const int lane = threadIdx.x & 63;
+                s[i] = wave_sum(lane < W ? lds[turn][lane & (W - 1)][i] : 0.0f);
+            } else {
+                s[i] = lds[turn][0][i];
+#pragma unroll
+                for (int w = 1; w < W; ++w) s[i] += lds[turn][w][i];
+            }
+        }
+        turn ^= 1;
+    }
+}
+
+template <int DT, int PT, int W, int EPT, bool TAIL>
+__global__ void __launch_bounds__((Team<DT, W, EPT, TAIL>::NT)) norm_run(NormArgs a) {
+    using T = Team<DT, W, EPT, TAIL>;
+    __shared__ float lds[2][W][1];
+    const int K = (int)a.K, team = W == 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
+    const int64_t step = (int64_t)gridDim.x * T::TEAMS, pitch = a.K * Vec<DT>::EB;
+    int64_t row = (int64_t)blockIdx.x * T::TEAMS + team;
+    int turn = 0;
+    T x, next;
+    next.load(a.X + row * pitch, K, row < a.rows);
+    float w[EPT], b[EPT];
+    load_params<PT, T>(a.weight, K, 1.0f, w);
+    load_params<PT, T>(a.bias, K, 0.0f, b);
+    for (; row < a.rows; row += step) {
+        x = next;
+        next.load(a.X + (row + step) * pitch, K, row + step < a.rows);
+        float s[1] = {0.0f};
+#pragma unroll
+        for (int j = 0; j < EPT; ++j) s[0] += x[j];
+        team_sums<W, 1>(s, lds, turn);
+        const float mean = s[0] / (float)K;
+        s[0] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < EPT; ++j) {
+            const float c = x[j] - mean;
+            s[0] += T::at(j / T::E) + j % T::E < K ? c * c : 0.0f;
+        }
+        team_sums<W, 1>(s, lds, turn);
+        const float rstd = 1.0f / sqrtf(s[0] / (float)K + a.eps);
+        if (a.mean && (threadIdx.x & (W * 64 - 1)) == 0) {
+            a.mean[row] = mean;
+            a.rstd[row] = rstd;
+        }
+#pragma unroll
+        for (int i = 0; i < T::V; ++i) {
+            float y[T::E];
+#pragma unroll
+            for (int e = 0; e < T::E; ++e)
+                y[e] = __builtin_fmaf((x[i * T::E + e] - mean) * rstd, w[i * T::E + e], b[i * T::E + e]);
+            if (T::at(i) < K) T::store(a.Y + row * pitch, T::at(i), K, y);
+        }
+    }
+}
+
+// dX, and each workgroup's share of the parameters' gradients, summed in registers over its
+// rows: part [gridDim.x][2][pitch] fp32.  (x and dy past the row's end are zero, and what they
+// give is zero or not stored.)
+template <int DT, int PT, int W, int EPT, bool TAIL>
+__global__ void __launch_bounds__((Team<DT, W, EPT, TAIL>::NT)) norm_back(NormArgs a) {
+    using T = Team<DT, W, EPT, TAIL>;
+    __shared__ float lds[2][W][2];
+    const int K = (int)a.K, team = W == 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
+    const int64_t step = (int64_t)gridDim.x * T::TEAMS, pitch = a.K * Vec<DT>::EB;
+    int64_t row = (int64_t)blockIdx.x * T::TEAMS + team;
+    int turn = 0;
+    // the widest teams have no registers left for the next row's loads
+    constexpr bool AHEAD = W < 16 || EPT < 16;
+    T x, dy, nx, ndy;
+    if constexpr (AHEAD) {
+        nx.load(a.X + row * pitch, K, row < a.rows);
+        ndy.load(a.dY + row * pitch, K, row < a.rows);
+    }
+    float w[EPT], dw[EPT], db[EPT];
+    load_params<PT, T>(a.weight, K, 1.0f, w);
+#pragma unroll
+    for (int j = 0; j < EPT; ++j) dw[j] = db[j] = 0.0f;
+    for (; row < a.rows; row += step) {
+        if constexpr (AHEAD) {
+            x = nx;
+            dy = ndy;
+            const bool more = row + step < a.rows;
+            nx.load(a.X + (row + step) * pitch, K, more);
+            ndy.load(a.dY + (row + step) * pitch, K, more);
+        } else {
+            x.load(a.X + row * pitch, K, true);
+            dy.load(a.dY + row * pitch, K, true);
+        }
+        const float mean = a.mean[row], rstd = a.rstd[row];
+        float s[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < EPT; ++j) {
+            const float d = dy[j], n = (x[j] - mean) * rstd, g = d * w[j];
+            dw[j] = __builtin_fmaf(d, n, dw[j]);
+            db[j] += d;
+            s[0] += g;
+            s[1] = __builtin_fmaf(g, n, s[1]);
+        }
+        team_sums<W, 2>(s, lds, turn);
+        const float ms = s[0] / (float)K, mt = s[1] / (float)K;
+#pragma unroll
+        for (int i = 0; i < T::V; ++i) {
+            float o[T::E];
+#pragma unroll
+            for (int e = 0; e < T::E; ++e) {
+                const int j = i * T::E + e;
+                const float n = (x[j] - mean) * rstd;
+                o[e] = rstd * (dy[j] * w[j] - ms - n * mt);
+            }
+            if (T::at(i) < K) T::store(a.dX + row * pitch, T::at(i), K, o);
+        }
+    }
+    if (!a.part) return;
+    if constexpr (T::TEAMS > 1) {
+        // the four waves' sums meet, in order
+        __shared__ __attribute__((aligned(16))) float sums[T::TEAMS - 1][2][EPT][64];
+        const int lane = threadIdx.x & 63;
+        if (team > 0)
+#pragma unroll
+            for (int j = 0; j < EPT; ++j) {
+                sums[team - 1][0][j][lane] = dw[j];
+                sums[team - 1][1][j][lane] = db[j];
+            }
+        __syncthreads();
+        if (team > 0) return;
+        for (int t = 0; t < T::TEAMS - 1; ++t)
+#pragma unroll
+            for (int j = 0; j < EPT; ++j) {
+                dw[j] += sums[t][0][j][lane];
+                db[j] += sums[t][1][j][lane];
+            }
+    }
+    float* part = a.part + (int64_t)blockIdx.x * 2 * a.pitch;
+#pragma unroll
+    for (int i = 0; i < T::V; ++i)
+        if (T::at(i) < K)
+#pragma unroll
+            for (int e = 0; e < T::E; e += 4) {
+                const int j = i * T::E + e;
+                *(floatx4*)(part + T::at(i) + e) = floatx4{dw[j], dw[j + 1], dw[j + 2], dw[j + 3]};
+                *(floatx4*)(part + a.pitch + T::at(i) + e) = floatx4{db[j], db[j + 1], db[j + 2], db[j + 3]};
+            }
+}
+
+// The workgroups' shares added: 64 columns a workgroup, 16 waves share the parts, in order.
+constexpr int kParamWaves = 16;
+template <int PT>
+__global__ void __launch_bounds__(kParamWaves * 64) norm_params(NormArgs a, int parts) {
+    __shared__ float lds[kParamWaves][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int per = (int)(a.pitch + 63) / 64;              // workgroups of one gradient
+    const int which = blockIdx.x >= per;
+    const int64_t k = (int64_t)(blockIdx.x - which * per) * 64 + lane;
+    char* out = which ? a.dbias : a.dweight;
+    if (!out) return;
+    float s = 0.0f;
+    if (k < a.pitch) {
+        const float* p = a.part + which * a.pitch + k;
+        constexpr int U = 8;
+        for (int i = wave; i < parts; i += U * kParamWaves) {
+            float v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = i + u * kParamWaves < parts ? p[(int64_t)(i + u * kParamWaves) * 2 * a.pitch] : 0.0f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) s += v[u];
+        }
+    }
+    lds[wave][lane] = s;
+    __syncthreads();
+    if (wave > 0 || k >= a.K) return;
+    for (int i = 1; i < kParamWaves; ++i) s += lds[i][lane];
+    store1<PT>(out, k, s);
+}
+
+// ---- rows of any length: read again for each sum -------------------------------------------
 
 template <int DT, int PT>
 __global__ void __launch_bounds__(kThreads) norm_rows(NormArgs a) {
@@ -49,13 +283,13 @@ __global__ void __launch_bounds__(kThreads) norm_rows(NormArgs a) {
     const char* x = a.X + row * K * Vec<DT>::EB;
     float s = 0.0f;
     for (int64_t k = threadIdx.x * E; k < K; k += kThreads * E) {
-        const u32x4 v = load_vec<DT>(x, k, K);
+        const u32x4 v = load_short<DT>(x, k, K);
         for (int e = 0; e < E; ++e) s += elem<DT>(v, e);
     }
     const float mean = group_sum(s, lds) / (float)K;
     s = 0.0f;
     for (int64_t k = threadIdx.x * E; k < K; k += kThreads * E) {
-        const u32x4 v = load_vec<DT>(x, k, K);
+        const u32x4 v = load_short<DT>(x, k, K);
         for (int e = 0; e < E; ++e) {
             const float c = elem<DT>(v, e) - mean;
             if (k + e < K) s += c * c;
@@ -138,6 +372,9 @@ struct gemm_norm_plan {
     int64_t rows, K;
     int dt, pt;
     float eps;
+    int waves, ept;            // of a team; 0: rows of any length
+    int64_t wgs, back_wgs;     // workgroups
+    int64_t pitch() const { return (K + 7) / 8 * 8; }
 };
 
 namespace {
@@ -156,6 +393,23 @@ void with_types(const gemm_norm_plan* h, F&& f) {
     else f(f32, f32);
 }
 
+// f(waves of a team, values a thread, rows end inside a vector) for a plan whose rows stay in registers
+template <typename F>
+void with_team(const gemm_norm_plan* h, F&& f) {
+    using std::integral_constant;
+    auto tail = [&](auto w, auto ept) {
+        if (h->K % 8 == 0) f(w, ept, std::false_type{});
+        else f(w, ept, std::true_type{});
+    };
+    auto go = [&](auto w) {
+        if (h->ept == 8) tail(w, integral_constant<int, 8>{});
+        else tail(w, integral_constant<int, 16>{});
+    };
+    if (h->waves == 1) go(integral_constant<int, 1>{});
+    else if (h->waves == 4) go(integral_constant<int, 4>{});
+    else go(integral_constant<int, 16>{});
+}
+
 }  // namespace
 
 extern "C" {
@@ -169,13 +423,24 @@ gemm_status gemm_norm_create(gemm_norm_handle* out, int64_t rows, int64_t K, gem
     if (param_dtype != dtype && param_dtype != GEMM_F32) return GEMM_ERR_INVALID_ARG;
     const int64_t lim = INT32_MAX / 2 - 512;
     if (rows > lim || K > lim) return GEMM_ERR_UNSUPPORTED;
-    gemm_norm_plan* p = new (std::nothrow) gemm_norm_plan{rows, K, (int)dtype, (int)param_dtype, eps};
+    gemm_norm_plan* p = new (std::nothrow) gemm_norm_plan{rows, K, (int)dtype, (int)param_dtype, eps, 0, 0, 0, 0};
     if (!p) return GEMM_ERR_OUT_OF_MEMORY;
+    // rows shorter than a vector: as rows of any length
+    if (K < 8) p->waves = 0;
+    else if (K <= 1024 && rows >= 2048) p->waves = 1;
+    else if (K <= 4096) p->waves = 4;
+    else if (K <= 16384) p->waves = 16;
+    if (p->waves) {
+        p->ept = K <= 64 * 8 * p->waves ? 8 : 16;
+        const int64_t teams = p->waves == 1 ? (rows + 3) / 4 : rows;
+        p->wgs = std::min<int64_t>(teams, p->waves == 16 ? 512 : 2048);
+        p->back_wgs = std::min<int64_t>(teams, p->waves == 16 ? 256 : 512);
+    }
     *out = p;
     return GEMM_OK;
 }
 
-int64_t gemm_norm_workspace(gemm_norm_handle h) { return h ? 0 : -1; }
+int64_t gemm_norm_workspace(gemm_norm_handle h) { return h ? h->back_wgs * 2 * h->pitch() * 4 : -1; }
 
 gemm_status gemm_norm_run(gemm_norm_handle h, const void* X, const void* weight, const void* bias, void* Y, float* mean,
                           float* rstd, hipStream_t stream) {
@@ -193,7 +458,14 @@ gemm_status gemm_norm_run(gemm_norm_handle h, const void* X, const void* weight,
     a.K = h->K;
     a.eps = h->eps;
     with_types(h, [&](auto dt, auto pt) {
-        hipLaunchKernelGGL((spg::norm_rows<decltype(dt)::value, decltype(pt)::value>), spg::row_grid(h->rows),
+        constexpr int D = decltype(dt)::value, P = decltype(pt)::value;
+        if (h->waves)
+            return with_team(h, [&](auto w, auto ept, auto tail) {
+                constexpr int W = decltype(w)::value, N = decltype(ept)::value;
+                constexpr bool T = decltype(tail)::value;
+                hipLaunchKernelGGL((spg::norm_run<D, P, W, N, T>), dim3((unsigned)h->wgs), dim3(spg::Team<D, W, N, T>::NT), 0, stream, a);
+            });
+        hipLaunchKernelGGL((spg::norm_rows<D, P>), spg::row_grid(h->rows),
                            dim3(spg::kThreads), 0, stream, a);
     });
     return spg::launched();
@@ -202,11 +474,12 @@ gemm_status gemm_norm_run(gemm_norm_handle h, const void* X, const void* weight,
 gemm_status gemm_norm_backward(gemm_norm_handle h, const void* dY, const void* X, const void* weight, const float* mean,
                                const float* rstd, void* dX, void* dweight, void* dbias, void* workspace,
                                int64_t workspace_bytes, hipStream_t stream) {
-    (void)workspace;
-    (void)workspace_bytes;
     if (!h) return GEMM_ERR_INVALID_ARG;
     if (h->K == 0) return GEMM_OK;
     if (h->rows > 0 && (!dY || !X || !mean || !rstd || !dX)) return GEMM_ERR_INVALID_ARG;
+    const int64_t need = gemm_norm_workspace(h);
+    if (need > 0 && (dweight || dbias) && (!workspace || (uintptr_t)workspace % 16 != 0 || workspace_bytes < need))
+        return GEMM_ERR_INVALID_ARG;
     spg::NormArgs a{};
     a.X = (const char*)X;
     a.dY = (const char*)dY;
@@ -220,6 +493,19 @@ gemm_status gemm_norm_backward(gemm_norm_handle h, const void* dY, const void* X
     a.K = h->K;
     with_types(h, [&](auto dt, auto pt) {
         constexpr int D = decltype(dt)::value, P = decltype(pt)::value;
+        if (h->waves && h->rows > 0) {
+            a.part = dweight || dbias ? (float*)workspace : nullptr;
+            a.pitch = h->pitch();
+            with_team(h, [&](auto w, auto ept, auto tail) {
+                constexpr int W = decltype(w)::value, N = decltype(ept)::value;
+                constexpr bool T = decltype(tail)::value;
+                hipLaunchKernelGGL((spg::norm_back<D, P, W, N, T>), dim3((unsigned)h->back_wgs), dim3(spg::Team<D, W, N, T>::NT), 0, stream, a);
+            });
+            if (a.part)
+                hipLaunchKernelGGL((spg::norm_params<P>), dim3((unsigned)(2 * ((h->pitch() + 63) / 64))),
+                                   dim3(spg::kParamWaves * 64), 0, stream, a, (int)h->back_wgs);
+            return;
+        }
         if (h->rows > 0)
             hipLaunchKernelGGL((spg::norm_rows_back<D, P>), spg::row_grid(h->rows), dim3(spg::kThreads), 0, stream, a);
         if (dweight || dbias)

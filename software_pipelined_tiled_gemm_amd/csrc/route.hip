@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(256) combine_rows(CombineArgs a) {
         const int64_t r = a.slot[t * a.k + j];
         if (r < 0 || r >= a.rows) continue;
         const float g = a.gate ? a.gate[t * a.k + j] : 1.0f;
-        const u32x4 v = load_vec<DT>(a.Y + r * a.N * EB, n, a.N);
+        const u32x4 v = load_short<DT>(a.Y + r * a.N * EB, n, a.N);
 #pragma unroll
         for (int e = 0; e < E; ++e) s[e] = __builtin_fmaf(g, elem<DT>(v, e), s[e]);
     }
@@ -336,10 +336,10 @@ __global__ void __launch_bounds__(256) combine_back(CombineArgs a) {
         float dot = 0.0f;
         if (in)
             for (int64_t n = threadIdx.x * E; n < a.N; n += 256 * E) {
-                const u32x4 v = load_vec<DT>(d, n, a.N);
+                const u32x4 v = load_short<DT>(d, n, a.N);
                 float o[E];
                 if (a.dgate) {
-                    const u32x4 y = load_vec<DT>(a.Y + r * a.N * EB, n, a.N);
+                    const u32x4 y = load_short<DT>(a.Y + r * a.N * EB, n, a.N);
 #pragma unroll
                     for (int e = 0; e < E; ++e) dot = __builtin_fmaf(elem<DT>(v, e), elem<DT>(y, e), dot);
                 }
