@@ -66,9 +66,11 @@ def product_units() -> list:
 
 
 def grouped_units() -> list:
-    """(element type, product, copy mode) of every grouped_unit.hip object: the enum of
-    csrc/grouped_launch.hpp in fp16 and bf16, with direct copies and register-staged."""
-    return [(et, p, reg) for p in range(7) for et in (0, 1) for reg in (0, 1)]
+    """(element type, product, copy mode, gathered) of every grouped_unit.hip object: the enum of
+    csrc/grouped_launch.hpp in fp16 and bf16, with direct copies and register-staged; the products
+    that read X's rows in order and by their source."""
+    return [(et, p, reg, g) for p in range(7) for et in (0, 1) for reg in (0, 1)
+            for g in ((0, 1) if p in (0, 1, 4, 5) else (0,))]
 
 
 def build(out: str = OUT, extra=(), poison: bool = False) -> str:
@@ -87,9 +89,9 @@ def build(out: str = OUT, extra=(), poison: bool = False) -> str:
     jobs += [(os.path.join(CSRC, "product_unit.hip"), f"product_unit_{et}_{p}_{reg}.o",
               pdef + [f"-DSPG_ET={et}", f"-DSPG_PRODUCT={p}", f"-DSPG_REG={reg}"])
              for et, p, reg in product_units()]
-    jobs += [(os.path.join(CSRC, "grouped_unit.hip"), f"grouped_unit_{et}_{p}_{reg}.o",
-              pdef + [f"-DSPG_ET={et}", f"-DSPG_PRODUCT={p}", f"-DSPG_REG={reg}"])
-             for et, p, reg in grouped_units()]
+    jobs += [(os.path.join(CSRC, "grouped_unit.hip"), f"grouped_unit_{et}_{p}_{reg}_{g}.o",
+              pdef + [f"-DSPG_ET={et}", f"-DSPG_PRODUCT={p}", f"-DSPG_REG={reg}", f"-DSPG_GATHER={g}"])
+             for et, p, reg, g in grouped_units()]
     jobs += [(unit_src, f"gemm_unit{u}.o", pdef + [f"-DSPG_UNIT_IS_{u}=~,1"]) for u in us]
     inc = ["-I", os.path.join(ROOT, "include"), "-I", CSRC]
     with tempfile.TemporaryDirectory(prefix="spgemm_build_") as tmp:

@@ -97,33 +97,62 @@ double grid_us(int t, bool reg, bool crooked, double wgs, double kt, double byte
 
 bool staged(int t) { return t != spg::kTileBig && t != spg::kTilePair; }   // tiles that stage through registers
 
-int choose_rows(const RowsShape& s, bool reg) {
-    int best = spg::kTileNarrow;
-    double best_us = 1e30;
+struct Choice {
+    int tile;
+    double us;   // estimated
+};
+
+double rows_wgs(const RowsShape& s, int t) {
+    return row_tiles(s, spg::kTileM[t]) * (double)ceil_div(s.N, spg::kTileN[t] / s.mats);
+}
+
+Choice choose_rows(const RowsShape& s, bool reg) {
+    Choice best{spg::kTileNarrow, 1e30};
     for (int t = 0; t < spg::kTiles; ++t) {
         if (reg && !staged(t)) continue;
-        const double wgs = row_tiles(s, spg::kTileM[t]) * (double)ceil_div(s.N, spg::kTileN[t] / s.mats);
-        const double us = grid_us(t, reg, s.crooked, wgs, (double)s.kt, s.bytes);
-        if (us < best_us) {
-            best_us = us;
-            best = t;
-        }
+        const double us = grid_us(t, reg, s.crooked, rows_wgs(s, t), (double)s.kt, s.bytes);
+        if (us < best.us) best = Choice{t, us};
     }
     return best;
 }
 
-int choose_weights(const Common& c, int mats, bool reg) {
-    int best = spg::kTileNarrow;
-    double best_us = 1e30;
-    const double kt = (double)c.rows / (double)c.groups / 64.0 + 0.5;
-    const bool crooked = c.N % 64 != 0 || c.K % 64 != 0;
+// Gradients of the matrices: `mats` results of every group, a reduction over its rows.
+struct WeightsShape {
+    int64_t groups, M, N;
+    int mats;
+    double kt, bytes;
+    bool crooked;
+};
+WeightsShape weights_shape(const Common& c, int mats) {
+    return WeightsShape{c.groups, c.nk ? c.N : c.K, c.nk ? c.K : c.N, mats, (double)c.rows / (double)c.groups / 64.0 + 0.5,
+                        (double)mats * c.matrix() * c.groups, c.N % 64 != 0 || c.K % 64 != 0};
+}
+double weights_wgs(const WeightsShape& s, int t) {
+    return (double)s.groups * s.mats * (double)(ceil_div(s.M, spg::kTileM[t]) * ceil_div(s.N, spg::kTileN[t]));
+}
+
+Choice choose_weights(const WeightsShape& s, bool reg) {
+    Choice best{spg::kTileNarrow, 1e30};
     for (int t = 0; t < spg::kTiles; ++t) {
         if (reg && !staged(t)) continue;
-        const int64_t m = c.nk ? c.N : c.K, n = c.nk ? c.K : c.N;
-        const double wgs = (double)c.groups * mats * (double)(ceil_div(m, spg::kTileM[t]) * ceil_div(n, spg::kTileN[t]));
-        const double us = grid_us(t, reg, crooked, wgs, kt, 2.0 * mats * c.N * c.K * c.groups);
-        if (us < best_us) {
-            best_us = us;
+        const double us = grid_us(t, reg, s.crooked, weights_wgs(s, t), s.kt, s.bytes);
+        if (us < best.us) best = Choice{t, us};
+    }
+    return best;
+}
+
+// One launch for both gradients if its estimate is below that of two (as merge() in
+// product.hip): the tile, or -1.
+int choose_both(const RowsShape& x, const WeightsShape& w, bool reg, double apart) {
+    int best = -1;
+    for (int t : {(int)spg::kTileMid, (int)spg::kTileSmall}) {
+        const double nx = rows_wgs(x, t), nw = weights_wgs(w, t), all = nx + nw;
+        const double k = spg::tile_us(t, reg, x.crooked || w.crooked, (int64_t)all), s0 = spg::start_us(t, reg, (int64_t)all);
+        const double cx = k * (double)x.kt + s0, cw = k * w.kt + s0, slots = spg::slots(t, reg);
+        double us = std::max(std::max(cx, cw), all > slots ? (nx * cx + nw * cw) / slots + 0.5 * std::max(cx, cw) : 0.0);
+        us = spg::kLaunchUs + std::max(us, 3.0 + (x.bytes + w.bytes) / 5.0e6);
+        if (us < apart) {
+            apart = us;
             best = t;
         }
     }
@@ -132,14 +161,35 @@ int choose_weights(const Common& c, int mats, bool reg) {
 
 // ---- launches --------------------------------------------------------------------------
 
+template <int ET, int P>
+void launch_type(bool reg, int tile, const ProductArgs& a, const GroupArgs& g, int per, dim3 grid, hipStream_t st) {
+    constexpr bool ROWS_OF_X = P == spg::kRowsGatedNK || P == spg::kRowsGatedKN || P == spg::kRowsNK || P == spg::kRowsKN;
+    if constexpr (ROWS_OF_X) {
+        if (g.source) {
+            if (reg) spg::launch_grouped<ET, P, true, true>(tile, a, g, per, grid, st);
+            else spg::launch_grouped<ET, P, false, true>(tile, a, g, per, grid, st);
+            return;
+        }
+    }
+    if (reg) spg::launch_grouped<ET, P, true, false>(tile, a, g, per, grid, st);
+    else spg::launch_grouped<ET, P, false, false>(tile, a, g, per, grid, st);
+}
+
 template <int P>
 void launch_product(bool bf, bool reg, int tile, const ProductArgs& a, const GroupArgs& g, int per, dim3 grid, hipStream_t st) {
+    if (bf) launch_type<spg::kElBF16, P>(reg, tile, a, g, per, grid, st);
+    else launch_type<spg::kElF16, P>(reg, tile, a, g, per, grid, st);
+}
+
+template <int P>
+void launch_both(bool bf, bool reg, int tile, const ProductArgs& x, const ProductArgs& w, const GroupArgs& g, int nx, int per,
+                 dim3 grid, hipStream_t st) {
     if (bf) {
-        if (reg) spg::launch_grouped<spg::kElBF16, P, true>(tile, a, g, per, grid, st);
-        else spg::launch_grouped<spg::kElBF16, P, false>(tile, a, g, per, grid, st);
+        if (reg) spg::launch_group_gradients<spg::kElBF16, P, true>(tile, x, w, g, nx, per, grid, st);
+        else spg::launch_group_gradients<spg::kElBF16, P, false>(tile, x, w, g, nx, per, grid, st);
     } else {
-        if (reg) spg::launch_grouped<spg::kElF16, P, true>(tile, a, g, per, grid, st);
-        else spg::launch_grouped<spg::kElF16, P, false>(tile, a, g, per, grid, st);
+        if (reg) spg::launch_group_gradients<spg::kElF16, P, true>(tile, x, w, g, nx, per, grid, st);
+        else spg::launch_group_gradients<spg::kElF16, P, false>(tile, x, w, g, nx, per, grid, st);
     }
 }
 
@@ -161,9 +211,8 @@ constexpr int32_t kWhole = 1 << 28;   // k-tiles of a part: the reduction is not
 // rows of tiles rastered together, as set_grid in product.hip
 uint8_t raster_rows(int64_t rows) { return (uint8_t)(rows <= 8 ? std::max<int64_t>(rows, 1) : 4); }
 
-gemm_status run_rows(int product, const Common& c, bool reg, int tile, int mats, ProductArgs a, const int32_t* offsets,
-                     hipStream_t st) {
-    GroupArgs g = group_args(c, offsets, nullptr);
+// The rest of a rows product's arguments; returns its workgroups.
+int64_t rows_grid(const Common& c, int tile, int mats, ProductArgs& a) {
     a.zm = a.zn = a.split = 1;
     a.kt_part = kWhole;
     const int BM = spg::kTileM[tile];
@@ -172,13 +221,20 @@ gemm_status run_rows(int product, const Common& c, bool reg, int tile, int mats,
     a.tiles_m = 0;   // found on the device
     a.tiles_n = (int32_t)ceil_div(a.N, spg::kTileN[tile] / mats);
     a.group_m = raster_rows(tiles);
-    launch_any(product, c.bf, reg, tile, a, g, 0, dim3((unsigned)up(tiles * a.tiles_n, 8)), st);
+    return up(tiles * a.tiles_n, 8);
+}
+
+gemm_status run_rows(int product, const Common& c, bool reg, int tile, int mats, ProductArgs a, const int32_t* offsets,
+                     const int32_t* source, hipStream_t st) {
+    const int64_t wgs = rows_grid(c, tile, mats, a);
+    launch_any(product, c.bf, reg, tile, a, group_args(c, offsets, source), 0, dim3((unsigned)wgs), st);
     return launched();
 }
 
-// dW (and with two results dWg, dWu): D rows of `ldd` bytes, two matrices `second` bytes apart
-gemm_status run_weights(const Common& c, int mats, bool reg, int tile, const char* D, int64_t ldd, int64_t d_cols, int64_t second,
-                        const char* X, int64_t ldx, int64_t x_cols, void* dW, void* dW1, const int32_t* offsets, hipStream_t st) {
+// dW's operands (and with two results dWg's and dWu's): D rows of `ldd` bytes, two matrices
+// `second` bytes apart
+ProductArgs weights_args(const Common& c, int mats, const char* D, int64_t ldd, int64_t d_cols, int64_t second, const char* X,
+                         int64_t ldx, int64_t x_cols, void* dW, void* dW1) {
     ProductArgs w{};
     w.A = c.nk ? D : X;
     if (mats == 2) {
@@ -198,12 +254,42 @@ gemm_status run_weights(const Common& c, int mats, bool reg, int tile, const cha
     w.zm = (uint8_t)(c.nk ? mats : 1);
     w.zn = (uint8_t)(c.nk ? 1 : mats);
     w.kt_part = kWhole;
+    return w;
+}
+
+// Its tiles; returns the workgroups of a group.
+int64_t weights_grid(int tile, ProductArgs& w) {
     w.tiles_m = (int32_t)ceil_div(w.M, spg::kTileM[tile]);
     w.tiles_n = (int32_t)ceil_div(w.N, spg::kTileN[tile]);
     w.group_m = raster_rows((int64_t)w.tiles_m * w.zm);
-    const int64_t per = up((int64_t)w.tiles_m * w.tiles_n * mats, 8);
+    return up((int64_t)w.tiles_m * w.zm * w.tiles_n * w.zn, 8);
+}
+
+gemm_status run_weights(const Common& c, bool reg, int tile, ProductArgs w, const int32_t* offsets, hipStream_t st) {
+    const int64_t per = weights_grid(tile, w);
     launch_any(spg::kGroupWeights, c.bf, reg, tile, w, group_args(c, offsets, nullptr), (int)per, dim3((unsigned)(per * c.groups)), st);
     return launched();
+}
+
+// Both gradients, in one launch where `both` names a tile for it.
+gemm_status run_gradients(int product, const Common& c, bool regx, bool regw, const int* dx, const int* dw, const int* both,
+                          ProductArgs x, ProductArgs w, const int32_t* offsets, hipStream_t st) {
+    const bool reg = regx || regw;
+    if (both[reg] >= 0) {
+        const int t = both[reg];
+        const int64_t nx = rows_grid(c, t, 1, x), per = weights_grid(t, w);
+        const GroupArgs g = group_args(c, offsets, nullptr);
+        const dim3 grid((unsigned)(nx + per * c.groups));
+        switch (product) {
+            case spg::kRowsSumNK: launch_both<spg::kRowsSumNK>(c.bf, reg, t, x, w, g, (int)nx, (int)per, grid, st); break;
+            case spg::kRowsSumKN: launch_both<spg::kRowsSumKN>(c.bf, reg, t, x, w, g, (int)nx, (int)per, grid, st); break;
+            case spg::kRowsNK: launch_both<spg::kRowsNK>(c.bf, reg, t, x, w, g, (int)nx, (int)per, grid, st); break;
+            default: launch_both<spg::kRowsKN>(c.bf, reg, t, x, w, g, (int)nx, (int)per, grid, st); break;
+        }
+        return launched();
+    }
+    const gemm_status e = run_rows(product, c, regx, dx[regx], 1, x, offsets, nullptr, st);
+    return e != GEMM_OK ? e : run_weights(c, regw, dw[regw], w, offsets, st);
 }
 
 template <bool BF16, bool DUAL>
@@ -222,10 +308,13 @@ gemm_status run_stream(const Common& c, bool dual, const ProductArgs& a, const i
     return launched();
 }
 
+spg::GatherArgs gather_args(const Common& c, const void* X, const int32_t* source, void* to) {
+    return spg::GatherArgs{(const char*)X, (char*)to, source, c.rows, c.K * 2, (int32_t)(c.pitch() / 16), (int32_t)c.tokens};
+}
+int64_t gather_wgs(const Common& c) { return ceil_div(c.rows * (c.pitch() / 16), 256); }
+
 gemm_status run_gather(const Common& c, const void* X, const int32_t* source, void* to, hipStream_t st) {
-    const int64_t per = c.pitch() / 16;
-    const spg::GatherArgs a{(const char*)X, (char*)to, source, c.rows, c.K * 2, (int32_t)per, (int32_t)c.tokens};
-    hipLaunchKernelGGL(spg::gather_rows<2>, spread(ceil_div(c.rows * per, 256)), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((spg::gather_rows<>), spread(gather_wgs(c)), dim3(256), 0, st, gather_args(c, X, source, to));
     return launched();
 }
 
@@ -264,22 +353,22 @@ bool streams(const Common& c, bool along) {
 }
 
 // Operands' first row and last byte within 32-bit offsets of the stream
-bool fits(int64_t rows, int64_t row_bytes) { return rows * row_bytes + 64 < kMaxBytes; }
+bool fits(int64_t rows, int64_t row_bytes) { return rows * row_bytes + 2048 < kMaxBytes; }
 
 }  // namespace
 
 struct gemm_grouped_plan {
     Common c;
-    bool simple, simple_back, stream, stream_back;
-    int fwd[2], dx[2], dw[2];      // tile classes [register-staged]
+    bool simple, simple_back, stream, stream_back, gather;   // gather: X's rows copied into their groups' order
+    int fwd[2], dx[2], dw[2], both[2];   // tile classes [register-staged]; both: -1 for two launches
     int64_t ws_run, ws_back;
 };
 
 struct gemm_experts_plan {
     Common c;
     int act;
-    bool simple, simple_back, stream;
-    int fwd[2], dx[2], dw[2];
+    bool simple, simple_back, stream, gather;
+    int fwd[2], dx[2], dw[2], both[2];
     int64_t np;                    // columns of dG and of dU in the workspace
     int64_t ws_run, ws_back, off_x;
 };
@@ -301,12 +390,17 @@ gemm_status gemm_grouped_create(gemm_grouped_handle* out, int64_t rows, int64_t 
     p->stream_back = !p->simple_back && streams(c, !c.nk) && fits(rows, N * 2);
     const double live = (double)c.live(), io = 2.0 * rows * (N + K) + live * c.matrix();
     const bool crooked = N % 64 != 0 || K % 64 != 0;
+    const RowsShape fwd{rows, c.live(), N, ceil_div(K, 64), 1, io, crooked}, dx{rows, c.live(), K, ceil_div(N, 64), 1, io, crooked};
+    const WeightsShape dw = weights_shape(c, 1);
     for (int r = 0; r < 2; ++r) {
-        p->fwd[r] = choose_rows(RowsShape{rows, c.live(), N, ceil_div(K, 64), 1, io, crooked}, r == 1);
-        p->dx[r] = choose_rows(RowsShape{rows, c.live(), K, ceil_div(N, 64), 1, io, crooked}, r == 1);
-        p->dw[r] = choose_weights(c, 1, r == 1);
+        const Choice x = choose_rows(dx, r == 1), w = choose_weights(dw, r == 1);
+        p->fwd[r] = choose_rows(fwd, r == 1).tile;
+        p->dx[r] = x.tile;
+        p->dw[r] = w.tile;
+        p->both[r] = choose_both(dx, dw, r == 1, x.us + w.us);
     }
-    p->ws_run = p->simple || p->stream ? 0 : c.gathered();
+    p->gather = tokens >= 0 && !fits(tokens, K * 2);
+    p->ws_run = p->simple || p->stream || !p->gather ? 0 : c.gathered();
     p->ws_back = p->simple_back ? 0 : c.gathered();
     *out = p;
     return GEMM_OK;
@@ -337,14 +431,15 @@ gemm_status gemm_grouped_run(gemm_grouped_handle h, const void* X, const void* W
     if (h->simple) return simple_rows(c, a, c.nk, c.K, 0, false, offsets, source, stream);
     if (h->stream) return run_stream(c, false, a, offsets, source, stream);
     if (small_workspace(workspace, workspace_bytes, h->ws_run)) return GEMM_ERR_INVALID_ARG;
-    if (source) {
+    if (h->gather) {
         const gemm_status e = run_gather(c, X, source, workspace, stream);
         if (e != GEMM_OK) return e;
         a.A = (const char*)workspace;
         a.lda = (uint32_t)c.pitch();
+        source = nullptr;
     }
     const bool reg = a.lda % 4 != 0 || !words(a.A) || a.ldb % 4 != 0 || !words(W);
-    return run_rows(c.nk ? spg::kRowsNK : spg::kRowsKN, c, reg, h->fwd[reg], 1, a, offsets, stream);
+    return run_rows(c.nk ? spg::kRowsNK : spg::kRowsKN, c, reg, h->fwd[reg], 1, a, offsets, source, stream);
 }
 
 gemm_status gemm_grouped_backward(gemm_grouped_handle h, const void* dY, const void* X, const void* W,
@@ -357,42 +452,43 @@ gemm_status gemm_grouped_backward(gemm_grouped_handle h, const void* dY, const v
     if (!offsets) return GEMM_ERR_INVALID_ARG;
     if (c.rows > 0 && c.N > 0 && (!dY || (dX && !W) || (dW && !X && c.tokens != 0))) return GEMM_ERR_INVALID_ARG;
     if (small_workspace(workspace, workspace_bytes, c.N > 0 ? h->ws_back : 0)) return GEMM_ERR_INVALID_ARG;
-    if (dX && c.rows > 0) {
-        ProductArgs a{};
-        a.A = (const char*)dY;
-        a.B[0] = (const char*)W;
-        a.C = dX;
-        a.M = (int32_t)c.rows;
-        a.N = (int32_t)c.K;
-        a.K = (int32_t)c.N;
-        a.lda = (uint32_t)(c.N * 2);
-        a.ldb = (uint32_t)((c.nk ? c.K : c.N) * 2);
-        a.b_cols = (int32_t)c.K;
-        a.segments = 1;
-        gemm_status e;
-        if (h->simple_back) {
-            e = simple_rows(c, a, !c.nk, c.N, 0, false, offsets, nullptr, stream);
-        } else if (h->stream_back) {
-            e = run_stream(c, false, a, offsets, nullptr, stream);
-        } else {
-            const bool reg = a.lda % 4 != 0 || !words(dY) || a.ldb % 4 != 0 || !words(W);
-            e = run_rows(c.nk ? spg::kRowsKN : spg::kRowsNK, c, reg, h->dx[reg], 1, a, offsets, stream);
-        }
-        if (e != GEMM_OK) return e;
+    const bool rows = dX && c.rows > 0, weights = dW && c.N > 0;
+    ProductArgs a{};
+    a.A = (const char*)dY;
+    a.B[0] = (const char*)W;
+    a.C = dX;
+    a.M = (int32_t)c.rows;
+    a.N = (int32_t)c.K;
+    a.K = (int32_t)c.N;
+    a.lda = (uint32_t)(c.N * 2);
+    a.ldb = (uint32_t)((c.nk ? c.K : c.N) * 2);
+    a.b_cols = (int32_t)c.K;
+    a.segments = 1;
+    if (h->simple_back) {
+        gemm_status e = GEMM_OK;
+        if (rows) e = simple_rows(c, a, !c.nk, c.N, 0, false, offsets, nullptr, stream);
+        return e != GEMM_OK || !weights ? e : simple_weights(c, dY, c.N, X, dW, offsets, source, stream);
     }
-    if (!dW || c.N == 0) return GEMM_OK;
-    if (h->simple_back) return simple_weights(c, dY, c.N, X, dW, offsets, source, stream);
     const char* x = (const char*)X;
     int64_t ldx = c.K * 2, cols = c.K;
-    if (source) {
+    if (weights && source) {
         const gemm_status e = run_gather(c, X, source, workspace, stream);
         if (e != GEMM_OK) return e;
         x = (const char*)workspace;
         ldx = c.pitch();
         cols = up(c.K, 8);
     }
-    const bool reg = c.N % 2 != 0 || !words(dY) || ldx % 4 != 0 || !words(x);
-    return run_weights(c, 1, reg, h->dw[reg], (const char*)dY, c.N * 2, c.N, 0, x, ldx, cols, dW, nullptr, offsets, stream);
+    const ProductArgs w = weights_args(c, 1, (const char*)dY, c.N * 2, c.N, 0, x, ldx, cols, dW, nullptr);
+    const bool regd = a.lda % 4 != 0 || !words(dY);
+    const bool regx = regd || a.ldb % 4 != 0 || !words(W), regw = regd || ldx % 4 != 0 || !words(x);
+    const int product = c.nk ? spg::kRowsKN : spg::kRowsNK;
+    if (rows && weights && !h->stream_back)
+        return run_gradients(product, c, regx, regw, h->dx, h->dw, h->both, a, w, offsets, stream);
+    gemm_status e = GEMM_OK;
+    if (rows)
+        e = h->stream_back ? run_stream(c, false, a, offsets, nullptr, stream)
+                           : run_rows(product, c, regx, h->dx[regx], 1, a, offsets, nullptr, stream);
+    return e != GEMM_OK || !weights ? e : run_weights(c, regw, h->dw[regw], w, offsets, stream);
 }
 
 gemm_status gemm_grouped_destroy(gemm_grouped_handle h) {
@@ -416,12 +512,17 @@ gemm_status gemm_experts_create(gemm_experts_handle* out, int64_t rows, int64_t 
     p->stream = !p->simple && streams(c, c.nk) && fits(std::max(rows, tokens), K * 2);
     const double live = (double)c.live(), io = 2.0 * rows * (N + K) + 2.0 * live * c.matrix();
     const bool crooked = N % 64 != 0 || K % 64 != 0;
+    const RowsShape fwd{rows, c.live(), N, ceil_div(K, 64), 2, io, crooked}, dx{rows, c.live(), K, 2 * ceil_div(N, 64), 1, io, crooked};
+    const WeightsShape dw = weights_shape(c, 2);
     for (int r = 0; r < 2; ++r) {
-        p->fwd[r] = choose_rows(RowsShape{rows, c.live(), N, ceil_div(K, 64), 2, io, crooked}, r == 1);
-        p->dx[r] = choose_rows(RowsShape{rows, c.live(), K, 2 * ceil_div(N, 64), 1, io, crooked}, r == 1);
-        p->dw[r] = choose_weights(c, 2, r == 1);
+        const Choice x = choose_rows(dx, r == 1), w = choose_weights(dw, r == 1);
+        p->fwd[r] = choose_rows(fwd, r == 1).tile;
+        p->dx[r] = x.tile;
+        p->dw[r] = w.tile;
+        p->both[r] = choose_both(dx, dw, r == 1, x.us + w.us);
     }
-    p->ws_run = p->simple || p->stream ? 0 : c.gathered();
+    p->gather = tokens >= 0 && !fits(tokens, K * 2);
+    p->ws_run = p->simple || p->stream || !p->gather ? 0 : c.gathered();
     p->off_x = up(rows * p->np * 4, kAlign);
     p->ws_back = p->off_x + (p->simple_back ? 0 : c.gathered());
     *out = p;
@@ -457,14 +558,15 @@ gemm_status gemm_experts_run(gemm_experts_handle h, const void* X, const void* W
     if (h->simple) return simple_rows(c, a, c.nk, c.K, 0, true, offsets, source, stream);
     if (h->stream) return run_stream(c, true, a, offsets, source, stream);
     if (small_workspace(workspace, workspace_bytes, h->ws_run)) return GEMM_ERR_INVALID_ARG;
-    if (source) {
+    if (h->gather) {
         const gemm_status e = run_gather(c, X, source, workspace, stream);
         if (e != GEMM_OK) return e;
         a.A = (const char*)workspace;
         a.lda = (uint32_t)c.pitch();
+        source = nullptr;
     }
     const bool reg = a.lda % 4 != 0 || !words(a.A) || a.ldb % 4 != 0 || !words(Wg) || !words(Wu);
-    return run_rows(c.nk ? spg::kRowsGatedNK : spg::kRowsGatedKN, c, reg, h->fwd[reg], 2, a, offsets, stream);
+    return run_rows(c.nk ? spg::kRowsGatedNK : spg::kRowsGatedKN, c, reg, h->fwd[reg], 2, a, offsets, source, stream);
 }
 
 gemm_status gemm_experts_backward(gemm_experts_handle h, const void* dH, const void* X, const void* Wg, const void* Wu,
@@ -481,57 +583,48 @@ gemm_status gemm_experts_backward(gemm_experts_handle h, const void* dH, const v
     }
     const bool simple = h->simple_back || c.rows == 0 || c.N == 0;
     uint16_t* D = (uint16_t*)workspace;
+    const char* x = (const char*)X;
+    int64_t ldx = c.K * 2, cols = c.K;
     if (c.rows > 0 && c.N > 0) {
-        const dim3 grid((unsigned)ceil_div(c.rows * (h->np / 8), 256));
-        if (c.bf) hipLaunchKernelGGL((spg::gated_slopes<true>), grid, dim3(256), 0, stream, (const uint16_t*)dH,
-                                     (const uint16_t*)G, (const uint16_t*)U, D, (int)c.rows, (int)c.N, (int)h->np, h->act);
-        else hipLaunchKernelGGL((spg::gated_slopes<false>), grid, dim3(256), 0, stream, (const uint16_t*)dH,
-                                (const uint16_t*)G, (const uint16_t*)U, D, (int)c.rows, (int)c.N, (int)h->np, h->act);
+        spg::SlopeArgs d{(const uint16_t*)dH, (const uint16_t*)G, (const uint16_t*)U, D, (int32_t)c.rows, (int32_t)c.N,
+                         (int32_t)h->np, h->act, ceil_div(c.rows * (h->np / 8), 256)};
+        spg::GatherArgs xs{};
+        int64_t wgs = d.slopes;
+        if (source && !simple) {
+            x = (const char*)workspace + h->off_x;
+            xs = gather_args(c, X, source, (void*)x);
+            wgs += gather_wgs(c);
+            ldx = c.pitch();
+            cols = up(c.K, 8);
+        }
+        if (c.bf) hipLaunchKernelGGL((spg::grouped_slopes<true>), spread(wgs), dim3(256), 0, stream, d, xs);
+        else hipLaunchKernelGGL((spg::grouped_slopes<false>), spread(wgs), dim3(256), 0, stream, d, xs);
         const gemm_status e = launched();
         if (e != GEMM_OK) return e;
     }
-    if (c.rows > 0) {
-        // dX = [dG dU] . [Wg; Wu]: one sum over both segments
-        ProductArgs a{};
-        a.A = (const char*)D;
-        a.B[0] = (const char*)Wg;
-        a.B[1] = (const char*)Wu;
-        a.C = dX;
-        a.M = (int32_t)c.rows;
-        a.N = (int32_t)c.K;
-        a.K = (int32_t)c.N;
-        a.lda = (uint32_t)(h->np * 4);
-        a.ldb = (uint32_t)((c.nk ? c.K : c.N) * 2);
-        a.b_cols = (int32_t)c.K;
-        a.segments = 2;
-        gemm_status e;
-        if (simple) {
-            e = simple_rows(c, a, !c.nk, 2 * h->np, h->np, false, offsets, nullptr, stream);
-        } else {
-            const bool reg = a.ldb % 4 != 0 || !words(Wg) || !words(Wu);
-            e = run_rows(c.nk ? spg::kRowsSumNK : spg::kRowsSumKN, c, reg, h->dx[reg], 1, a, offsets, stream);
-        }
-        if (e != GEMM_OK) return e;
-    }
-    if (c.N == 0) return GEMM_OK;
+    // dX = [dG dU] . [Wg; Wu]: one sum over both segments
+    ProductArgs a{};
+    a.A = (const char*)D;
+    a.B[0] = (const char*)Wg;
+    a.B[1] = (const char*)Wu;
+    a.C = dX;
+    a.M = (int32_t)c.rows;
+    a.N = (int32_t)c.K;
+    a.K = (int32_t)c.N;
+    a.lda = (uint32_t)(h->np * 4);
+    a.ldb = (uint32_t)((c.nk ? c.K : c.N) * 2);
+    a.b_cols = (int32_t)c.K;
+    a.segments = 2;
     if (simple) {
-        for (int z = 0; z < 2; ++z) {
-            const gemm_status e = simple_weights(c, D + z * h->np, 2 * h->np, X, z ? dWu : dWg, offsets, source, stream);
-            if (e != GEMM_OK) return e;
-        }
-        return GEMM_OK;
+        gemm_status e = GEMM_OK;
+        if (c.rows > 0) e = simple_rows(c, a, !c.nk, 2 * h->np, h->np, false, offsets, nullptr, stream);
+        for (int z = 0; z < 2 && c.N > 0 && e == GEMM_OK; ++z)
+            e = simple_weights(c, D + z * h->np, 2 * h->np, X, z ? dWu : dWg, offsets, source, stream);
+        return e;
     }
-    const char* x = (const char*)X;
-    int64_t ldx = c.K * 2, cols = c.K;
-    if (source) {
-        x = (const char*)workspace + h->off_x;
-        const gemm_status e = run_gather(c, X, source, (void*)x, stream);
-        if (e != GEMM_OK) return e;
-        ldx = c.pitch();
-        cols = up(c.K, 8);
-    }
-    const bool reg = ldx % 4 != 0 || !words(x);
-    return run_weights(c, 2, reg, h->dw[reg], (const char*)D, h->np * 4, h->np, h->np * 2, x, ldx, cols, dWg, dWu, offsets, stream);
+    const ProductArgs w = weights_args(c, 2, (const char*)D, h->np * 4, h->np, h->np * 2, x, ldx, cols, dWg, dWu);
+    const bool regx = a.ldb % 4 != 0 || !words(Wg) || !words(Wu), regw = ldx % 4 != 0 || !words(x);
+    return run_gradients(c.nk ? spg::kRowsSumNK : spg::kRowsSumKN, c, regx, regw, h->dx, h->dw, h->both, a, w, offsets, stream);
 }
 
 gemm_status gemm_experts_destroy(gemm_experts_handle h) {

@@ -91,21 +91,20 @@ __device__ __forceinline__ void raster(int at, int rows, int cols, int group_m, 
 // The rows of every group times its matrix on the tiled kernel (product_tile_of): a workgroup
 // finds its tile among all groups' row tiles and takes its group for the whole problem.  The
 // grid covers the most row tiles that `rows` rows in `groups` groups can come to; what is left
-// over ends at once, and comes last.
+// over ends at once, and comes last.  GATHER: rows of X by their source, read where they lie
+// (gathered into a copy first they cost a pass of their own: 23 us of 24576 rows of 4 KiB).
 template <int ET, bool B_N, bool DUAL, bool SEG, bool REG, int BM, int BN, int WM, int WN, int S, bool DEEP, int KG, bool TAIL,
-          int WPS>
-__global__ void __launch_bounds__((ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP, KG>::NT), WPS)
-grouped_rows(ProductArgs args, GroupArgs g) {
-    __shared__ __attribute__((aligned(1024))) char lds[ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP, KG>::LDS];
+          bool GATHER>
+__device__ __forceinline__ void rows_tile(ProductArgs args, const GroupArgs& g, int wg, SPG_LDS char* lds) {
     const int lane = threadIdx.x & 63;
     const int rows = all_units<BM>(g, lane);
-    const int at = xcd_place(blockIdx.x, rows * args.tiles_n);
+    const int at = xcd_place(wg, rows * args.tiles_n);
     if (at < 0) return;
     int tm, tn;
     raster(at, rows, args.tiles_n, args.group_m, tm, tn);
     const Found f = find_unit<BM>(g, tm, lane);
     const size_t out = (size_t)f.g.first * args.N * 2;
-    args.A += (size_t)f.g.first * args.lda;
+    if (!GATHER) args.A += (size_t)f.g.first * args.lda;
     args.B[0] += (size_t)f.e * g.b_step;
     if (DUAL || SEG) args.B[1] += (size_t)f.e * g.b_step;
     args.C = (char*)args.C + out;
@@ -115,20 +114,27 @@ grouped_rows(ProductArgs args, GroupArgs g) {
     }
     args.M = f.g.n;
     args.part = nullptr;
-    product_tile_of<ET, false, B_N, DUAL, SEG, REG, BM, BN, WM, WN, S, DEEP, KG, TAIL>(args, f.unit, tn, 0, (SPG_LDS char*)lds);
+    product_tile_of<ET, false, B_N, DUAL, SEG, REG, BM, BN, WM, WN, S, DEEP, KG, TAIL, GATHER, true>(
+        args, f.unit, tn, 0, lds, SourceRows{GATHER ? g.source + f.g.first : nullptr, g.tokens});
+}
+
+template <int ET, bool B_N, bool DUAL, bool SEG, bool REG, int BM, int BN, int WM, int WN, int S, bool DEEP, int KG, bool TAIL,
+          int WPS, bool GATHER>
+__global__ void __launch_bounds__((ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP, KG>::NT), WPS)
+grouped_rows(ProductArgs args, GroupArgs g) {
+    __shared__ __attribute__((aligned(1024))) char lds[ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP, KG>::LDS];
+    rows_tile<ET, B_N, DUAL, SEG, REG, BM, BN, WM, WN, S, DEEP, KG, TAIL, GATHER>(args, g, blockIdx.x, (SPG_LDS char*)lds);
 }
 
 // The weights' gradients of every group: the reduction runs over the group's rows.  `per`
 // workgroups a group (a multiple of 8), so that every group's tiles are spread over all XCDs
 // whatever its rows.  A group without rows writes zeros.
-template <int ET, bool REG, int BM, int BN, int WM, int WN, int S, bool DEEP, int KG, int WPS>
-__global__ void __launch_bounds__((ProductGeom<false, BM, BN, WM, WN, S, DEEP, KG>::NT), WPS)
-grouped_weights(ProductArgs args, GroupArgs g, int per) {
+template <int ET, bool REG, int BM, int BN, int WM, int WN, int S, bool DEEP, int KG>
+__device__ __forceinline__ void weights_tile(ProductArgs args, const GroupArgs& g, int per, int wg, SPG_LDS char* lds) {
     using G = ProductGeom<false, BM, BN, WM, WN, S, DEEP, KG>;
-    __shared__ __attribute__((aligned(1024))) char lds[G::LDS];
-    const int e = blockIdx.x / per;
+    const int e = wg / per;
     const int rows = args.tiles_m * args.zm, cols = args.tiles_n * args.zn;
-    const int at = xcd_place(blockIdx.x - e * per, rows * cols);
+    const int at = xcd_place(wg - e * per, rows * cols);
     if (at < 0) return;
     int tm, tn;
     raster(at, rows, cols, args.group_m, tm, tn);
@@ -149,7 +155,25 @@ grouped_weights(ProductArgs args, GroupArgs g, int per) {
     if (args.zn == 2) args.B[1] += (size_t)gr.first * args.ldb;
     args.K = gr.n;
     args.part = nullptr;
-    product_tile_of<ET, true, true, false, false, REG, BM, BN, WM, WN, S, DEEP, KG, false>(args, tm, tn, 0, (SPG_LDS char*)lds);
+    product_tile_of<ET, true, true, false, false, REG, BM, BN, WM, WN, S, DEEP, KG, false>(args, tm, tn, 0, lds);
+}
+
+template <int ET, bool REG, int BM, int BN, int WM, int WN, int S, bool DEEP, int KG, int WPS>
+__global__ void __launch_bounds__((ProductGeom<false, BM, BN, WM, WN, S, DEEP, KG>::NT), WPS)
+grouped_weights(ProductArgs args, GroupArgs g, int per) {
+    __shared__ __attribute__((aligned(1024))) char lds[ProductGeom<false, BM, BN, WM, WN, S, DEEP, KG>::LDS];
+    weights_tile<ET, REG, BM, BN, WM, WN, S, DEEP, KG>(args, g, per, blockIdx.x, (SPG_LDS char*)lds);
+}
+
+// Both gradients in one launch, as gradients_kernel: workgroups 0 .. nx-1 (a multiple of 8) the
+// rows', the others the matrices'.
+template <int ET, bool B_N, bool SEG, bool REG, int BM, int BN, int WM, int WN, int S, int KG>
+__global__ void __launch_bounds__((ProductGeom<false, BM, BN, WM, WN, S, false, KG>::NT))
+grouped_gradients(ProductArgs x, ProductArgs w, GroupArgs g, int nx, int per) {
+    __shared__ __attribute__((aligned(1024))) char lds[ProductGeom<false, BM, BN, WM, WN, S, false, KG>::LDS];
+    const int wg = blockIdx.x;
+    if (wg < nx) rows_tile<ET, B_N, false, SEG, REG, BM, BN, WM, WN, S, false, KG, !(SEG && B_N), false>(x, g, wg, (SPG_LDS char*)lds);
+    else weights_tile<ET, REG, BM, BN, WM, WN, S, false, KG>(w, g, per, wg - nx, (SPG_LDS char*)lds);
 }
 
 // Few rows a group, matrices [N,K]: the product is the reading of the matrices, as in
@@ -290,9 +314,7 @@ struct GatherArgs {
     int32_t per, tokens;      // 16-byte chunks of a destination row; rows of src
 };
 
-template <int ES>
-__global__ void __launch_bounds__(256) gather_rows(GatherArgs a) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+__device__ __forceinline__ void gather_at(int64_t i, const GatherArgs& a) {
     const int64_t r = i / a.per;
     if (r >= a.rows) return;
     const int64_t c = (i - r * a.per) * 16, left = a.row_bytes - c;
@@ -300,14 +322,34 @@ __global__ void __launch_bounds__(256) gather_rows(GatherArgs a) {
     u32x4 v = {};
     if (from >= 0 && from < a.tokens && left > 0) {
         const char* s = a.src + from * a.row_bytes + c;
-        struct __attribute__((packed, aligned(ES))) B { u32x4 v; };
-        if (left >= 16) v = ((const B*)s)->v;
+        if (left >= 16) v = ((const Bytes16*)s)->v;
         else
 #pragma unroll
             for (int e = 0; e < 16; e += 2)
                 if (e < left) v[e >> 2] |= (uint32_t)*(const uint16_t*)(s + e) << ((e & 3) * 8);
     }
     *(u32x4*)(a.dst + i * 16) = v;
+}
+
+template <typename = void>   // a template, so that every unit may hold it
+__global__ void __launch_bounds__(256) gather_rows(GatherArgs a) {
+    gather_at(((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x, a);
+}
+
+// The elementwise part of the gated backward pass (gated_slopes), and in the same launch the
+// rows of X that the matrices' gradients read: workgroups 0 .. slopes-1 the one, the rest the other.
+struct SlopeArgs {
+    const uint16_t *dH, *G, *U;
+    uint16_t* D;
+    int32_t M, N, np, act;
+    int64_t slopes;
+};
+
+template <bool BF16>
+__global__ void __launch_bounds__(256) grouped_slopes(SlopeArgs a, GatherArgs x) {
+    const int64_t wg = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    if (wg < a.slopes) slopes_of<BF16>(wg * 256 + threadIdx.x, a.dH, a.G, a.U, a.D, a.M, a.N, a.np, a.act);
+    else if (x.dst) gather_at((wg - a.slopes) * 256 + threadIdx.x, x);
 }
 
 // Any strides, one thread per output, a group's outputs in blockIdx.y: for reductions and rows

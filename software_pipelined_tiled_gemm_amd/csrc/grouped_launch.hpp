@@ -19,12 +19,18 @@ enum {
     kGroupProducts = 7
 };
 
-// Tile classes are those of product_launch.hpp.  `per`: workgroups of a group (kGroupWeights)
-template <int ET, int P, bool REG>
+// Tile classes are those of product_launch.hpp.  `per`: workgroups of a group (kGroupWeights);
+// GATHER: rows of X by their source (kRowsGated*, kRowsNK and kRowsKN only)
+template <int ET, int P, bool REG, bool GATHER>
 void launch_grouped(int tile, const ProductArgs& a, const GroupArgs& g, int per, dim3 grid, hipStream_t st);
 
+// dX and dW in one launch (tiles Mid and Small); P: kRowsSumNK, kRowsSumKN, kRowsNK or kRowsKN
+template <int ET, int P, bool REG>
+void launch_group_gradients(int tile, const ProductArgs& x, const ProductArgs& w, const GroupArgs& g, int nx, int per, dim3 grid,
+                            hipStream_t st);
+
 #ifdef SPG_DEFINE_GROUPED
-template <int ET, int P, bool REG, int BM, int BN, int WM, int WN, int S, bool DEEP, int KG, bool TAIL, int WPS>
+template <int ET, int P, bool REG, bool GATHER, int BM, int BN, int WM, int WN, int S, bool DEEP, int KG, bool TAIL, int WPS>
 void launch_group_kernel(const ProductArgs& a, const GroupArgs& g, int per, dim3 grid, hipStream_t st) {
     constexpr bool DUAL = P == kRowsGatedNK || P == kRowsGatedKN, SEG = P == kRowsSumNK || P == kRowsSumKN;
     constexpr bool BN_ = P == kRowsGatedKN || P == kRowsSumNK || P == kRowsKN;
@@ -32,47 +38,65 @@ void launch_group_kernel(const ProductArgs& a, const GroupArgs& g, int per, dim3
     if constexpr (P == kGroupWeights)
         hipLaunchKernelGGL((grouped_weights<ET, REG, BM, BN, WM, WN, S, DEEP, KG, WPS>), grid, wg, 0, st, a, g, per);
     else
-        hipLaunchKernelGGL((grouped_rows<ET, BN_, DUAL, SEG, REG, BM, BN, WM, WN, S, DEEP, KG, TAIL, WPS>), grid, wg, 0, st, a, g);
+        hipLaunchKernelGGL((grouped_rows<ET, BN_, DUAL, SEG, REG, BM, BN, WM, WN, S, DEEP, KG, TAIL, WPS, GATHER>), grid, wg, 0, st, a, g);
 }
 
 // Tails as in launch_tile (product_launch.hpp)
-template <int ET, int P, bool REG, int BM, int BN, int WM, int WN, int S, bool DEEP, int KG, int WPS = 1>
+template <int ET, int P, bool REG, bool GATHER, int BM, int BN, int WM, int WN, int S, bool DEEP, int KG, int WPS = 1>
 void launch_group_tile(const ProductArgs& a, const GroupArgs& g, int per, dim3 grid, hipStream_t st) {
     if constexpr (P == kGroupWeights || P == kRowsSumNK) {
-        launch_group_kernel<ET, P, REG, BM, BN, WM, WN, S, DEEP, KG, false, WPS>(a, g, per, grid, st);
+        launch_group_kernel<ET, P, REG, GATHER, BM, BN, WM, WN, S, DEEP, KG, false, WPS>(a, g, per, grid, st);
     } else if constexpr (BM == 256 && !REG) {
-        if (a.K % 8 == 0) launch_group_kernel<ET, P, REG, BM, BN, WM, WN, S, DEEP, KG, false, WPS>(a, g, per, grid, st);
-        else launch_group_kernel<ET, P, REG, BM, BN, WM, WN, S, BN == 256, KG, true, WPS>(a, g, per, grid, st);
+        if (a.K % 8 == 0) launch_group_kernel<ET, P, REG, GATHER, BM, BN, WM, WN, S, DEEP, KG, false, WPS>(a, g, per, grid, st);
+        else launch_group_kernel<ET, P, REG, GATHER, BM, BN, WM, WN, S, BN == 256, KG, true, WPS>(a, g, per, grid, st);
     } else {
-        launch_group_kernel<ET, P, REG, BM, BN, WM, WN, S, DEEP, KG, true, WPS>(a, g, per, grid, st);
+        launch_group_kernel<ET, P, REG, GATHER, BM, BN, WM, WN, S, DEEP, KG, true, WPS>(a, g, per, grid, st);
     }
 }
 
-template <int ET, int P, bool REG>
+template <int ET, int P, bool REG, bool GATHER>
 void launch_grouped(int tile, const ProductArgs& a, const GroupArgs& g, int per, dim3 grid, hipStream_t st) {
     constexpr bool DUAL = P == kRowsGatedNK || P == kRowsGatedKN;
     // the ping-pong schedule as in launch_product
     constexpr bool DEEP = P != kRowsGatedKN && P != kGroupWeights;
     if constexpr (!REG) {
         if (tile == kTileBig) {
-            if constexpr (DUAL) launch_group_tile<ET, P, REG, 256, 256, 64, 128, 2, DEEP, 1>(a, g, per, grid, st);
-            else launch_group_tile<ET, P, REG, 256, 256, 128, 64, 2, DEEP, 1>(a, g, per, grid, st);
+            if constexpr (DUAL) launch_group_tile<ET, P, REG, GATHER, 256, 256, 64, 128, 2, DEEP, 1>(a, g, per, grid, st);
+            else launch_group_tile<ET, P, REG, GATHER, 256, 256, 128, 64, 2, DEEP, 1>(a, g, per, grid, st);
         } else if (tile == kTileTall) {
-            launch_group_tile<ET, P, REG, 256, 128, 64, 64, 3, false, 1>(a, g, per, grid, st);
+            launch_group_tile<ET, P, REG, GATHER, 256, 128, 64, 64, 3, false, 1>(a, g, per, grid, st);
         } else if (tile == kTileMid) {
-            launch_group_tile<ET, P, REG, 128, 128, 32, 64, 4, false, 1>(a, g, per, grid, st);
+            launch_group_tile<ET, P, REG, GATHER, 128, 128, 32, 64, 4, false, 1>(a, g, per, grid, st);
         } else if (tile == kTilePair) {
-            launch_group_tile<ET, P, REG, 128, 128, 32, 64, 2, false, 1, 4>(a, g, per, grid, st);
+            launch_group_tile<ET, P, REG, GATHER, 128, 128, 32, 64, 2, false, 1, 4>(a, g, per, grid, st);
         } else if (tile == kTileSmall) {
-            launch_group_tile<ET, P, REG, 64, 128, 32, 64, 3, false, 2>(a, g, per, grid, st);
+            launch_group_tile<ET, P, REG, GATHER, 64, 128, 32, 64, 3, false, 2>(a, g, per, grid, st);
         } else {
-            launch_group_tile<ET, P, REG, 64, 64, 32, 64, 2, false, 4>(a, g, per, grid, st);
+            launch_group_tile<ET, P, REG, GATHER, 64, 64, 32, 64, 2, false, 4>(a, g, per, grid, st);
         }
     } else {
-        if (tile == kTileTall) launch_group_tile<ET, P, REG, 256, 128, 64, 64, 2, false, 1>(a, g, per, grid, st);
-        else if (tile == kTileMid) launch_group_tile<ET, P, REG, 128, 128, 32, 64, 2, false, 1>(a, g, per, grid, st);
-        else if (tile == kTileSmall) launch_group_tile<ET, P, REG, 64, 128, 32, 64, 2, false, 1>(a, g, per, grid, st);
-        else launch_group_tile<ET, P, REG, 64, 64, 32, 64, 2, false, 4>(a, g, per, grid, st);
+        if (tile == kTileTall) launch_group_tile<ET, P, REG, GATHER, 256, 128, 64, 64, 2, false, 1>(a, g, per, grid, st);
+        else if (tile == kTileMid) launch_group_tile<ET, P, REG, GATHER, 128, 128, 32, 64, 2, false, 1>(a, g, per, grid, st);
+        else if (tile == kTileSmall) launch_group_tile<ET, P, REG, GATHER, 64, 128, 32, 64, 2, false, 1>(a, g, per, grid, st);
+        else launch_group_tile<ET, P, REG, GATHER, 64, 64, 32, 64, 2, false, 4>(a, g, per, grid, st);
+    }
+}
+template <int ET, int P, bool REG, int BM, int BN, int WM, int WN, int S, int KG>
+void launch_both(const ProductArgs& x, const ProductArgs& w, const GroupArgs& g, int nx, int per, dim3 grid, hipStream_t st) {
+    constexpr bool SEG = P == kRowsSumNK || P == kRowsSumKN, BN_ = P == kRowsSumNK || P == kRowsKN;
+    hipLaunchKernelGGL((grouped_gradients<ET, BN_, SEG, REG, BM, BN, WM, WN, S, KG>), grid,
+                       dim3(ProductGeom<false, BM, BN, WM, WN, S, false, KG>::NT), 0, st, x, w, g, nx, per);
+}
+
+template <int ET, int P, bool REG>
+void launch_group_gradients(int tile, const ProductArgs& x, const ProductArgs& w, const GroupArgs& g, int nx, int per, dim3 grid,
+                            hipStream_t st) {
+    if constexpr (!REG) {
+        if (tile == kTileMid) launch_both<ET, P, REG, 128, 128, 32, 64, 4, 1>(x, w, g, nx, per, grid, st);
+        else launch_both<ET, P, REG, 64, 128, 32, 64, 3, 2>(x, w, g, nx, per, grid, st);
+    } else {
+        if (tile == kTileMid) launch_both<ET, P, REG, 128, 128, 32, 64, 2, 1>(x, w, g, nx, per, grid, st);
+        else launch_both<ET, P, REG, 64, 128, 32, 64, 2, 1>(x, w, g, nx, per, grid, st);
     }
 }
 #endif

@@ -339,9 +339,17 @@ struct ProductGeom {
 // A K-contiguous row's last k-tile masks the chunks past K by an offset outside every
 // resource and clears the part of one that straddles K, so nothing of the next row is
 // multiplied: a 0 * inf could not be undone.
+//   GATHER  row r of A is row from.index[r] of a matrix of from.rows rows (outside them: zeros)
+//   SKIP    waves whose rows all lie past the last one neither read fragments nor multiply, which
+//           leaves their SIMDs' matrix cores to the others: for row tiles that are often cut
+struct SourceRows {
+    const int32_t* index;
+    int32_t rows;
+};
 template <int ET, bool A_T, bool B_N, bool DUAL, bool SEG, bool REG, int BM, int BN, int WM, int WN,
-          int S, bool DEEP, int KG, bool TAIL>
-__device__ __forceinline__ void product_tile_of(ProductArgs args, int tm, int tn, int sp, SPG_LDS char* lds) {
+          int S, bool DEEP, int KG, bool TAIL, bool GATHER = false, bool SKIP = false>
+__device__ __forceinline__ void product_tile_of(ProductArgs args, int tm, int tn, int sp, SPG_LDS char* lds,
+                                                SourceRows from = SourceRows{}) {
     using G = ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP, KG>;
     constexpr int TM = G::TM, TN = G::TN, BNS = G::BNS, WNS = G::WNS, NW = G::NW;
     constexpr int A_OPS = G::A_OPS, B_OPS = G::B_OPS, L = G::L;
@@ -351,6 +359,7 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, int tm, int tn
     static_assert(!REG || (S == 2 && !DEEP), "register staging: two slots");
     static_assert(!SEG || (!A_T && !DUAL), "two segments: the input gradient");
     static_assert(!DUAL || !A_T, "gated: A is [M,K]");
+    static_assert(!GATHER || (!A_T && !SEG), "gathered rows lie along the reduction");
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave_id = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -405,10 +414,10 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, int tm, int tn
     // last row.  Reduction-major: 64 rows further, as many of them as exist; columns past the
     // last are masked by offset.
     const uint32_t lda = args.lda, ldb = args.ldb;
-    const uint64_t a_at = (uint64_t)(uintptr_t)a_ptr + (A_T ? 0 : (uint64_t)m0 * lda - RowsA::kBack);
+    const uint64_t a_at = (uint64_t)(uintptr_t)a_ptr + (A_T ? 0 : (GATHER ? 0 : (uint64_t)m0 * lda) - RowsA::kBack);
     const uint64_t b_at[2] = {(uint64_t)(uintptr_t)b_mine + (B_N ? 0 : (uint64_t)n0 * ldb - RowsB::kBack),
                               (uint64_t)(uintptr_t)(SEG ? b_ptr1 : b_mine) + (B_N ? 0 : (uint64_t)n0 * ldb - RowsB::kBack)};
-    const uint32_t a_all = (uint32_t)(a_rows - 1) * lda + (SEG ? lda : row_bytes) + RowsA::kBack;
+    const uint32_t a_all = (uint32_t)((GATHER ? (from.rows > 0 ? from.rows : 1) : a_rows) - 1) * lda + (SEG ? lda : row_bytes) + RowsA::kBack;
     const uint32_t b_all = (uint32_t)(b_rows - 1) * ldb + row_bytes + RowsB::kBack;
     auto a_win = [&](int kt) __attribute__((always_inline)) -> Win {
         if constexpr (A_T) return Columns::window(a_at, lda, K, kt, kt < kt1);
@@ -447,6 +456,16 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, int tm, int tn
         kcB[h] = (uint32_t)((firstB + h) * 8 + lane / 8) * args.ldb + (uint32_t)kc_pos(firstB + h) + RowsB::kBack;
     }
     const int posA = kc_pos(firstA), posB = kc_pos(firstB);
+    // gathered: every op's own row; kMasked - 15 and above lie past the resource, too
+    uint32_t gaA[GATHER ? A_OPS : 1];
+    if constexpr (GATHER) {
+#pragma unroll
+        for (int j = 0; j < A_OPS; ++j) {
+            const int r = m0 + (firstA + j) * 8 + lane / 8;
+            const int row = r < M ? from.index[r] : -1;
+            gaA[j] = row >= 0 && row < from.rows ? (uint32_t)row * args.lda + (uint32_t)kc_pos(firstA + j) + RowsA::kBack : kMasked;
+        }
+    }
     // reduction-major: op d holds 64 / CPR rows; over: columns of the chunk past the last
     uint32_t trA[A_T ? A_OPS : 1], trB[B_N ? B_OPS : 1];
     int overA[A_T ? A_OPS : 1], overB[B_N ? B_OPS : 1];
@@ -472,6 +491,7 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, int tm, int tn
         constexpr int j = decltype(jc)::value;
         if constexpr (j < A_OPS) {
             if constexpr (A_T) return trA[j];
+            else if constexpr (GATHER) return RowsA::offset(gaA[j], posA ^ ((j & 1) * 64), lim);
             else return RowsA::offset(kcA[j & 1] + (uint32_t)(j >> 1) * 16u * args.lda, posA ^ ((j & 1) * 64), lim);
         } else {
             constexpr int i = j - A_OPS;
@@ -604,6 +624,7 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, int tm, int tn
         for (int kk = 0; kk < 2; ++kk) boff[kk] = frag_k(wn * WNS, kk);
     }
     struct Frags { u32x4 a[TM]; u32x4 b[TN]; };
+    const bool idle = SKIP && m0 + wm * WM >= M;
     constexpr int RA = A_T ? 2 * TM : TM, RB = B_N ? 2 * TN : TN, NRD = RA + RB;
     auto tr_read = [&](SPG_LDS char* p, u32x4& f, auto hc) __attribute__((always_inline)) {
         constexpr int h = decltype(hc)::value;
@@ -711,6 +732,7 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, int tm, int tn
         };
         Frags f;
         auto matrix_phase = [&]() __attribute__((always_inline)) {
+            if (SKIP && idle) return;
             static_for<0, NMMA>([&](auto ic) {
                 constexpr int i = decltype(ic)::value, bn = i / TM, bm = i % TM;
                 acc[bn][bm] = mma<ET>(f.b[bn], f.a[bm], acc[bn][bm]);
@@ -721,7 +743,7 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, int tm, int tn
             constexpr int i = decltype(sc)::value;
             const Slot cur = slot_of(sc);
             const Slot prev = slot_of(std::integral_constant<int, i + 5>{});
-            static_for<0, NRD>([&](auto rc) { read_op(cur, 0, f, rc); });
+            if (!SKIP || !idle) static_for<0, NRD>([&](auto rc) { read_op(cur, 0, f, rc); });
             if (u >= 1) {
                 poison_slot(prev);
                 const Src src = src_ab(kt0 + u + 1, kt0 + u + 2);
@@ -731,7 +753,7 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, int tm, int tn
             phase_barrier();
             matrix_phase();
             phase_barrier();
-            static_for<0, NRD>([&](auto rc) { read_op(cur, 1, f, rc); });
+            if (!SKIP || !idle) static_for<0, NRD>([&](auto rc) { read_op(cur, 1, f, rc); });
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
             const Slot nxt = slot_of(std::integral_constant<int, i + 1>{});
             if (grp == 1) {
@@ -749,7 +771,7 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, int tm, int tn
         if (grp == 0) phase_barrier();
     } else {
         Frags fr[2];
-        static_for<0, NRD>([&](auto rc) { read_op(slot_of(C0{}), 0, fr[0], rc); });
+        if (!SKIP || !idle) static_for<0, NRD>([&](auto rc) { read_op(slot_of(C0{}), 0, fr[0], rc); });
         const Src none{};
         over_ktiles([&](auto sc, int t) __attribute__((always_inline)) {
             constexpr int s = decltype(sc)::value;
@@ -763,7 +785,7 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, int tm, int tn
                 lwrite(nxt, Next{}, kt_of(t + 1));
                 gload(Next{}, kt_of(t + 1 + PD));
             }
-            stage(fr[0], cur, 1, fr[1], cur, none, std::false_type{});
+            if (!SKIP || !idle) stage(fr[0], cur, 1, fr[1], cur, none, std::false_type{});
             if constexpr (!REG) {
                 wait_vmcnt<(S - 2) * L>();
                 clear_tail(nxt, kt_of(t + 1));
@@ -773,11 +795,12 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, int tm, int tn
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_setprio(1);
             if constexpr (REG) {
-                stage(fr[1], nxt, 0, fr[0], cur, none, std::false_type{});
+                if (!SKIP || !idle) stage(fr[1], nxt, 0, fr[0], cur, none, std::false_type{});
             } else {
                 poison_slot(cur);
                 const Src src = src_ab(kt_of(t + S), kt_of(t + S));
-                stage(fr[1], nxt, 0, fr[0], cur, src, std::true_type{});
+                if (!SKIP || !idle) stage(fr[1], nxt, 0, fr[0], cur, src, std::true_type{});
+                else static_for<0, L>([&](auto jc) { dma_op(cur, src, jc); });
             }
             __builtin_amdgcn_s_setprio(0);
         });
@@ -1201,10 +1224,9 @@ __global__ void __launch_bounds__(256) simple_product(SimpleArgs a) {
 // of a finite sum when it rounded it for storage (fp16 ends at 65504), and zero slopes and zero
 // dH times infinity would be NaN in a whole row of dX and a whole column of dWg or dWu.
 template <bool BF16>
-__global__ void __launch_bounds__(256) gated_slopes(const uint16_t* dH, const uint16_t* G, const uint16_t* U,
-                                                    uint16_t* D, int M, int N, int np, int act) {
+__device__ __forceinline__ void slopes_of(int64_t i, const uint16_t* dH, const uint16_t* G, const uint16_t* U,
+                                          uint16_t* D, int M, int N, int np, int act) {
     const int per = np / 8;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= (int64_t)M * per) return;
     const int64_t m = i / per;
     const int n = (int)(i - m * per) * 8;
@@ -1266,6 +1288,12 @@ __global__ void __launch_bounds__(256) gated_slopes(const uint16_t* dH, const ui
     uint16_t* d = D + (size_t)m * 2 * np + n;
     *(u32x4*)d = dg;
     *(u32x4*)(d + np) = du;
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(256) gated_slopes(const uint16_t* dH, const uint16_t* G, const uint16_t* U,
+                                                    uint16_t* D, int M, int N, int np, int act) {
+    slopes_of<BF16>((int64_t)blockIdx.x * 256 + threadIdx.x, dH, G, U, D, M, N, np, act);
 }
 
 // ---------------------------------------------------------------------------

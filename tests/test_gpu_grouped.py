@@ -231,7 +231,13 @@ def test_either_gradient_alone_and_nothing_to_do():
         plan.backward(dy, x, w, offsets, *both, workspace=ws)
         plan.backward(dy, None, w, offsets, alone[0], None, workspace=ws)
         plan.backward(dy, x, None, offsets, None, alone[1], workspace=ws)
-        assert torch.equal(both[0], alone[0]) and torch.equal(both[1], alone[1])
+        # one launch or two: the tiles may differ and with them the order of a sum, so each result
+        # is held to the formula (both orders are within its tolerance) and not to the other's bits
+        for dx, dw in (both, alone):
+            for e in range(E):
+                r = slice(o[e], o[e + 1])
+                _check_rows(dy[r], _as_kn(w[e], "nk").t().contiguous(), dx[r], "bf16", f"dX of group {e}")
+                _check_weight(x[r], dy[r], dw[e], "bf16", "nk", f"dW of group {e}")
     # no rows: the weights' gradients are zero; K = 0: products of nothing are zero
     none = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
     for Z in (spg.GroupedGemm(0, N, K, E), spg.GroupedGated(0, N, K, E)):
