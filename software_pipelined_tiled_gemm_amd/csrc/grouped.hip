@@ -208,6 +208,8 @@ void launch_any(int product, bool bf, bool reg, int tile, const ProductArgs& a, 
 
 constexpr int32_t kWhole = 1 << 28;   // k-tiles of a part: the reduction is not split
 
+constexpr uint8_t kGroupRows = 6;     // row tiles of a group rastered together
+
 // rows of tiles rastered together, as set_grid in product.hip
 uint8_t raster_rows(int64_t rows) { return (uint8_t)(rows <= 8 ? std::max<int64_t>(rows, 1) : 4); }
 
@@ -220,7 +222,7 @@ int64_t rows_grid(const Common& c, int tile, int mats, ProductArgs& a) {
     const int64_t tiles = (c.rows - c.live()) / BM + c.live();
     a.tiles_m = 0;   // found on the device
     a.tiles_n = (int32_t)ceil_div(a.N, spg::kTileN[tile] / mats);
-    a.group_m = raster_rows(tiles);
+    a.group_m = kGroupRows;
     return up(tiles * a.tiles_n, 8);
 }
 

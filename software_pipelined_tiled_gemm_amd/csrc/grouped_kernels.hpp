@@ -100,9 +100,13 @@ __device__ __forceinline__ void rows_tile(ProductArgs args, const GroupArgs& g, 
     const int rows = all_units<BM>(g, lane);
     const int at = xcd_place(wg, rows * args.tiles_n);
     if (at < 0) return;
+    // a group's tiles one after the other, so that its matrix is read once for all its rows: up to
+    // group_m row tiles go through the columns together, more in even parts
+    const int u = at / args.tiles_n;
+    const Found f = find_unit<BM>(g, u, lane);
+    const int mine = (f.g.n + BM - 1) / BM, parts = (mine + args.group_m - 1) / args.group_m;
     int tm, tn;
-    raster(at, rows, args.tiles_n, args.group_m, tm, tn);
-    const Found f = find_unit<BM>(g, tm, lane);
+    raster(at - (u - f.unit) * args.tiles_n, mine, args.tiles_n, (mine + parts - 1) / parts, tm, tn);
     const size_t out = (size_t)f.g.first * args.N * 2;
     if (!GATHER) args.A += (size_t)f.g.first * args.lda;
     args.B[0] += (size_t)f.e * g.b_step;
@@ -115,7 +119,7 @@ __device__ __forceinline__ void rows_tile(ProductArgs args, const GroupArgs& g, 
     args.M = f.g.n;
     args.part = nullptr;
     product_tile_of<ET, false, B_N, DUAL, SEG, REG, BM, BN, WM, WN, S, DEEP, KG, TAIL, GATHER, true>(
-        args, f.unit, tn, 0, lds, SourceRows{GATHER ? g.source + f.g.first : nullptr, g.tokens});
+        args, tm, tn, 0, lds, SourceRows{GATHER ? g.source + f.g.first : nullptr, g.tokens});
 }
 
 template <int ET, bool B_N, bool DUAL, bool SEG, bool REG, int BM, int BN, int WM, int WN, int S, bool DEEP, int KG, bool TAIL,
