@@ -144,30 +144,37 @@ __device__ __forceinline__ void dma16(const i32x4& rsrc, SPG_LDS char* lds_dst, 
 
 // The 8 16-bit elements of a 16-byte chunk as one little-endian 128-bit number (element
 // e in bits 16e .. 16e+15) shifted toward higher elements (shl) or lower ones (shr) by
-// `bits` (a multiple of 16, 0 .. 112, per lane); zeros come in.  Realigns the chunks the
+// `bits` (a multiple of 8, 0 .. 120, per lane); zeros come in.  Realigns the chunks the
 // misaligned-operand copy mode loads from a shifted window, and zeroes the elements of
 // the window that lie outside the operand's valid range in the same step.
-// Both are written as selects between values computed for either half, so that they
-// compile to v_cndmask rather than to branches around per-lane conditions.
+// Whole words are moved by selects (v_cndmask, no branches around per-lane conditions), the
+// bytes within a word by v_alignbyte.  Not with 64-bit shifts: v_lshlrev_b64 by a lane's own
+// amount, twice in a row, now and then left the first shift's result in the register (products
+// of 32-row groups by the streaming kernel, K % 8 = 6: 0.5% of the outputs wrong, others from
+// run to run; none with a wait between the two, none in this form).
 __device__ __forceinline__ u32x4 shl128(u32x4 v, uint32_t bits) {
-    const uint64_t lo = ((uint64_t)v.y << 32) | v.x, hi = ((uint64_t)v.w << 32) | v.z;
-    const uint32_t b = bits & 63u;              // shift within a 64-bit half
-    // lo >> (64 - b) for b in 1 .. 63, written so that every shift count is < 64
-    const uint64_t carry = b == 0 ? 0 : (lo >> 1) >> (63u - b);
-    const bool big = bits >= 64;
-    const uint64_t nhi = big ? lo << b : (hi << b) | carry;
-    const uint64_t nlo = big ? 0 : lo << b;
-    return u32x4{(uint32_t)nlo, (uint32_t)(nlo >> 32), (uint32_t)nhi, (uint32_t)(nhi >> 32)};
+    // as 256 bits, zeros below v, shifted down by 128 - bits (8 .. 128)
+    const uint32_t down = 128u - bits, bytes = down >> 3;   // alignbyte reads the low two bits
+    const bool one = down & 32u, two = down & 64u, four = down & 128u;
+    const uint32_t w[12] = {0u, 0u, 0u, 0u, v.x, v.y, v.z, v.w, 0u, 0u, 0u, 0u};
+    uint32_t a[11], b[9], c[5];
+#pragma unroll
+    for (int e = 0; e < 11; ++e) a[e] = one ? w[e + 1] : w[e];
+#pragma unroll
+    for (int e = 0; e < 9; ++e) b[e] = two ? a[e + 2] : a[e];
+#pragma unroll
+    for (int e = 0; e < 5; ++e) c[e] = four ? b[e + 4] : b[e];
+    return u32x4{__builtin_amdgcn_alignbyte(c[1], c[0], bytes), __builtin_amdgcn_alignbyte(c[2], c[1], bytes),
+                 __builtin_amdgcn_alignbyte(c[3], c[2], bytes), __builtin_amdgcn_alignbyte(c[4], c[3], bytes)};
 }
 
 __device__ __forceinline__ u32x4 shr128(u32x4 v, uint32_t bits) {
-    const uint64_t lo = ((uint64_t)v.y << 32) | v.x, hi = ((uint64_t)v.w << 32) | v.z;
-    const uint32_t b = bits & 63u;
-    const uint64_t carry = b == 0 ? 0 : (hi << 1) << (63u - b);
-    const bool big = bits >= 64;
-    const uint64_t nlo = big ? hi >> b : (lo >> b) | carry;
-    const uint64_t nhi = big ? 0 : hi >> b;
-    return u32x4{(uint32_t)nlo, (uint32_t)(nlo >> 32), (uint32_t)nhi, (uint32_t)(nhi >> 32)};
+    const uint32_t bytes = bits >> 3;
+    const bool one = bits & 32u, two = bits & 64u;
+    const uint32_t a0 = one ? v.y : v.x, a1 = one ? v.z : v.y, a2 = one ? v.w : v.z, a3 = one ? 0u : v.w;
+    const uint32_t b0 = two ? a2 : a0, b1 = two ? a3 : a1, b2 = two ? 0u : a2, b3 = two ? 0u : a3;
+    return u32x4{__builtin_amdgcn_alignbyte(b1, b0, bytes), __builtin_amdgcn_alignbyte(b2, b1, bytes),
+                 __builtin_amdgcn_alignbyte(b3, b2, bytes), __builtin_amdgcn_alignbyte(0u, b3, bytes)};
 }
 
 // Wait until at most N vector-memory instructions of this wave are outstanding.

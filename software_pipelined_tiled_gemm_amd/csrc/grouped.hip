@@ -103,7 +103,7 @@ struct Choice {
 };
 
 double rows_wgs(const RowsShape& s, int t) {
-    return row_tiles(s, spg::kTileM[t]) * (double)ceil_div(s.N, spg::kTileN[t] / s.mats);
+    return row_tiles(s, spg::kGroupTileM[t]) * (double)ceil_div(s.N, spg::group_tile_n(t, s.mats));
 }
 
 Choice choose_rows(const RowsShape& s, bool reg) {
@@ -217,11 +217,11 @@ uint8_t raster_rows(int64_t rows) { return (uint8_t)(rows <= 8 ? std::max<int64_
 int64_t rows_grid(const Common& c, int tile, int mats, ProductArgs& a) {
     a.zm = a.zn = a.split = 1;
     a.kt_part = kWhole;
-    const int BM = spg::kTileM[tile];
+    const int BM = spg::kGroupTileM[tile];
     // every group with rows has at most one tile that is not full
     const int64_t tiles = (c.rows - c.live()) / BM + c.live();
     a.tiles_m = 0;   // found on the device
-    a.tiles_n = (int32_t)ceil_div(a.N, spg::kTileN[tile] / mats);
+    a.tiles_n = (int32_t)ceil_div(a.N, spg::group_tile_n(tile, mats));
     a.group_m = kGroupRows;
     return up(tiles * a.tiles_n, 8);
 }

@@ -148,9 +148,16 @@ __device__ __forceinline__ void weights_tile(ProductArgs args, const GroupArgs& 
     if (gr.n == 0) {
         const bool second = tm >= args.tiles_m || tn >= args.tiles_n;
         const int m0 = (tm >= args.tiles_m ? tm - args.tiles_m : tm) * BM, n0 = (tn >= args.tiles_n ? tn - args.tiles_n : tn) * BN;
-        uint16_t* c = (uint16_t*)(second ? args.C1 : args.C);
+        // 16 bytes a thread at any alignment, a row's last elements one by one
+        uint16_t* c = (uint16_t*)(second ? args.C1 : args.C) + (size_t)m0 * args.N + n0;
         const int w = args.N - n0 < BN ? args.N - n0 : BN, h = args.M - m0 < BM ? args.M - m0 : BM;
-        for (int i = threadIdx.x; i < h * w; i += G::NT) c[(size_t)(m0 + i / w) * args.N + n0 + i % w] = 0;
+        for (int i = threadIdx.x; i < h * (BN / 8); i += G::NT) {
+            const int col = i % (BN / 8) * 8;
+            uint16_t* d = c + (size_t)(i / (BN / 8)) * args.N + col;
+            if (col + 8 <= w) ((Bytes16*)d)->v = u32x4{};
+            else
+                for (int e = col; e < w; ++e) *d++ = 0;
+        }
         return;
     }
     args.A += (size_t)gr.first * args.lda;

@@ -19,7 +19,14 @@ enum {
     kGroupProducts = 7
 };
 
-// Tile classes are those of product_launch.hpp.  `per`: workgroups of a group (kGroupWeights);
+// Tile classes: those of product_launch.hpp, and Thin for groups of few rows, whose time is the
+// reading of their matrices: 32 rows (one row of waves), so that nearly all of the ring's LDS
+// holds parts of the matrices, and two workgroups a CU.
+enum { kTileThin = kTiles, kGroupTiles = kTiles + 1 };
+constexpr int kGroupTileM[kGroupTiles] = {256, 256, 128, 64, 64, 128, 32};
+constexpr int group_tile_n(int tile, int mats) { return kTileN[tile == kTileThin ? (int)kTileMid : tile] / mats; }   // of one result
+
+// `per`: workgroups of a group (kGroupWeights);
 // GATHER: rows of X by their source (kRowsGated*, kRowsNK and kRowsKN only)
 template <int ET, int P, bool REG, bool GATHER>
 void launch_grouped(int tile, const ProductArgs& a, const GroupArgs& g, int per, dim3 grid, hipStream_t st);
@@ -69,6 +76,9 @@ void launch_grouped(int tile, const ProductArgs& a, const GroupArgs& g, int per,
             launch_group_tile<ET, P, REG, GATHER, 128, 128, 32, 64, 4, false, 1>(a, g, per, grid, st);
         } else if (tile == kTilePair) {
             launch_group_tile<ET, P, REG, GATHER, 128, 128, 32, 64, 2, false, 1, 4>(a, g, per, grid, st);
+        } else if (tile == kTileThin) {
+            if constexpr (DUAL) launch_group_tile<ET, P, REG, GATHER, 32, 128, 32, 64, 4, false, 1>(a, g, per, grid, st);
+            else if constexpr (P != kGroupWeights) launch_group_tile<ET, P, REG, GATHER, 32, 128, 32, 32, 4, false, 1, 2>(a, g, per, grid, st);
         } else if (tile == kTileSmall) {
             launch_group_tile<ET, P, REG, GATHER, 64, 128, 32, 64, 3, false, 2>(a, g, per, grid, st);
         } else {
@@ -77,6 +87,10 @@ void launch_grouped(int tile, const ProductArgs& a, const GroupArgs& g, int per,
     } else {
         if (tile == kTileTall) launch_group_tile<ET, P, REG, GATHER, 256, 128, 64, 64, 2, false, 1>(a, g, per, grid, st);
         else if (tile == kTileMid) launch_group_tile<ET, P, REG, GATHER, 128, 128, 32, 64, 2, false, 1>(a, g, per, grid, st);
+        else if (tile == kTileThin) {
+            if constexpr (DUAL) launch_group_tile<ET, P, REG, GATHER, 32, 128, 32, 64, 2, false, 1>(a, g, per, grid, st);
+            else if constexpr (P != kGroupWeights) launch_group_tile<ET, P, REG, GATHER, 32, 128, 32, 32, 2, false, 1, 2>(a, g, per, grid, st);
+        }
         else if (tile == kTileSmall) launch_group_tile<ET, P, REG, GATHER, 64, 128, 32, 64, 2, false, 1>(a, g, per, grid, st);
         else launch_group_tile<ET, P, REG, GATHER, 64, 64, 32, 64, 2, false, 4>(a, g, per, grid, st);
     }

@@ -41,19 +41,27 @@ __device__ __forceinline__ uint32_t order_of(float x) {
 }
 constexpr uint32_t kNothing = 0x007fffffu;   // order_of(-inf): it and NaN are never chosen
 
+// The largest key of a wave, as a scalar; by shifts within rows of lanes and the rows' ends, a
+// dependent instruction each instead of a trip through LDS (16384 tokens, 8 of 64 experts: the
+// choices take %CHOOSE%).
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-    for (int s = 32; s > 0; s >>= 1) {
-        const uint32_t o = (uint32_t)__shfl_xor((int)v, s);
+    auto most = [&](auto ctrl, auto rows) {
+        const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, decltype(ctrl)::value, decltype(rows)::value, 0xf, false);
         v = o > v ? o : v;
-    }
-    return v;
+    };
+    using std::integral_constant;
+    constexpr integral_constant<int, 0xf> all{};
+    most(integral_constant<int, 0x111>{}, all);   // row_shr:1
+    most(integral_constant<int, 0x112>{}, all);
+    most(integral_constant<int, 0x114>{}, all);
+    most(integral_constant<int, 0x118>{}, all);
+    most(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});   // row_bcast:15
+    most(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});   // row_bcast:31
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-__device__ __forceinline__ float wave_fmax(float v) {
-#pragma unroll
-    for (int s = 32; s > 0; s >>= 1) v = __builtin_fmaxf(v, __shfl_xor(v, s));
-    return v;
+__device__ __forceinline__ float value_of(uint32_t key) {
+    return __builtin_bit_cast(float, key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
 
 // One wave, one token: C * 64 logits in registers, the k largest one by one.  Lane j ends with
@@ -90,7 +98,7 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int64_t t, int lane, 
                 if (lane == l) key[c] = 0u;
             }
         }
-        const float v = __builtin_bit_cast(float, best & 0x80000000u ? best & 0x7fffffffu : ~best);
+        const float v = value_of(best);
         if (j == 0) top = v;
         if (lane == j) {
             expert = e;
@@ -249,7 +257,7 @@ __global__ void __launch_bounds__(256) route_back(RouteBack a) {
     const float d = e >= 0 ? a.dgate[t * a.k + lane] : 0.0f;
     float x[C], g[C];
     bool mine[C], nan = false;
-    float top = -__builtin_inff();
+    uint32_t top_key = 0;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int i = c * 64 + lane;
@@ -257,11 +265,12 @@ __global__ void __launch_bounds__(256) route_back(RouteBack a) {
         g[c] = 0.0f;
         mine[c] = false;
         nan |= x[c] != x[c];
-        top = __builtin_fmaxf(top, x[c]);
+        const uint32_t key = order_of(x[c]);
+        top_key = key > top_key ? key : top_key;
     }
     for (int j = 0; j < a.k; ++j) {
-        const int ej = __shfl(e, j);
-        const float dj = __shfl(d, j);
+        const int ej = __builtin_amdgcn_readlane(e, j);
+        const float dj = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, d), j));
 #pragma unroll
         for (int c = 0; c < C; ++c)
             if (ej == c * 64 + lane) {
@@ -269,7 +278,7 @@ __global__ void __launch_bounds__(256) route_back(RouteBack a) {
                 mine[c] = true;
             }
     }
-    top = wave_fmax(top);
+    const float top = value_of(wave_max(top_key));
     const bool some = __ballot(e >= 0) != 0;
     float all = 0.0f, inner = 0.0f;
 #pragma unroll
@@ -310,13 +319,25 @@ __global__ void __launch_bounds__(256) combine_rows(CombineArgs a) {
     const int64_t t = i / per, n = (i - t * per) * E;
     if (t >= a.tokens) return;
     float s[E] = {};
-    for (int j = 0; j < a.k; ++j) {
-        const int64_t r = a.slot[t * a.k + j];
-        if (r < 0 || r >= a.rows) continue;
-        const float g = a.gate ? a.gate[t * a.k + j] : 1.0f;
-        const u32x4 v = load_short<DT>(a.Y + r * a.N * EB, n, a.N);
+    // four rows' loads in flight; what a slot out of range would add is left out, not multiplied
+    for (int j0 = 0; j0 < a.k; j0 += 4) {
+        int64_t r[4];
+        float g[4];
+        u32x4 v[4];
 #pragma unroll
-        for (int e = 0; e < E; ++e) s[e] = __builtin_fmaf(g, elem<DT>(v, e), s[e]);
+        for (int i = 0; i < 4; ++i) {
+            r[i] = j0 + i < a.k ? a.slot[t * a.k + j0 + i] : -1;
+            g[i] = a.gate && j0 + i < a.k ? a.gate[t * a.k + j0 + i] : 1.0f;
+            if (r[i] >= a.rows) r[i] = -1;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (r[i] >= 0) v[i] = load_short<DT>(a.Y + r[i] * a.N * EB, n, a.N);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (r[i] >= 0)
+#pragma unroll
+                for (int e = 0; e < E; ++e) s[e] = __builtin_fmaf(g[i], elem<DT>(v[i], e), s[e]);
     }
     store_vec<DT>(a.out + t * a.N * EB, n, a.N, s);
 }

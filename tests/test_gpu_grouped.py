@@ -340,3 +340,23 @@ def test_results_repeat(layout):
             seen.append((h, g, u, dx, dwg, dwu))
     for other in seen[1:]:
         assert all(torch.equal(p, q) for p, q in zip(seen[0], other))
+
+
+@pytest.mark.parametrize("K", [46, 54, 62, 214, 44, 50])
+def test_rows_that_end_inside_a_chunk_many_times(K):
+    # groups of more rows than one MFMA tile, a reduction that ends inside a 16-byte chunk, and
+    # enough workgroups to fill the device: realigned chunks came out wrong in some of them
+    torch = _t()
+    counts = [32, 0] * 30
+    o = [sum(counts[:i]) for i in range(len(counts) + 1)]
+    offsets = torch.tensor(o, dtype=torch.int32, device="cuda")
+    rows, N, E = o[-1], 1912, len(counts)
+    x = _normal(_gen(1), (rows, K), 1.0).bfloat16()
+    w = _weights(E, N, K, "bf16", "nk", 2, 0).t
+    with spg.GroupedGemm(rows, N, K, E, "bf16", "nk") as plan:
+        ws = _workspace(plan.workspace_bytes())
+        for _ in range(6):
+            y = torch.zeros(rows, N, device="cuda", dtype=torch.bfloat16)
+            plan(x, w, offsets, y, workspace=ws)
+            for e in range(0, E, 2):
+                _check_rows(x[o[e]:o[e + 1]], _as_kn(w[e], "nk"), y[o[e]:o[e + 1]], "bf16", f"group {e}")
