@@ -88,14 +88,41 @@ double row_tiles(const RowsShape& s, int BM) {
     return std::max((double)s.live, (double)s.rows / BM + 0.5 * (double)s.live);
 }
 
-// Microseconds of a grid of `wgs` workgroups of tile class t, `kt` k-tiles each
-double grid_us(int t, bool reg, bool crooked, double wgs, double kt, double bytes) {
-    const double rounds = std::max(1.0, wgs / spg::slots(t, reg) + 0.3);
-    const double us = rounds * (spg::tile_us(t, reg, crooked, (int64_t)wgs) * kt + spg::start_us(t, reg, (int64_t)wgs));
-    return spg::kLaunchUs + std::max(us, 3.0 + bytes / 5.0e6);
-}
+// What a tile class costs, in microseconds: a call takes
+//     base + max(k-tiles * alone, rounds * (k-tiles * busy + tile), bytes / bw)
+// with rounds the workgroups over the slots of the CUs: `alone` bounds a grid that leaves CUs
+// idle (a k-tile's copies have to come in), `busy` and `tile` (a workgroup's start and store) one
+// that fills them, and the matrices' reading (writing, for their gradients) at bw bytes a
+// microsecond the rest.  Fitted to every class at 2500 drawn shapes (1 to 256 groups, 1 to 8192
+// rows, matrices of 48 to 12288 x 40 to 4096); of the classes' measured times the choice takes
+// 2.0% more than the best on average, 14% more at 5% of the shapes.
+struct Cost {
+    double alone, busy, tile, base, bw;   // bw 0: the class is not chosen
+};
+// 256x128 is nowhere more than 2% ahead of the others for rows, nor 128x128 for the gradients
+constexpr Cost kNone{0, 0, 0, 0, 0};
+constexpr Cost kRows[2][2][spg::kGroupTiles] = {   // [register-staged][two matrices]
+    {{{0.93, 0.84, 2.5, 6.8, 5.8e6}, kNone, {0.36, 0.41, 2.0, 5.1, 7.4e6}, {0.27, 0.38, 2.4, 5.4, 8.3e6},
+      {0.18, 0.26, 2.6, 5.5, 6.0e6}, {0.43, 0.88, 1.8, 4.8, 7.2e6}, {0.24, 0.57, 1.9, 4.3, 10.0e6}},
+     {{0.86, 1.10, 2.8, 7.5, 5.9e6}, kNone, {0.37, 0.50, 2.1, 5.2, 7.1e6}, {0.29, 0.43, 2.6, 5.3, 7.3e6},
+      {0.19, 0.29, 3.1, 5.6, 5.4e6}, {0.48, 1.05, 1.9, 4.8, 6.9e6}, {0.34, 1.31, 4.6, 4.5, 8.0e6}}},
+    {{kNone, kNone, {0.64, 0.51, 2.1, 5.6, 6.6e6}, {0.61, 1.33, 1.5, 5.3, 8.3e6}, {0.32, 0.29, 3.2, 6.3, 6.0e6}, kNone,
+      {0.53, 0.77, 1.3, 4.9, 8.8e6}},
+     {kNone, kNone, {0.64, 0.56, 2.5, 5.6, 6.2e6}, {0.62, 1.46, 1.8, 5.1, 7.7e6}, {0.37, 0.31, 3.6, 6.4, 5.5e6}, kNone,
+      {0.77, 1.84, 2.9, 4.9, 8.3e6}}}};
+constexpr Cost kWeights[2][spg::kGroupTiles] = {
+    {{0.91, 1.91, 4.4, 7.8, 6.3e6}, {0.49, 1.14, 2.8, 6.1, 5.0e6}, kNone, {0.19, 0.45, 2.4, 5.4, 5.0e6},
+     {0.14, 0.37, 2.6, 5.5, 5.0e6}, {0.31, 1.22, 2.6, 4.9, 5.4e6}, kNone},
+    {kNone, {0.88, 1.51, 3.4, 7.4, 3.4e6}, kNone, {0.62, 1.58, 3.4, 5.3, 5.0e6}, {0.34, 0.47, 3.2, 6.5, 5.0e6}, kNone, kNone}};
+// ... of the tiles that both gradients may share a launch with
+constexpr Cost kWeightsMid[2] = {{0.32, 0.67, 2.1, 5.1, 5.0e6}, {0.62, 0.92, 2.4, 6.0, 5.0e6}};
 
-bool staged(int t) { return t != spg::kTileBig && t != spg::kTilePair; }   // tiles that stage through registers
+// Workgroups that the CUs hold at once
+double slots(int t, bool reg) { return t == spg::kTileThin ? 512.0 : reg && t == spg::kTileSmall ? 768.0 : spg::slots(t, reg); }
+
+double cost_us(const Cost& c, double rounds, double kt, double bytes) {
+    return c.base + std::max(std::max(kt * c.alone, rounds * (kt * c.busy + c.tile)), bytes / c.bw);
+}
 
 struct Choice {
     int tile;
@@ -108,9 +135,10 @@ double rows_wgs(const RowsShape& s, int t) {
 
 Choice choose_rows(const RowsShape& s, bool reg) {
     Choice best{spg::kTileNarrow, 1e30};
-    for (int t = 0; t < spg::kTiles; ++t) {
-        if (reg && !staged(t)) continue;
-        const double us = grid_us(t, reg, s.crooked, rows_wgs(s, t), (double)s.kt, s.bytes);
+    for (int t = 0; t < spg::kGroupTiles; ++t) {
+        const Cost& c = kRows[reg][s.mats == 2][t];
+        if (c.bw == 0) continue;
+        const double us = cost_us(c, rows_wgs(s, t) / slots(t, reg), (double)s.kt, s.bytes);
         if (us < best.us) best = Choice{t, us};
     }
     return best;
@@ -134,8 +162,9 @@ double weights_wgs(const WeightsShape& s, int t) {
 Choice choose_weights(const WeightsShape& s, bool reg) {
     Choice best{spg::kTileNarrow, 1e30};
     for (int t = 0; t < spg::kTiles; ++t) {
-        if (reg && !staged(t)) continue;
-        const double us = grid_us(t, reg, s.crooked, weights_wgs(s, t), s.kt, s.bytes);
+        const Cost& c = kWeights[reg][t];
+        if (c.bw == 0) continue;
+        const double us = cost_us(c, weights_wgs(s, t) / slots(t, reg), s.kt, s.bytes);
         if (us < best.us) best = Choice{t, us};
     }
     return best;
@@ -146,11 +175,12 @@ Choice choose_weights(const WeightsShape& s, bool reg) {
 int choose_both(const RowsShape& x, const WeightsShape& w, bool reg, double apart) {
     int best = -1;
     for (int t : {(int)spg::kTileMid, (int)spg::kTileSmall}) {
-        const double nx = rows_wgs(x, t), nw = weights_wgs(w, t), all = nx + nw;
-        const double k = spg::tile_us(t, reg, x.crooked || w.crooked, (int64_t)all), s0 = spg::start_us(t, reg, (int64_t)all);
-        const double cx = k * (double)x.kt + s0, cw = k * w.kt + s0, slots = spg::slots(t, reg);
-        double us = std::max(std::max(cx, cw), all > slots ? (nx * cx + nw * cw) / slots + 0.5 * std::max(cx, cw) : 0.0);
-        us = spg::kLaunchUs + std::max(us, 3.0 + (x.bytes + w.bytes) / 5.0e6);
+        const Cost& cx = kRows[reg][0][t];
+        const Cost& cw = t == spg::kTileMid ? kWeightsMid[reg] : kWeights[reg][t];
+        const double nx = rows_wgs(x, t) / slots(t, reg), nw = weights_wgs(w, t) / slots(t, reg);
+        const double full = nx * ((double)x.kt * cx.busy + cx.tile) + nw * (w.kt * cw.busy + cw.tile);
+        const double us = cx.base + std::max(std::max(std::max((double)x.kt * cx.alone, w.kt * cw.alone), full),
+                                             x.bytes / cx.bw + w.bytes / cw.bw);
         if (us < apart) {
             apart = us;
             best = t;
@@ -349,9 +379,12 @@ gemm_status simple_weights(const Common& c, const void* D, int64_t ldd, const vo
     return launched();
 }
 
-// The streaming kernel: matrices along the reduction, few rows a group.
-bool streams(const Common& c, bool along) {
-    return along && c.rows <= 16 * c.live() && c.rows <= 1024;
+// The streaming kernel: matrices along the reduction, few rows a group and few workgroups in
+// all.  Against the best tile at 800 drawn shapes it takes 0.5 to 0.8 of the time up to 256
+// workgroups (16 columns of one group each), the same at 1024 and up to three times as long
+// beyond; a group of more than 16 rows reads its matrix again for every 16 of them.
+bool streams(const Common& c, int64_t N, bool along) {
+    return along && c.rows <= 16 * c.live() && ceil_div(N, 16) * std::max(c.live(), c.rows / 2) <= 1024;
 }
 
 // Operands' first row and last byte within 32-bit offsets of the stream
@@ -388,8 +421,8 @@ gemm_status gemm_grouped_create(gemm_grouped_handle* out, int64_t rows, int64_t 
     // the tiled kernels need 16 bytes of every row they copy, and 32-bit offsets
     p->simple = K < 8 || (!c.nk && N < 8) || K * 2 > kMaxRowBytes || N * 2 > kMaxRowBytes;
     p->simple_back = p->simple || N < 8;
-    p->stream = !p->simple && streams(c, c.nk) && fits(std::max(rows, tokens), K * 2);
-    p->stream_back = !p->simple_back && streams(c, !c.nk) && fits(rows, N * 2);
+    p->stream = !p->simple && streams(c, N, c.nk) && fits(std::max(rows, tokens), K * 2);
+    p->stream_back = !p->simple_back && streams(c, K, !c.nk) && fits(rows, N * 2);
     const double live = (double)c.live(), io = 2.0 * rows * (N + K) + live * c.matrix();
     const bool crooked = N % 64 != 0 || K % 64 != 0;
     const RowsShape fwd{rows, c.live(), N, ceil_div(K, 64), 1, io, crooked}, dx{rows, c.live(), K, ceil_div(N, 64), 1, io, crooked};
@@ -511,7 +544,7 @@ gemm_status gemm_experts_create(gemm_experts_handle* out, int64_t rows, int64_t 
     p->np = up(N, 64);
     p->simple = K < 8 || (!c.nk && N < 8) || K * 2 > kMaxRowBytes || N * 2 > kMaxRowBytes;
     p->simple_back = p->simple || p->np * 4 > kMaxRowBytes;
-    p->stream = !p->simple && streams(c, c.nk) && fits(std::max(rows, tokens), K * 2);
+    p->stream = !p->simple && streams(c, N, c.nk) && fits(std::max(rows, tokens), K * 2);
     const double live = (double)c.live(), io = 2.0 * rows * (N + K) + 2.0 * live * c.matrix();
     const bool crooked = N % 64 != 0 || K % 64 != 0;
     const RowsShape fwd{rows, c.live(), N, ceil_div(K, 64), 2, io, crooked}, dx{rows, c.live(), K, 2 * ceil_div(N, 64), 1, io, crooked};

@@ -70,10 +70,10 @@ void launch_grouped(int tile, const ProductArgs& a, const GroupArgs& g, int per,
         if (tile == kTileBig) {
             if constexpr (DUAL) launch_group_tile<ET, P, REG, GATHER, 256, 256, 64, 128, 2, DEEP, 1>(a, g, per, grid, st);
             else launch_group_tile<ET, P, REG, GATHER, 256, 256, 128, 64, 2, DEEP, 1>(a, g, per, grid, st);
-        } else if (tile == kTileTall) {
-            launch_group_tile<ET, P, REG, GATHER, 256, 128, 64, 64, 3, false, 1>(a, g, per, grid, st);
-        } else if (tile == kTileMid) {
-            launch_group_tile<ET, P, REG, GATHER, 128, 128, 32, 64, 4, false, 1>(a, g, per, grid, st);
+        } else if (tile == kTileTall) {   // the matrices' gradients only
+            if constexpr (P == kGroupWeights) launch_group_tile<ET, P, REG, GATHER, 256, 128, 64, 64, 3, false, 1>(a, g, per, grid, st);
+        } else if (tile == kTileMid) {    // rows only
+            if constexpr (P != kGroupWeights) launch_group_tile<ET, P, REG, GATHER, 128, 128, 32, 64, 4, false, 1>(a, g, per, grid, st);
         } else if (tile == kTilePair) {
             launch_group_tile<ET, P, REG, GATHER, 128, 128, 32, 64, 2, false, 1, 4>(a, g, per, grid, st);
         } else if (tile == kTileThin) {
@@ -85,13 +85,14 @@ void launch_grouped(int tile, const ProductArgs& a, const GroupArgs& g, int per,
             launch_group_tile<ET, P, REG, GATHER, 64, 64, 32, 64, 2, false, 4>(a, g, per, grid, st);
         }
     } else {
-        if (tile == kTileTall) launch_group_tile<ET, P, REG, GATHER, 256, 128, 64, 64, 2, false, 1>(a, g, per, grid, st);
-        else if (tile == kTileMid) launch_group_tile<ET, P, REG, GATHER, 128, 128, 32, 64, 2, false, 1>(a, g, per, grid, st);
-        else if (tile == kTileThin) {
+        if (tile == kTileTall) {
+            if constexpr (P == kGroupWeights) launch_group_tile<ET, P, REG, GATHER, 256, 128, 64, 64, 2, false, 1>(a, g, per, grid, st);
+        } else if (tile == kTileMid) {
+            if constexpr (P != kGroupWeights) launch_group_tile<ET, P, REG, GATHER, 128, 128, 32, 64, 2, false, 1>(a, g, per, grid, st);
+        } else if (tile == kTileThin) {
             if constexpr (DUAL) launch_group_tile<ET, P, REG, GATHER, 32, 128, 32, 64, 2, false, 1>(a, g, per, grid, st);
             else if constexpr (P != kGroupWeights) launch_group_tile<ET, P, REG, GATHER, 32, 128, 32, 32, 2, false, 1, 2>(a, g, per, grid, st);
-        }
-        else if (tile == kTileSmall) launch_group_tile<ET, P, REG, GATHER, 64, 128, 32, 64, 2, false, 1>(a, g, per, grid, st);
+        } else if (tile == kTileSmall) launch_group_tile<ET, P, REG, GATHER, 64, 128, 32, 64, 2, false, 1>(a, g, per, grid, st);
         else launch_group_tile<ET, P, REG, GATHER, 64, 64, 32, 64, 2, false, 4>(a, g, per, grid, st);
     }
 }
