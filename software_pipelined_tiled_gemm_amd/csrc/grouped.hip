@@ -382,9 +382,12 @@ gemm_status simple_weights(const Common& c, const void* D, int64_t ldd, const vo
 // The streaming kernel: matrices along the reduction, few rows a group and few workgroups in
 // all.  Against the best tile at 800 drawn shapes it takes 0.5 to 0.8 of the time up to 256
 // workgroups (16 columns of one group each), the same at 1024 and up to three times as long
-// beyond; a group of more than 16 rows reads its matrix again for every 16 of them.
-bool streams(const Common& c, int64_t N, bool along) {
-    return along && c.rows <= 16 * c.live() && ceil_div(N, 16) * std::max(c.live(), c.rows / 2) <= 1024;
+// beyond; a group of more than 16 rows reads its matrix again for every 16 of them.  Two long
+// matrices keep its workgroups busy enough to go on up to 4096 (single rows, 12288 x 4096: 70 us
+// against 81; of 2000 to 3500 reductions the same time).
+bool streams(const Common& c, int64_t N, int64_t K, int mats, bool along) {
+    return along && c.rows <= 16 * c.live() &&
+           ceil_div(N, 16) * std::max(c.live(), c.rows / 2) <= (mats == 2 && K >= 2048 ? 4096 : 1024);
 }
 
 // Operands' first row and last byte within 32-bit offsets of the stream
@@ -421,8 +424,8 @@ gemm_status gemm_grouped_create(gemm_grouped_handle* out, int64_t rows, int64_t 
     // the tiled kernels need 16 bytes of every row they copy, and 32-bit offsets
     p->simple = K < 8 || (!c.nk && N < 8) || K * 2 > kMaxRowBytes || N * 2 > kMaxRowBytes;
     p->simple_back = p->simple || N < 8;
-    p->stream = !p->simple && streams(c, N, c.nk) && fits(std::max(rows, tokens), K * 2);
-    p->stream_back = !p->simple_back && streams(c, K, !c.nk) && fits(rows, N * 2);
+    p->stream = !p->simple && streams(c, N, K, 1, c.nk) && fits(std::max(rows, tokens), K * 2);
+    p->stream_back = !p->simple_back && streams(c, K, N, 1, !c.nk) && fits(rows, N * 2);
     const double live = (double)c.live(), io = 2.0 * rows * (N + K) + live * c.matrix();
     const bool crooked = N % 64 != 0 || K % 64 != 0;
     const RowsShape fwd{rows, c.live(), N, ceil_div(K, 64), 1, io, crooked}, dx{rows, c.live(), K, ceil_div(N, 64), 1, io, crooked};
@@ -544,7 +547,7 @@ gemm_status gemm_experts_create(gemm_experts_handle* out, int64_t rows, int64_t 
     p->np = up(N, 64);
     p->simple = K < 8 || (!c.nk && N < 8) || K * 2 > kMaxRowBytes || N * 2 > kMaxRowBytes;
     p->simple_back = p->simple || p->np * 4 > kMaxRowBytes;
-    p->stream = !p->simple && streams(c, N, c.nk) && fits(std::max(rows, tokens), K * 2);
+    p->stream = !p->simple && streams(c, N, K, 2, c.nk) && fits(std::max(rows, tokens), K * 2);
     const double live = (double)c.live(), io = 2.0 * rows * (N + K) + 2.0 * live * c.matrix();
     const bool crooked = N % 64 != 0 || K % 64 != 0;
     const RowsShape fwd{rows, c.live(), N, ceil_div(K, 64), 2, io, crooked}, dx{rows, c.live(), K, 2 * ceil_div(N, 64), 1, io, crooked};
