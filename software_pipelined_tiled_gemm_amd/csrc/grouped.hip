@@ -70,7 +70,7 @@ bool small_workspace(const void* workspace, int64_t bytes, int64_t need) {
 }
 
 GroupArgs group_args(const Common& c, const int32_t* offsets, const int32_t* source) {
-    return GroupArgs{offsets, source, c.matrix(), (int32_t)c.groups, (int32_t)c.rows, (int32_t)std::max<int64_t>(c.tokens, 0)};
+    return GroupArgs{offsets, source, nullptr, c.matrix(), (int32_t)c.groups, (int32_t)c.rows, (int32_t)std::max<int64_t>(c.tokens, 0)};
 }
 
 // ---- the choice of kernel --------------------------------------------------------------
@@ -243,6 +243,15 @@ constexpr uint8_t kGroupRows = 6;     // row tiles of a group rastered together
 // rows of tiles rastered together, as set_grid in product.hip
 uint8_t raster_rows(int64_t rows) { return (uint8_t)(rows <= 8 ? std::max<int64_t>(rows, 1) : 4); }
 
+// A section of `bytes` at the end of a workspace of `size` bytes so far, -1 if it is not `wanted`.
+int64_t section(bool wanted, int64_t bytes, int64_t& size) {
+    if (!wanted) return -1;
+    const int64_t at = size;
+    size += up(bytes, kAlign);
+    return at;
+}
+void* at(void* workspace, int64_t offset) { return offset < 0 ? nullptr : (char*)workspace + offset; }
+
 // The rest of a rows product's arguments; returns its workgroups.
 int64_t rows_grid(const Common& c, int tile, int mats, ProductArgs& a) {
     a.zm = a.zn = a.split = 1;
@@ -256,10 +265,34 @@ int64_t rows_grid(const Common& c, int tile, int mats, ProductArgs& a) {
     return up(tiles * a.tiles_n, 8);
 }
 
+template <bool DUAL, bool SEG>
+void launch_join(bool bf, const ProductArgs& a, const GroupArgs& g, hipStream_t st) {
+    const dim3 grid(spg::kRound / 2 * spg::kJoin);
+    if (bf) hipLaunchKernelGGL((spg::grouped_join<spg::kElBF16, DUAL, SEG>), grid, dim3(256), 0, st, a, g);
+    else hipLaunchKernelGGL((spg::grouped_join<spg::kElF16, DUAL, SEG>), grid, dim3(256), 0, st, a, g);
+}
+
+// Whether the last round's tiles may be split: the parts' buffer is asked for and the launch that
+// joins them made.  Long reductions in few rounds; past 12 a round is less than 8% of the call.
+bool may_split(const RowsShape& s, int tile) {
+    return tile == spg::kTileBig && s.kt >= 2 * spg::kSplitGain && rows_wgs(s, tile) <= 12.0 * spg::kRound;
+}
+
+// parts: null where no tile is split
 gemm_status run_rows(int product, const Common& c, bool reg, int tile, int mats, ProductArgs a, const int32_t* offsets,
-                     const int32_t* source, hipStream_t st) {
-    const int64_t wgs = rows_grid(c, tile, mats, a);
-    launch_any(product, c.bf, reg, tile, a, group_args(c, offsets, source), 0, dim3((unsigned)wgs), st);
+                     const int32_t* source, void* parts, hipStream_t st) {
+    int64_t wgs = rows_grid(c, tile, mats, a);
+    GroupArgs g = group_args(c, offsets, source);
+    if (tile == spg::kTileBig && !reg && parts) {
+        g.part = (float*)parts;
+        wgs += spg::kRound;    // a whole round of parts in the place of a part of one
+    }
+    launch_any(product, c.bf, reg, tile, a, g, 0, dim3((unsigned)wgs), st);
+    const gemm_status e = launched();
+    if (e != GEMM_OK || !g.part) return e;
+    if (mats == 2) launch_join<true, false>(c.bf, a, g, st);
+    else if (a.segments == 2) launch_join<false, true>(c.bf, a, g, st);
+    else launch_join<false, false>(c.bf, a, g, st);
     return launched();
 }
 
@@ -305,7 +338,7 @@ gemm_status run_weights(const Common& c, bool reg, int tile, ProductArgs w, cons
 
 // Both gradients, in one launch where `both` names a tile for it.
 gemm_status run_gradients(int product, const Common& c, bool regx, bool regw, const int* dx, const int* dw, const int* both,
-                          ProductArgs x, ProductArgs w, const int32_t* offsets, hipStream_t st) {
+                          ProductArgs x, ProductArgs w, const int32_t* offsets, void* parts, hipStream_t st) {
     const bool reg = regx || regw;
     if (both[reg] >= 0) {
         const int t = both[reg];
@@ -320,7 +353,7 @@ gemm_status run_gradients(int product, const Common& c, bool regx, bool regw, co
         }
         return launched();
     }
-    const gemm_status e = run_rows(product, c, regx, dx[regx], 1, x, offsets, nullptr, st);
+    const gemm_status e = run_rows(product, c, regx, dx[regx], 1, x, offsets, nullptr, parts, st);
     return e != GEMM_OK ? e : run_weights(c, regw, dw[regw], w, offsets, st);
 }
 
@@ -400,6 +433,7 @@ struct gemm_grouped_plan {
     bool simple, simple_back, stream, stream_back, gather;   // gather: X's rows copied into their groups' order
     int fwd[2], dx[2], dw[2], both[2];   // tile classes [register-staged]; both: -1 for two launches
     int64_t ws_run, ws_back;
+    int64_t part_run, part_back;         // where the last round's parts go in the workspace, -1: nothing is split
 };
 
 struct gemm_experts_plan {
@@ -409,6 +443,7 @@ struct gemm_experts_plan {
     int fwd[2], dx[2], dw[2], both[2];
     int64_t np;                    // columns of dG and of dU in the workspace
     int64_t ws_run, ws_back, off_x;
+    int64_t part_run, part_back;
 };
 
 extern "C" {
@@ -439,7 +474,9 @@ gemm_status gemm_grouped_create(gemm_grouped_handle* out, int64_t rows, int64_t 
     }
     p->gather = tokens >= 0 && !fits(tokens, K * 2);
     p->ws_run = p->simple || p->stream || !p->gather ? 0 : c.gathered();
+    p->part_run = section(!p->simple && !p->stream && may_split(fwd, p->fwd[0]), spg::kPartBytes, p->ws_run);
     p->ws_back = p->simple_back ? 0 : c.gathered();
+    p->part_back = section(!p->simple_back && !p->stream_back && may_split(dx, p->dx[0]), spg::kPartBytes, p->ws_back);
     *out = p;
     return GEMM_OK;
 }
@@ -477,7 +514,7 @@ gemm_status gemm_grouped_run(gemm_grouped_handle h, const void* X, const void* W
         source = nullptr;
     }
     const bool reg = a.lda % 4 != 0 || !words(a.A) || a.ldb % 4 != 0 || !words(W);
-    return run_rows(c.nk ? spg::kRowsNK : spg::kRowsKN, c, reg, h->fwd[reg], 1, a, offsets, source, stream);
+    return run_rows(c.nk ? spg::kRowsNK : spg::kRowsKN, c, reg, h->fwd[reg], 1, a, offsets, source, at(workspace, h->part_run), stream);
 }
 
 gemm_status gemm_grouped_backward(gemm_grouped_handle h, const void* dY, const void* X, const void* W,
@@ -521,11 +558,11 @@ gemm_status gemm_grouped_backward(gemm_grouped_handle h, const void* dY, const v
     const bool regx = regd || a.ldb % 4 != 0 || !words(W), regw = regd || ldx % 4 != 0 || !words(x);
     const int product = c.nk ? spg::kRowsKN : spg::kRowsNK;
     if (rows && weights && !h->stream_back)
-        return run_gradients(product, c, regx, regw, h->dx, h->dw, h->both, a, w, offsets, stream);
+        return run_gradients(product, c, regx, regw, h->dx, h->dw, h->both, a, w, offsets, at(workspace, h->part_back), stream);
     gemm_status e = GEMM_OK;
     if (rows)
         e = h->stream_back ? run_stream(c, false, a, offsets, nullptr, stream)
-                           : run_rows(product, c, regx, h->dx[regx], 1, a, offsets, nullptr, stream);
+                           : run_rows(product, c, regx, h->dx[regx], 1, a, offsets, nullptr, at(workspace, h->part_back), stream);
     return e != GEMM_OK || !weights ? e : run_weights(c, regw, h->dw[regw], w, offsets, stream);
 }
 
@@ -561,8 +598,10 @@ gemm_status gemm_experts_create(gemm_experts_handle* out, int64_t rows, int64_t 
     }
     p->gather = tokens >= 0 && !fits(tokens, K * 2);
     p->ws_run = p->simple || p->stream || !p->gather ? 0 : c.gathered();
+    p->part_run = section(!p->simple && !p->stream && may_split(fwd, p->fwd[0]), spg::kPartBytes, p->ws_run);
     p->off_x = up(rows * p->np * 4, kAlign);
     p->ws_back = p->off_x + (p->simple_back ? 0 : c.gathered());
+    p->part_back = section(!p->simple_back && may_split(dx, p->dx[0]), spg::kPartBytes, p->ws_back);
     *out = p;
     return GEMM_OK;
 }
@@ -604,7 +643,7 @@ gemm_status gemm_experts_run(gemm_experts_handle h, const void* X, const void* W
         source = nullptr;
     }
     const bool reg = a.lda % 4 != 0 || !words(a.A) || a.ldb % 4 != 0 || !words(Wg) || !words(Wu);
-    return run_rows(c.nk ? spg::kRowsGatedNK : spg::kRowsGatedKN, c, reg, h->fwd[reg], 2, a, offsets, source, stream);
+    return run_rows(c.nk ? spg::kRowsGatedNK : spg::kRowsGatedKN, c, reg, h->fwd[reg], 2, a, offsets, source, at(workspace, h->part_run), stream);
 }
 
 gemm_status gemm_experts_backward(gemm_experts_handle h, const void* dH, const void* X, const void* Wg, const void* Wu,
@@ -662,7 +701,7 @@ gemm_status gemm_experts_backward(gemm_experts_handle h, const void* dH, const v
     }
     const ProductArgs w = weights_args(c, 2, (const char*)D, h->np * 4, h->np, h->np * 2, x, ldx, cols, dWg, dWu);
     const bool regx = a.ldb % 4 != 0 || !words(Wg) || !words(Wu), regw = ldx % 4 != 0 || !words(x);
-    return run_gradients(c.nk ? spg::kRowsSumNK : spg::kRowsSumKN, c, regx, regw, h->dx, h->dw, h->both, a, w, offsets, stream);
+    return run_gradients(c.nk ? spg::kRowsSumNK : spg::kRowsSumKN, c, regx, regw, h->dx, h->dw, h->both, a, w, offsets, at(workspace, h->part_back), stream);
 }
 
 gemm_status gemm_experts_destroy(gemm_experts_handle h) {

@@ -10,6 +10,7 @@ namespace spg {
 struct GroupArgs {
     const int32_t* offsets;   // [groups + 1]
     const int32_t* source;    // row -> row of X, or null
+    float* part;              // sums of the last tiles' parts, or null: no tile is split (rows)
     int64_t b_step;           // bytes from one group's B matrix to the next (rows), or of C (weights)
     int32_t groups, rows;
     int32_t tokens;           // rows of X where there is a source
@@ -88,6 +89,28 @@ __device__ __forceinline__ void raster(int at, int rows, int cols, int group_m, 
     tn = in / gm;
 }
 
+// Tiles come in rounds of one per CU, and the last round leaves CUs idle: 592 tiles of 256
+// k-tiles are 2.3 rounds and take 3.  Where it is worth it the last round's tiles are split along
+// the reduction, a part to each workgroup, and a second launch (grouped_join) adds the parts in
+// order.  How many tiles there are is only known here, so both kernels work it out.
+struct LastRound {
+    int full;      // tiles that stay whole
+    int parts;     // of each of the others; 1: none is split
+    int kt_part;
+};
+constexpr int kRound = 256, kMostParts = 8;
+// Parts cost a write, a read and a launch: about 24 k-tiles of a 256x256 tile.
+constexpr int kSplitGain = 24;
+__device__ __forceinline__ LastRound last_round(int tiles, int kt) {
+    const int full = tiles / kRound * kRound, rest = tiles - full;
+    int parts = rest > 0 ? kRound / rest : 1;
+    parts = parts < kMostParts ? parts : kMostParts;
+    const int kt_part = (kt + parts - 1) / parts;
+    parts = (kt + kt_part - 1) / kt_part;
+    if (parts < 2 || kt - kt_part < kSplitGain) return LastRound{tiles, 1, kt};
+    return LastRound{full, parts, kt_part};
+}
+
 // The rows of every group times its matrix on the tiled kernel (product_tile_of): a workgroup
 // finds its tile among all groups' row tiles and takes its group for the whole problem.  The
 // grid covers the most row tiles that `rows` rows in `groups` groups can come to; what is left
@@ -96,9 +119,25 @@ __device__ __forceinline__ void raster(int at, int rows, int cols, int group_m, 
 template <int ET, bool B_N, bool DUAL, bool SEG, bool REG, int BM, int BN, int WM, int WN, int S, bool DEEP, int KG, bool TAIL,
           bool GATHER>
 __device__ __forceinline__ void rows_tile(ProductArgs args, const GroupArgs& g, int wg, SPG_LDS char* lds) {
+    constexpr bool SPLIT = BM == 256 && BN == 256 && !REG;
     const int lane = threadIdx.x & 63;
-    const int rows = all_units<BM>(g, lane);
-    const int at = xcd_place(wg, rows * args.tiles_n);
+    const int tiles = all_units<BM>(g, lane) * args.tiles_n;
+    int at = -1, sp = 0;
+    args.part = nullptr;
+    LastRound last{tiles, 1, 0};
+    if constexpr (SPLIT)
+        if (g.part) last = last_round(tiles, (args.K + 63) / 64 * (SEG ? 2 : 1));
+    if (!SPLIT || wg < last.full) {
+        at = xcd_place(wg, last.full);
+    } else if (last.parts > 1) {
+        at = xcd_place(wg - last.full, (tiles - last.full) * last.parts);
+        if (at >= 0) {
+            args.part = g.part + (size_t)at * BM * BN;
+            args.kt_part = last.kt_part;
+            sp = at % last.parts;
+            at = last.full + at / last.parts;
+        }
+    }
     if (at < 0) return;
     // a group's tiles one after the other, so that its matrix is read once for all its rows: up to
     // group_m row tiles go through the columns together, more in even parts
@@ -117,9 +156,8 @@ __device__ __forceinline__ void rows_tile(ProductArgs args, const GroupArgs& g, 
         args.U = (char*)args.U + out;
     }
     args.M = f.g.n;
-    args.part = nullptr;
-    product_tile_of<ET, false, B_N, DUAL, SEG, REG, BM, BN, WM, WN, S, DEEP, KG, TAIL, GATHER, true>(
-        args, tm, tn, 0, lds, SourceRows{GATHER ? g.source + f.g.first : nullptr, g.tokens});
+    product_tile_of<ET, false, B_N, DUAL, SEG, REG, BM, BN, WM, WN, S, DEEP, KG, TAIL, GATHER, true, KG == 1>(
+        args, tm, tn, sp, lds, SourceRows{GATHER ? g.source + f.g.first : nullptr, g.tokens});
 }
 
 template <int ET, bool B_N, bool DUAL, bool SEG, bool REG, int BM, int BN, int WM, int WN, int S, bool DEEP, int KG, bool TAIL,
@@ -128,6 +166,43 @@ __global__ void __launch_bounds__((ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP, KG
 grouped_rows(ProductArgs args, GroupArgs g) {
     __shared__ __attribute__((aligned(1024))) char lds[ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP, KG>::LDS];
     rows_tile<ET, B_N, DUAL, SEG, REG, BM, BN, WM, WN, S, DEEP, KG, TAIL, GATHER>(args, g, blockIdx.x, (SPG_LDS char*)lds);
+}
+
+// The parts of the last round's tiles added, and the epilogue: 16 workgroups a tile, each of
+// whose waves adds some of the accumulators of the tile's waves, 16 rows x 16 columns a time.
+constexpr int kJoin = 16;
+template <int ET, bool DUAL, bool SEG>
+__global__ void __launch_bounds__(256) grouped_join(ProductArgs args, GroupArgs g) {
+    constexpr int WM = DUAL ? 64 : 128, WN = DUAL ? 128 : 64;      // the 256x256 tile of grouped_launch.hpp
+    using G = ProductGeom<DUAL, 256, 256, WM, WN, 2, false, 1>;
+    constexpr int UNITS = (DUAL ? G::TN / 2 : G::TN) * G::TM, EACH = G::NW * UNITS / (kJoin * 4);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tiles = all_units<256>(g, lane) * args.tiles_n;
+    const LastRound last = last_round(tiles, (args.K + 63) / 64 * (SEG ? 2 : 1));
+    const int t = blockIdx.x / kJoin;
+    if (last.parts == 1 || t >= tiles - last.full) return;
+    const int at = last.full + t, u = at / args.tiles_n;
+    const Found f = find_unit<256>(g, u, lane);
+    const int mine = (f.g.n + 255) / 256, in = (mine + args.group_m - 1) / args.group_m;
+    int tm, tn;
+    raster(at - (u - f.unit) * args.tiles_n, mine, args.tiles_n, (mine + in - 1) / in, tm, tn);
+    const float* part = g.part + (size_t)t * last.parts * 65536;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        const int q = ((blockIdx.x % kJoin) * 4 + wave) * EACH + i, w = q / UNITS, j = q % UNITS;
+        const int m = tm * 256 + w / G::WAVES_N * WM + j % G::TM * 16 + (lane & 15);
+        const int n = tn * G::BNS + w % G::WAVES_N * G::WNS + j / G::TM * 16 + 4 * (lane >> 4);
+        if (m >= f.g.n || n >= args.N) continue;
+        const float* p = part + ((w * G::TN * G::TM + j) * 64 + lane) * 4;
+        floatx4 s0 = *(const floatx4*)p, s1 = s0;
+        constexpr int UP = DUAL ? UNITS * 256 : 0;                  // the up projection's accumulators
+        if (DUAL) s1 = *(const floatx4*)(p + UP);
+        for (int k = 1; k < last.parts; ++k) {
+            s0 += *(const floatx4*)(p + (size_t)k * 65536);
+            if (DUAL) s1 += *(const floatx4*)(p + (size_t)k * 65536 + UP);
+        }
+        finish4<ET, DUAL>(s0, s1, 0, n, args.N - n < 4 ? args.N - n : 4, (size_t)(f.g.first + m) * args.N + n, args);
+    }
 }
 
 // The weights' gradients of every group: the reduction runs over the group's rows.  `per`

@@ -342,12 +342,14 @@ struct ProductGeom {
 //   GATHER  row r of A is row from.index[r] of a matrix of from.rows rows (outside them: zeros)
 //   SKIP    waves whose rows all lie past the last one neither read fragments nor multiply, which
 //           leaves their SIMDs' matrix cores to the others: for row tiles that are often cut
+//   LOCAL   a part of the sum (args.part) goes to a buffer of this tile and part alone, in the
+//           accumulators' order
 struct SourceRows {
     const int32_t* index;
     int32_t rows;
 };
 template <int ET, bool A_T, bool B_N, bool DUAL, bool SEG, bool REG, int BM, int BN, int WM, int WN,
-          int S, bool DEEP, int KG, bool TAIL, bool GATHER = false, bool SKIP = false>
+          int S, bool DEEP, int KG, bool TAIL, bool GATHER = false, bool SKIP = false, bool LOCAL = false>
 __device__ __forceinline__ void product_tile_of(ProductArgs args, int tm, int tn, int sp, SPG_LDS char* lds,
                                                 SourceRows from = SourceRows{}) {
     using G = ProductGeom<DUAL, BM, BN, WM, WN, S, DEEP, KG>;
@@ -827,7 +829,17 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, int tm, int tn
 
     // ---- epilogue ----
     const int m_base = m0 + wm * WM, n_base = n0 + wn * WNS;
-    if (args.part) {
+    if constexpr (LOCAL) {
+        static_assert(KG == 1, "one accumulator a wave");
+        if (args.part) {
+            float* to = args.part + (size_t)wave * TN * TM * 256 + lane * 4;
+            if (!(SKIP && idle))
+#pragma unroll
+                for (int i = 0; i < TN * TM; ++i) *(AccOf<ET>*)(to + i * 256) = acc[i / TM][i % TM];
+            wait_vmcnt<0>();   // as below
+            return;
+        }
+    } else if (args.part) {
         // a part of the sum: raw accumulators, row-major, 16 bytes per lane
         const int np4 = (N + 3) & ~3;
         const int zrow = args.zm == 2 ? z * M : 0, zcol = args.zn == 2 ? z * np4 : 0;

@@ -360,3 +360,48 @@ def test_rows_that_end_inside_a_chunk_many_times(K):
             plan(x, w, offsets, y, workspace=ws)
             for e in range(0, E, 2):
                 _check_rows(x[o[e]:o[e + 1]], _as_kn(w[e], "nk"), y[o[e]:o[e + 1]], "bf16", f"group {e}")
+
+
+@pytest.mark.parametrize("layout", ["nk", "kn"])
+@pytest.mark.parametrize("case", [([1300, 1100, 0, 900], 2304, 4160), ([2050], 4096, 6154), ([300, 515, 257, 600, 256, 1024, 70], 2050, 4096)],
+                         ids=["groups", "one", "many"])
+def test_last_round_in_parts(case, layout):
+    # grids of a little more than a round of 256x256 tiles with long reductions: the last tiles are
+    # split along the sum; rows cut on both sides of a tile's half, columns cut, G and U kept
+    torch = _t()
+    counts, N, K = case
+    o = [3 + sum(counts[:i]) for i in range(len(counts) + 1)]
+    rows, E = o[-1] + 2, len(counts)
+    offsets = torch.tensor(o, dtype=torch.int32, device="cuda")
+    tokens = 1500
+    for dtype, src in (("bf16", True), ("f16", False)):
+        dt = _dt(dtype)
+        xr = tokens if src else rows
+        x = Buf((xr, K), dt, 0, _normal(_gen(1), (xr, K), 1.0).to(dt))
+        w = [_weights(E, N, K, dtype, layout, 2 + i, 0) for i in (0, 1)]
+        dh = Buf((rows, N), dt, 0, _normal(_gen(4), (rows, N), 0.3).to(dt))
+        source = _source(rows, tokens, 5) if src else None
+        h, g, u, dx, y, dx1 = (Buf((rows, n), dt) for n in (N, N, N, K, N, K))
+        dwg, dwu, dw = (Buf(w[0].t.shape, dt) for _ in range(3))
+        t = tokens if src else None
+        with spg.GroupedGated(rows, N, K, E, dtype, layout, "silu", tokens=t) as plan:
+            plan(x.t, w[0].t, w[1].t, offsets, h.t, source=source, G=g.t, U=u.t,
+                 workspace=_workspace(plan.workspace_bytes(backward=False)))
+            plan.backward(dh.t, x.t, w[0].t, w[1].t, g.t, u.t, offsets, dx.t, dwg.t, dwu.t, source=source,
+                          workspace=_workspace(plan.workspace_bytes()))
+        with spg.GroupedGemm(rows, N, K, E, dtype, layout, tokens=t) as plan:
+            plan(x.t, w[0].t, offsets, y.t, source=source, workspace=_workspace(plan.workspace_bytes(backward=False)))
+            plan.backward(dh.t, x.t, w[0].t, offsets, dx1.t, dw.t, source=source, workspace=_workspace(plan.workspace_bytes()))
+        torch.cuda.synchronize()
+        xs = _gathered(x.t, source)
+        for e in range(E):
+            r = slice(o[e], o[e + 1])
+            if o[e] == o[e + 1]:
+                continue
+            _check_forward(xs[r], w[0].t[e], w[1].t[e], h.t[r], g.t[r], u.t[r], dtype, layout, "silu")
+            _check_backward(dh.t[r], xs[r], w[0].t[e], w[1].t[e], g.t[r], u.t[r], dx.t[r], dwg.t[e], dwu.t[e], dtype, layout, "silu")
+            wd = _as_kn(w[0].t[e], layout)
+            _check_rows(xs[r], wd, y.t[r], dtype, f"Y of group {e}")
+            _check_rows(dh.t[r], wd.t().contiguous(), dx1.t[r], dtype, f"dX of group {e}")
+        assert all(_untouched(b, o) for b in (h, g, u, dx, y, dx1))
+        assert all(b.intact() for b in (x, *w, dh, h, g, u, dx, y, dx1, dwg, dwu, dw))
