@@ -4,6 +4,7 @@
 #pragma once
 
 #include "product_kernels.hpp"
+#include "wave_scan.hpp"
 
 namespace spg {
 
@@ -24,17 +25,6 @@ __device__ __forceinline__ Group group_of(const GroupArgs& g, int e) {
     auto inside = [&](int v) { return v < 0 ? 0 : v > g.rows ? g.rows : v; };
     const int a = inside(g.offsets[e]), b = inside(g.offsets[e + 1]);
     return Group{a, b > a ? b - a : 0};
-}
-
-// Inclusive sum over a wave's lanes: shifts within rows of 16 lanes, then the rows' ends.
-__device__ __forceinline__ int wave_scan(int v) {
-    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);   // row_shr:1
-    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);   // row_shr:2
-    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);   // row_shr:4
-    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);   // row_shr:8
-    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row_bcast:15 into rows 1 and 3
-    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // row_bcast:31 into rows 2 and 3
-    return v;
 }
 
 // Group e of 64 from `first` on in lane e - first, and how many units of U rows it has.

@@ -7,7 +7,7 @@ namespace spg {
 
 // Microseconds of a tile class: a k-tile, and a workgroup's start and store, with direct
 // copies and register-staged (which has no 256x256 and no pair tile): fitted to the products of
-// product.hip (see choose() there); grouped.hip prices its own by the same
+// product.hip (see choose() there); grouped.hip has its own and takes the slots from here
 constexpr double kTileUs[kTiles] = {1.27, 0.76, 0.51, 0.32, 0.26, 0.70};
 constexpr double kStartUs[kTiles] = {5.3, 5.6, 2.5, 2.75, 2.75, 2.9};
 constexpr double kStagedUs[kTiles] = {0.0, 1.30, 0.65, 0.48, 0.42, 0.0};
