@@ -323,9 +323,10 @@ gemm_status gemm_quantize_rows(const void* X, gemm_dtype dtype, int64_t rows, in
  * Groups.  Rows that belong to the same expert lie together: group e is rows offsets[e] to
  * offsets[e+1] - 1 of `rows`, offsets [groups + 1] int32 on the device, read there (no call
  * waits for them).  Groups may be empty, and rows may be left over in front of the first
- * group and behind the last: no call reads or writes them.  Offsets outside 0 .. rows count
- * as the nearest of the two, and a group that would end before it starts is empty; where that
- * makes groups overlap, rows may be left out, but nothing outside the operands is touched. */
+ * group and behind the last: no call writes them, and what they hold changes nothing.  Offsets
+ * outside 0 .. rows count as the nearest of the two, and a group that would end before it
+ * starts is empty; where groups overlap, their rows' results are not specified, but nothing
+ * outside the operands is touched. */
 
 typedef struct gemm_norm_plan* gemm_norm_handle;
 typedef struct gemm_route_plan* gemm_route_handle;

@@ -125,19 +125,29 @@ double cost_us(const Cost& c, double rounds, double kt, double bytes) {
 }
 
 struct Choice {
-    int tile;
+    int tile;    // -1: no class has few enough workgroups for a launch
     double us;   // estimated
 };
+
+// A launch has less than 2^32 threads, a workgroup up to 512.
+constexpr int64_t kMostWgs = ((int64_t)1 << 23) - 2 * spg::kRound;
+
+// The most workgroups that the rows can come to: every group with rows has at most one tile that is
+// not full.
+int64_t most_wgs(int64_t rows, int64_t live, int64_t N, int t, int mats) {
+    const int64_t BM = spg::kGroupTileM[t];
+    return ((rows - live) / BM + live) * ceil_div(N, spg::group_tile_n(t, mats));
+}
 
 double rows_wgs(const RowsShape& s, int t) {
     return row_tiles(s, spg::kGroupTileM[t]) * (double)ceil_div(s.N, spg::group_tile_n(t, s.mats));
 }
 
 Choice choose_rows(const RowsShape& s, bool reg) {
-    Choice best{spg::kTileNarrow, 1e30};
+    Choice best{-1, 1e30};
     for (int t = 0; t < spg::kGroupTiles; ++t) {
         const Cost& c = kRows[reg][s.mats == 2][t];
-        if (c.bw == 0) continue;
+        if (c.bw == 0 || most_wgs(s.rows, s.live, s.N, t, s.mats) > kMostWgs) continue;
         const double us = cost_us(c, rows_wgs(s, t) / slots(t, reg), (double)s.kt, s.bytes);
         if (us < best.us) best = Choice{t, us};
     }
@@ -158,12 +168,14 @@ WeightsShape weights_shape(const Common& c, int mats) {
 double weights_wgs(const WeightsShape& s, int t) {
     return (double)s.groups * s.mats * (double)(ceil_div(s.M, spg::kTileM[t]) * ceil_div(s.N, spg::kTileN[t]));
 }
+// ... as launched: whole eights of them a group
+bool too_many(const WeightsShape& s, int t) { return weights_wgs(s, t) + 8.0 * s.groups > (double)kMostWgs; }
 
 Choice choose_weights(const WeightsShape& s, bool reg) {
-    Choice best{spg::kTileNarrow, 1e30};
+    Choice best{-1, 1e30};
     for (int t = 0; t < spg::kTiles; ++t) {
         const Cost& c = kWeights[reg][t];
-        if (c.bw == 0) continue;
+        if (c.bw == 0 || too_many(s, t)) continue;
         const double us = cost_us(c, weights_wgs(s, t) / slots(t, reg), s.kt, s.bytes);
         if (us < best.us) best = Choice{t, us};
     }
@@ -177,6 +189,7 @@ int choose_both(const RowsShape& x, const WeightsShape& w, bool reg, double apar
     for (int t : {(int)spg::kTileMid, (int)spg::kTileSmall}) {
         const Cost& cx = kRows[reg][0][t];
         const Cost& cw = t == spg::kTileMid ? kWeightsMid[reg] : kWeights[reg][t];
+        if ((double)most_wgs(x.rows, x.live, x.N, t, 1) + weights_wgs(w, t) + 8.0 * w.groups > (double)kMostWgs) continue;
         const double nx = rows_wgs(x, t) / slots(t, reg), nw = weights_wgs(w, t) / slots(t, reg);
         const double full = nx * ((double)x.kt * cx.busy + cx.tile) + nw * (w.kt * cw.busy + cw.tile);
         const double us = cx.base + std::max(std::max(std::max((double)x.kt * cx.alone, w.kt * cw.alone), full),
@@ -256,13 +269,10 @@ void* at(void* workspace, int64_t offset) { return offset < 0 ? nullptr : (char*
 int64_t rows_grid(const Common& c, int tile, int mats, ProductArgs& a) {
     a.zm = a.zn = a.split = 1;
     a.kt_part = kWhole;
-    const int BM = spg::kGroupTileM[tile];
-    // every group with rows has at most one tile that is not full
-    const int64_t tiles = (c.rows - c.live()) / BM + c.live();
     a.tiles_m = 0;   // found on the device
     a.tiles_n = (int32_t)ceil_div(a.N, spg::group_tile_n(tile, mats));
     a.group_m = kGroupRows;
-    return up(tiles * a.tiles_n, 8);
+    return up(most_wgs(c.rows, c.live(), a.N, tile, mats), 8);
 }
 
 template <bool DUAL, bool SEG>
@@ -456,7 +466,7 @@ gemm_status gemm_grouped_create(gemm_grouped_handle* out, int64_t rows, int64_t 
     gemm_grouped_plan* p = new (std::nothrow) gemm_grouped_plan{};
     if (!p) return GEMM_ERR_OUT_OF_MEMORY;
     const Common c = p->c = Common{rows, N, K, groups, tokens, dtype == GEMM_BF16, layout == GEMM_B_NK};
-    // the tiled kernels need 16 bytes of every row they copy, and 32-bit offsets
+    // the tiled kernels need 16 bytes of every row they copy, 32-bit offsets, and a grid that can be launched
     p->simple = K < 8 || (!c.nk && N < 8) || K * 2 > kMaxRowBytes || N * 2 > kMaxRowBytes;
     p->simple_back = p->simple || N < 8;
     p->stream = !p->simple && streams(c, N, K, 1, c.nk) && fits(std::max(rows, tokens), K * 2);
@@ -471,7 +481,12 @@ gemm_status gemm_grouped_create(gemm_grouped_handle* out, int64_t rows, int64_t 
         p->dx[r] = x.tile;
         p->dw[r] = w.tile;
         p->both[r] = choose_both(dx, dw, r == 1, x.us + w.us);
+        p->simple |= p->fwd[r] < 0;
+        p->simple_back |= x.tile < 0 || w.tile < 0;
     }
+    p->simple_back |= p->simple;
+    p->stream &= !p->simple;
+    p->stream_back &= !p->simple_back;
     p->gather = tokens >= 0 && !fits(tokens, K * 2);
     p->ws_run = p->simple || p->stream || !p->gather ? 0 : c.gathered();
     p->part_run = section(!p->simple && !p->stream && may_split(fwd, p->fwd[0]), spg::kPartBytes, p->ws_run);
@@ -595,7 +610,11 @@ gemm_status gemm_experts_create(gemm_experts_handle* out, int64_t rows, int64_t 
         p->dx[r] = x.tile;
         p->dw[r] = w.tile;
         p->both[r] = choose_both(dx, dw, r == 1, x.us + w.us);
+        p->simple |= p->fwd[r] < 0;
+        p->simple_back |= x.tile < 0 || w.tile < 0;
     }
+    p->simple_back |= p->simple;
+    p->stream &= !p->simple;
     p->gather = tokens >= 0 && !fits(tokens, K * 2);
     p->ws_run = p->simple || p->stream || !p->gather ? 0 : c.gathered();
     p->part_run = section(!p->simple && !p->stream && may_split(fwd, p->fwd[0]), spg::kPartBytes, p->ws_run);

@@ -484,10 +484,10 @@ __global__ void __launch_bounds__(256) simple_group_weights(SimpleWeightArgs a) 
                 int64_t row = r;
                 if (a.g.source) {
                     row = a.g.source[r];
-                    if (row < 0 || row >= a.g.tokens) continue;
+                    if (row < 0 || row >= a.g.tokens) row = -1;   // a row of zeros
                 }
                 s += bits_to_f32(((const uint16_t*)a.D)[r * a.ldd + n], BF16) *
-                     bits_to_f32(((const uint16_t*)a.X)[row * a.K + k], BF16);
+                     (row < 0 ? 0.0f : bits_to_f32(((const uint16_t*)a.X)[row * a.K + k], BF16));
             }
             c[n * a.sn + k * a.sk] = f32_to_bits(s, BF16);
         }
