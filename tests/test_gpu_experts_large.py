@@ -190,3 +190,26 @@ def test_many_matrices(layout):
         _check_rows(dy[r], wd.t().contiguous(), dx[r], "bf16", f"dX of group {e}")
         _check_weight(x[r], dy[r], dw[e], "bf16", layout, f"dW of group {e}")
     assert bool((dw[0] == 0).all()) and bool(torch.isfinite(dw[-6:]).all())
+
+
+@pytest.mark.parametrize("layout", ["nk", "kn"])
+def test_more_rows_than_small_tiles_launch(layout):
+    # row tiles of 64 rows would be more workgroups than a launch holds
+    torch = _t()
+    rows, N, K = 600_000_000, 8, 8
+    o = [1, rows // 2 + 3, rows // 2 + 3, rows - 2]
+    offsets = torch.tensor(o, dtype=torch.int32, device="cuda")
+    x = _rand((rows, K), 1.0, 18, torch.bfloat16)
+    w = _rand((3, N, K) if layout == "nk" else (3, K, N), 0.3, 19, torch.bfloat16)
+    y, dx = torch.zeros_like(x), torch.zeros_like(x)
+    with spg.GroupedGemm(rows, N, K, 3, "bf16", layout) as plan:
+        plan(x, w, offsets, y, workspace=_workspace(plan.workspace_bytes(backward=False)))
+        plan.backward(x, None, w, offsets, dx, None, workspace=_workspace(plan.workspace_bytes()))
+    torch.cuda.synchronize()
+    for e in (0, 2):
+        n = o[e + 1] - o[e]
+        r = _some(n, 4096) + o[e]
+        wd = _as_kn(w[e], layout)
+        _check_rows(x[r], wd, y[r], "bf16", f"Y of group {e}")
+        _check_rows(x[r], wd.t().contiguous(), dx[r], "bf16", f"dX of group {e}")
+    assert bool((y[0] == 0).all()) and bool((y[-2:] == 0).all()) and bool((dx[-2:] == 0).all())
