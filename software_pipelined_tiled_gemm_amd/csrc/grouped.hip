@@ -80,7 +80,6 @@ struct RowsShape {
     int64_t rows, live, N, kt;
     int mats;
     double bytes;
-    bool crooked;
 };
 
 // Row tiles of BM rows: the last tile of a group is half full on average.
@@ -125,8 +124,9 @@ double cost_us(const Cost& c, double rounds, double kt, double bytes) {
 }
 
 struct Choice {
-    int tile;    // -1: no class has few enough workgroups for a launch
-    double us;   // estimated
+    int tile;     // -1: no class has few enough workgroups for a launch
+    double us;    // estimated
+    bool split;   // the last round's tiles (a grid of less than a round: all of them) in parts
 };
 
 // A launch has less than 2^32 threads, a workgroup up to 512.
@@ -143,13 +143,31 @@ double rows_wgs(const RowsShape& s, int t) {
     return row_tiles(s, spg::kGroupTileM[t]) * (double)ceil_div(s.N, spg::group_tile_n(t, s.mats));
 }
 
+// Long reductions of few tiles are split over the CUs that have none.  256x256 tiles are in their
+// last round, too: past 12 rounds one is less than 8% of the call.  At 400 drawn shapes (1 to 32
+// groups, 1 to 2048 rows, matrices of 32 to 2048 columns and reductions of 1024 to 12288) the best
+// class with parts takes 0.27 to 1 of the time of the best without (5 columns of 736, 9728:
+// 13 and 37 us), and the choice 4.6% more than the best on average.
+constexpr double kJoinUs[spg::kGroupTiles] = {0, 0, 0, 4.5, 4.0, 0, 3.5};   // the parts' launch, write and read; 0: not split
+double split_us(const RowsShape& s, const Cost& c, int t, double wgs) {
+    if (kJoinUs[t] == 0) return 1e30;
+    const int bm = spg::kGroupTileM[t], bn = spg::group_tile_n(t, 1);
+    const double parts = std::min((double)spg::most_parts(bm, bn), std::floor(spg::kRound / wgs));
+    if (parts < 2.0) return 1e30;
+    const double kt = std::ceil((double)s.kt / parts);
+    if ((double)s.kt - kt < spg::split_gain(bm, bn)) return 1e30;
+    return kJoinUs[t] + cost_us(c, std::min(1.0, wgs * parts / spg::kRound), kt, s.bytes);
+}
+
 Choice choose_rows(const RowsShape& s, bool reg) {
-    Choice best{-1, 1e30};
+    Choice best{-1, 1e30, false};
     for (int t = 0; t < spg::kGroupTiles; ++t) {
         const Cost& c = kRows[reg][s.mats == 2][t];
         if (c.bw == 0 || most_wgs(s.rows, s.live, s.N, t, s.mats) > kMostWgs) continue;
-        const double us = cost_us(c, rows_wgs(s, t) / slots(t, reg), (double)s.kt, s.bytes);
-        if (us < best.us) best = Choice{t, us};
+        const double wgs = rows_wgs(s, t), us = cost_us(c, wgs / slots(t, reg), (double)s.kt, s.bytes), parts = split_us(s, c, t, wgs);
+        const bool last = t == spg::kTileBig && s.kt >= 2 * spg::split_gain(256, 256) && wgs <= 12.0 * spg::kRound;
+        if (us < best.us) best = Choice{t, us, last};
+        if (parts < best.us) best = Choice{t, parts, true};
     }
     return best;
 }
@@ -159,11 +177,10 @@ struct WeightsShape {
     int64_t groups, M, N;
     int mats;
     double kt, bytes;
-    bool crooked;
 };
 WeightsShape weights_shape(const Common& c, int mats) {
     return WeightsShape{c.groups, c.nk ? c.N : c.K, c.nk ? c.K : c.N, mats, (double)c.rows / (double)c.groups / 64.0 + 0.5,
-                        (double)mats * c.matrix() * c.groups, c.N % 64 != 0 || c.K % 64 != 0};
+                        (double)mats * c.matrix() * c.groups};
 }
 double weights_wgs(const WeightsShape& s, int t) {
     return (double)s.groups * s.mats * (double)(ceil_div(s.M, spg::kTileM[t]) * ceil_div(s.N, spg::kTileN[t]));
@@ -172,12 +189,12 @@ double weights_wgs(const WeightsShape& s, int t) {
 bool too_many(const WeightsShape& s, int t) { return weights_wgs(s, t) + 8.0 * s.groups > (double)kMostWgs; }
 
 Choice choose_weights(const WeightsShape& s, bool reg) {
-    Choice best{-1, 1e30};
+    Choice best{-1, 1e30, false};
     for (int t = 0; t < spg::kTiles; ++t) {
         const Cost& c = kWeights[reg][t];
         if (c.bw == 0 || too_many(s, t)) continue;
         const double us = cost_us(c, weights_wgs(s, t) / slots(t, reg), s.kt, s.bytes);
-        if (us < best.us) best = Choice{t, us};
+        if (us < best.us) best = Choice{t, us, false};
     }
     return best;
 }
@@ -256,9 +273,17 @@ constexpr uint8_t kGroupRows = 6;     // row tiles of a group rastered together
 // rows of tiles rastered together, as set_grid in product.hip
 uint8_t raster_rows(int64_t rows) { return (uint8_t)(rows <= 8 ? std::max<int64_t>(rows, 1) : 4); }
 
-// A section of `bytes` at the end of a workspace of `size` bytes so far, -1 if it is not `wanted`.
+// The parts of either choice
+int64_t most_part_bytes(const Choice* c) {
+    int64_t most = 0;
+    for (int r = 0; r < 2; ++r)
+        if (c[r].split) most = std::max(most, spg::part_bytes(c[r].tile));
+    return most;
+}
+
+// A section of `bytes` at the end of a workspace of `size` bytes so far, -1 if it is not wanted.
 int64_t section(bool wanted, int64_t bytes, int64_t& size) {
-    if (!wanted) return -1;
+    if (!wanted || bytes == 0) return -1;
     const int64_t at = size;
     size += up(bytes, kAlign);
     return at;
@@ -275,34 +300,50 @@ int64_t rows_grid(const Common& c, int tile, int mats, ProductArgs& a) {
     return up(most_wgs(c.rows, c.live(), a.N, tile, mats), 8);
 }
 
+// tiles and wave tiles as in launch_grouped
+template <int ET, bool DUAL, bool SEG>
+void launch_join(int tile, const ProductArgs& a, const GroupArgs& g, hipStream_t st) {
+    auto go = [&](auto bm, auto bn, auto wm, auto wn) {
+        constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value;
+        hipLaunchKernelGGL((spg::grouped_join<ET, DUAL, SEG, BM, BN, decltype(wm)::value, decltype(wn)::value>),
+                           dim3(spg::kRound / 2 * (BM * BN / 4096)), dim3(256), 0, st, a, g);
+    };
+    using std::integral_constant;
+    constexpr integral_constant<int, 32> i32{};
+    constexpr integral_constant<int, 64> i64{};
+    constexpr integral_constant<int, 128> i128{};
+    constexpr integral_constant<int, 256> i256{};
+    if (tile == spg::kTileBig) {
+        if constexpr (DUAL) go(i256, i256, i64, i128);
+        else go(i256, i256, i128, i64);
+    } else if (tile == spg::kTileThin) {
+        if constexpr (DUAL) go(i32, i128, i32, i64);
+        else go(i32, i128, i32, i32);
+    } else if (tile == spg::kTileSmall) go(i64, i128, i32, i64);
+    else go(i64, i64, i32, i64);
+}
 template <bool DUAL, bool SEG>
-void launch_join(bool bf, const ProductArgs& a, const GroupArgs& g, hipStream_t st) {
-    const dim3 grid(spg::kRound / 2 * spg::kJoin);
-    if (bf) hipLaunchKernelGGL((spg::grouped_join<spg::kElBF16, DUAL, SEG>), grid, dim3(256), 0, st, a, g);
-    else hipLaunchKernelGGL((spg::grouped_join<spg::kElF16, DUAL, SEG>), grid, dim3(256), 0, st, a, g);
+void launch_join(bool bf, int tile, const ProductArgs& a, const GroupArgs& g, hipStream_t st) {
+    if (bf) launch_join<spg::kElBF16, DUAL, SEG>(tile, a, g, st);
+    else launch_join<spg::kElF16, DUAL, SEG>(tile, a, g, st);
 }
 
-// Whether the last round's tiles may be split: the parts' buffer is asked for and the launch that
-// joins them made.  Long reductions in few rounds; past 12 a round is less than 8% of the call.
-bool may_split(const RowsShape& s, int tile) {
-    return tile == spg::kTileBig && s.kt >= 2 * spg::kSplitGain && rows_wgs(s, tile) <= 12.0 * spg::kRound;
-}
-
-// parts: null where no tile is split
-gemm_status run_rows(int product, const Common& c, bool reg, int tile, int mats, ProductArgs a, const int32_t* offsets,
+// parts: their place, used where the choice splits tiles
+gemm_status run_rows(int product, const Common& c, bool reg, const Choice& choice, int mats, ProductArgs a, const int32_t* offsets,
                      const int32_t* source, void* parts, hipStream_t st) {
+    const int tile = choice.tile;
     int64_t wgs = rows_grid(c, tile, mats, a);
     GroupArgs g = group_args(c, offsets, source);
-    if (tile == spg::kTileBig && !reg && parts) {
+    if (choice.split) {
         g.part = (float*)parts;
         wgs += spg::kRound;    // a whole round of parts in the place of a part of one
     }
     launch_any(product, c.bf, reg, tile, a, g, 0, dim3((unsigned)wgs), st);
     const gemm_status e = launched();
     if (e != GEMM_OK || !g.part) return e;
-    if (mats == 2) launch_join<true, false>(c.bf, a, g, st);
-    else if (a.segments == 2) launch_join<false, true>(c.bf, a, g, st);
-    else launch_join<false, false>(c.bf, a, g, st);
+    if (mats == 2) launch_join<true, false>(c.bf, tile, a, g, st);
+    else if (a.segments == 2) launch_join<false, true>(c.bf, tile, a, g, st);
+    else launch_join<false, false>(c.bf, tile, a, g, st);
     return launched();
 }
 
@@ -347,7 +388,7 @@ gemm_status run_weights(const Common& c, bool reg, int tile, ProductArgs w, cons
 }
 
 // Both gradients, in one launch where `both` names a tile for it.
-gemm_status run_gradients(int product, const Common& c, bool regx, bool regw, const int* dx, const int* dw, const int* both,
+gemm_status run_gradients(int product, const Common& c, bool regx, bool regw, const Choice* dx, const Choice* dw, const int* both,
                           ProductArgs x, ProductArgs w, const int32_t* offsets, void* parts, hipStream_t st) {
     const bool reg = regx || regw;
     if (both[reg] >= 0) {
@@ -364,7 +405,7 @@ gemm_status run_gradients(int product, const Common& c, bool regx, bool regw, co
         return launched();
     }
     const gemm_status e = run_rows(product, c, regx, dx[regx], 1, x, offsets, nullptr, parts, st);
-    return e != GEMM_OK ? e : run_weights(c, regw, dw[regw], w, offsets, st);
+    return e != GEMM_OK ? e : run_weights(c, regw, dw[regw].tile, w, offsets, st);
 }
 
 template <bool BF16, bool DUAL>
@@ -427,10 +468,16 @@ gemm_status simple_weights(const Common& c, const void* D, int64_t ldd, const vo
 // workgroups (16 columns of one group each), the same at 1024 and up to three times as long
 // beyond; a group of more than 16 rows reads its matrix again for every 16 of them.  Two long
 // matrices keep its workgroups busy enough to go on up to 4096 (single rows, 12288 x 4096: 70 us
-// against 81; of 2000 to 3500 reductions the same time).
+// against 81; of 2000 to 3500 reductions the same time).  A workgroup reads its columns one
+// chunk after the other, and where there are few of them and much to read, tiles in parts are
+// faster (72 rows of 5 groups, two matrices 96 x 12024: 86 us against 16).  Over 1300 shapes
+// this choice and that of the tiles take 4.0% more than the best.
 bool streams(const Common& c, int64_t N, int64_t K, int mats, bool along) {
-    return along && c.rows <= 16 * c.live() &&
-           ceil_div(N, 16) * std::max(c.live(), c.rows / 2) <= (mats == 2 && K >= 2048 ? 4096 : 1024);
+    if (!along || c.rows > 16 * c.live()) return false;
+    const int64_t columns = ceil_div(N, 16);
+    if (columns * std::max(c.live(), c.rows / 2) > (mats == 2 && K >= 2048 ? 4096 : 1024)) return false;
+    const double reads = (1.0 + (double)c.rows / (16.0 * (double)c.live())) * (double)K * mats;
+    return reads <= 14000.0 || columns * c.live() >= 512;
 }
 
 // Operands' first row and last byte within 32-bit offsets of the stream
@@ -441,7 +488,8 @@ bool fits(int64_t rows, int64_t row_bytes) { return rows * row_bytes + 2048 < kM
 struct gemm_grouped_plan {
     Common c;
     bool simple, simple_back, stream, stream_back, gather;   // gather: X's rows copied into their groups' order
-    int fwd[2], dx[2], dw[2], both[2];   // tile classes [register-staged]; both: -1 for two launches
+    Choice fwd[2], dx[2], dw[2];         // [register-staged]
+    int both[2];                         // a tile class, -1 for two launches
     int64_t ws_run, ws_back;
     int64_t part_run, part_back;         // where the last round's parts go in the workspace, -1: nothing is split
 };
@@ -450,7 +498,8 @@ struct gemm_experts_plan {
     Common c;
     int act;
     bool simple, simple_back, stream, gather;
-    int fwd[2], dx[2], dw[2], both[2];
+    Choice fwd[2], dx[2], dw[2];
+    int both[2];
     int64_t np;                    // columns of dG and of dU in the workspace
     int64_t ws_run, ws_back, off_x;
     int64_t part_run, part_back;
@@ -472,26 +521,24 @@ gemm_status gemm_grouped_create(gemm_grouped_handle* out, int64_t rows, int64_t 
     p->stream = !p->simple && streams(c, N, K, 1, c.nk) && fits(std::max(rows, tokens), K * 2);
     p->stream_back = !p->simple_back && streams(c, K, N, 1, !c.nk) && fits(rows, N * 2);
     const double live = (double)c.live(), io = 2.0 * rows * (N + K) + live * c.matrix();
-    const bool crooked = N % 64 != 0 || K % 64 != 0;
-    const RowsShape fwd{rows, c.live(), N, ceil_div(K, 64), 1, io, crooked}, dx{rows, c.live(), K, ceil_div(N, 64), 1, io, crooked};
+    const RowsShape fwd{rows, c.live(), N, ceil_div(K, 64), 1, io}, dx{rows, c.live(), K, ceil_div(N, 64), 1, io};
     const WeightsShape dw = weights_shape(c, 1);
     for (int r = 0; r < 2; ++r) {
-        const Choice x = choose_rows(dx, r == 1), w = choose_weights(dw, r == 1);
-        p->fwd[r] = choose_rows(fwd, r == 1).tile;
-        p->dx[r] = x.tile;
-        p->dw[r] = w.tile;
-        p->both[r] = choose_both(dx, dw, r == 1, x.us + w.us);
-        p->simple |= p->fwd[r] < 0;
-        p->simple_back |= x.tile < 0 || w.tile < 0;
+        p->fwd[r] = choose_rows(fwd, r == 1);
+        p->dx[r] = choose_rows(dx, r == 1);
+        p->dw[r] = choose_weights(dw, r == 1);
+        p->both[r] = choose_both(dx, dw, r == 1, p->dx[r].us + p->dw[r].us);
+        p->simple |= p->fwd[r].tile < 0;
+        p->simple_back |= p->dx[r].tile < 0 || p->dw[r].tile < 0;
     }
     p->simple_back |= p->simple;
     p->stream &= !p->simple;
     p->stream_back &= !p->simple_back;
     p->gather = tokens >= 0 && !fits(tokens, K * 2);
     p->ws_run = p->simple || p->stream || !p->gather ? 0 : c.gathered();
-    p->part_run = section(!p->simple && !p->stream && may_split(fwd, p->fwd[0]), spg::kPartBytes, p->ws_run);
+    p->part_run = section(!p->simple && !p->stream, most_part_bytes(p->fwd), p->ws_run);
     p->ws_back = p->simple_back ? 0 : c.gathered();
-    p->part_back = section(!p->simple_back && !p->stream_back && may_split(dx, p->dx[0]), spg::kPartBytes, p->ws_back);
+    p->part_back = section(!p->simple_back && !p->stream_back, most_part_bytes(p->dx), p->ws_back);
     *out = p;
     return GEMM_OK;
 }
@@ -578,7 +625,7 @@ gemm_status gemm_grouped_backward(gemm_grouped_handle h, const void* dY, const v
     if (rows)
         e = h->stream_back ? run_stream(c, false, a, offsets, nullptr, stream)
                            : run_rows(product, c, regx, h->dx[regx], 1, a, offsets, nullptr, at(workspace, h->part_back), stream);
-    return e != GEMM_OK || !weights ? e : run_weights(c, regw, h->dw[regw], w, offsets, stream);
+    return e != GEMM_OK || !weights ? e : run_weights(c, regw, h->dw[regw].tile, w, offsets, stream);
 }
 
 gemm_status gemm_grouped_destroy(gemm_grouped_handle h) {
@@ -601,26 +648,24 @@ gemm_status gemm_experts_create(gemm_experts_handle* out, int64_t rows, int64_t 
     p->simple_back = p->simple || p->np * 4 > kMaxRowBytes;
     p->stream = !p->simple && streams(c, N, K, 2, c.nk) && fits(std::max(rows, tokens), K * 2);
     const double live = (double)c.live(), io = 2.0 * rows * (N + K) + 2.0 * live * c.matrix();
-    const bool crooked = N % 64 != 0 || K % 64 != 0;
-    const RowsShape fwd{rows, c.live(), N, ceil_div(K, 64), 2, io, crooked}, dx{rows, c.live(), K, 2 * ceil_div(N, 64), 1, io, crooked};
+    const RowsShape fwd{rows, c.live(), N, ceil_div(K, 64), 2, io}, dx{rows, c.live(), K, 2 * ceil_div(N, 64), 1, io};
     const WeightsShape dw = weights_shape(c, 2);
     for (int r = 0; r < 2; ++r) {
-        const Choice x = choose_rows(dx, r == 1), w = choose_weights(dw, r == 1);
-        p->fwd[r] = choose_rows(fwd, r == 1).tile;
-        p->dx[r] = x.tile;
-        p->dw[r] = w.tile;
-        p->both[r] = choose_both(dx, dw, r == 1, x.us + w.us);
-        p->simple |= p->fwd[r] < 0;
-        p->simple_back |= x.tile < 0 || w.tile < 0;
+        p->fwd[r] = choose_rows(fwd, r == 1);
+        p->dx[r] = choose_rows(dx, r == 1);
+        p->dw[r] = choose_weights(dw, r == 1);
+        p->both[r] = choose_both(dx, dw, r == 1, p->dx[r].us + p->dw[r].us);
+        p->simple |= p->fwd[r].tile < 0;
+        p->simple_back |= p->dx[r].tile < 0 || p->dw[r].tile < 0;
     }
     p->simple_back |= p->simple;
     p->stream &= !p->simple;
     p->gather = tokens >= 0 && !fits(tokens, K * 2);
     p->ws_run = p->simple || p->stream || !p->gather ? 0 : c.gathered();
-    p->part_run = section(!p->simple && !p->stream && may_split(fwd, p->fwd[0]), spg::kPartBytes, p->ws_run);
+    p->part_run = section(!p->simple && !p->stream, most_part_bytes(p->fwd), p->ws_run);
     p->off_x = up(rows * p->np * 4, kAlign);
     p->ws_back = p->off_x + (p->simple_back ? 0 : c.gathered());
-    p->part_back = section(!p->simple_back && may_split(dx, p->dx[0]), spg::kPartBytes, p->ws_back);
+    p->part_back = section(!p->simple_back, most_part_bytes(p->dx), p->ws_back);
     *out = p;
     return GEMM_OK;
 }

@@ -82,22 +82,27 @@ __device__ __forceinline__ void raster(int at, int rows, int cols, int group_m, 
 // Tiles come in rounds of one per CU, and the last round leaves CUs idle: 592 tiles of 256
 // k-tiles are 2.3 rounds and take 3.  Where it is worth it the last round's tiles are split along
 // the reduction, a part to each workgroup, and a second launch (grouped_join) adds the parts in
-// order.  How many tiles there are is only known here, so both kernels work it out.
+// order: 8192 rows in 8 groups, 4096 x 8192, both passes 3340 us without, 3120 with.  So are the
+// tiles of a grid of less than half a round: 12 groups' single row, 840 x 6472 stored [K,N], 26.5
+// and 16.5 us.  How many tiles there are is only known here, so both kernels work it out.
 struct LastRound {
     int full;      // tiles that stay whole
     int parts;     // of each of the others; 1: none is split
     int kt_part;
 };
-constexpr int kRound = 256, kMostParts = 8;
-// Parts cost a write, a read and a launch: about 24 k-tiles of a 256x256 tile.
-constexpr int kSplitGain = 24;
+constexpr int kRound = 256;
+// Parts cost a write, a read and a launch: as many k-tiles have to be saved as take that long
+// (tile rows by tile columns).
+__host__ __device__ constexpr int split_gain(int bm, int bn) { return bm * bn == 256 * 256 ? 24 : 16; }
+__host__ __device__ constexpr int most_parts(int bm, int bn) { return bm * bn == 256 * 256 ? 8 : 16; }
+template <int BM, int BN>
 __device__ __forceinline__ LastRound last_round(int tiles, int kt) {
     const int full = tiles / kRound * kRound, rest = tiles - full;
     int parts = rest > 0 ? kRound / rest : 1;
-    parts = parts < kMostParts ? parts : kMostParts;
+    parts = parts < most_parts(BM, BN) ? parts : most_parts(BM, BN);
     const int kt_part = (kt + parts - 1) / parts;
     parts = (kt + kt_part - 1) / kt_part;
-    if (parts < 2 || kt - kt_part < kSplitGain) return LastRound{tiles, 1, kt};
+    if (parts < 2 || kt - kt_part < split_gain(BM, BN)) return LastRound{tiles, 1, kt};
     return LastRound{full, parts, kt_part};
 }
 
@@ -109,14 +114,14 @@ __device__ __forceinline__ LastRound last_round(int tiles, int kt) {
 template <int ET, bool B_N, bool DUAL, bool SEG, bool REG, int BM, int BN, int WM, int WN, int S, bool DEEP, int KG, bool TAIL,
           bool GATHER>
 __device__ __forceinline__ void rows_tile(ProductArgs args, const GroupArgs& g, int wg, SPG_LDS char* lds) {
-    constexpr bool SPLIT = BM == 256 && BN == 256 && !REG;
     const int lane = threadIdx.x & 63;
     const int tiles = all_units<BM>(g, lane) * args.tiles_n;
     int at = -1, sp = 0;
     args.part = nullptr;
     LastRound last{tiles, 1, 0};
+    constexpr bool SPLIT = BM == 256 || BM <= 64;   // the classes that the host splits
     if constexpr (SPLIT)
-        if (g.part) last = last_round(tiles, (args.K + 63) / 64 * (SEG ? 2 : 1));
+        if (g.part) last = last_round<BM, BN>(tiles, (args.K + 63) / 64 * (SEG ? 2 : 1));
     if (!SPLIT || wg < last.full) {
         at = xcd_place(wg, last.full);
     } else if (last.parts > 1) {
@@ -146,7 +151,7 @@ __device__ __forceinline__ void rows_tile(ProductArgs args, const GroupArgs& g, 
         args.U = (char*)args.U + out;
     }
     args.M = f.g.n;
-    product_tile_of<ET, false, B_N, DUAL, SEG, REG, BM, BN, WM, WN, S, DEEP, KG, TAIL, GATHER, true, KG == 1>(
+    product_tile_of<ET, false, B_N, DUAL, SEG, REG, BM, BN, WM, WN, S, DEEP, KG, TAIL, GATHER, true, SPLIT>(
         args, tm, tn, sp, lds, SourceRows{GATHER ? g.source + f.g.first : nullptr, g.tokens});
 }
 
@@ -158,40 +163,61 @@ grouped_rows(ProductArgs args, GroupArgs g) {
     rows_tile<ET, B_N, DUAL, SEG, REG, BM, BN, WM, WN, S, DEEP, KG, TAIL, GATHER>(args, g, blockIdx.x, (SPG_LDS char*)lds);
 }
 
-// The parts of the last round's tiles added, and the epilogue: 16 workgroups a tile, each of
-// whose waves adds some of the accumulators of the tile's waves, 16 rows x 16 columns a time.
-constexpr int kJoin = 16;
-template <int ET, bool DUAL, bool SEG>
+// The parts of the last round's tiles added, and the epilogue: a workgroup for every 4096 of a
+// tile's elements, each of whose waves adds some of the accumulators of the tile's waves, 16 rows x
+// 16 columns a time.
+template <int ET, bool DUAL, bool SEG, int BM, int BN, int WM, int WN>
 __global__ void __launch_bounds__(256) grouped_join(ProductArgs args, GroupArgs g) {
-    constexpr int WM = DUAL ? 64 : 128, WN = DUAL ? 128 : 64;      // the 256x256 tile of grouped_launch.hpp
-    using G = ProductGeom<DUAL, 256, 256, WM, WN, 2, false, 1>;
-    constexpr int UNITS = (DUAL ? G::TN / 2 : G::TN) * G::TM, EACH = G::NW * UNITS / (kJoin * 4);
+    using G = ProductGeom<DUAL, BM, BN, WM, WN, 2, false, 1>;
+    constexpr int JOIN = BM * BN / 4096;
+    constexpr int UNITS = (DUAL ? G::TN / 2 : G::TN) * G::TM, EACH = G::NW * UNITS / (JOIN * 4);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int tiles = all_units<256>(g, lane) * args.tiles_n;
-    const LastRound last = last_round(tiles, (args.K + 63) / 64 * (SEG ? 2 : 1));
-    const int t = blockIdx.x / kJoin;
+    const int tiles = all_units<BM>(g, lane) * args.tiles_n;
+    const LastRound last = last_round<BM, BN>(tiles, (args.K + 63) / 64 * (SEG ? 2 : 1));
+    const int t = blockIdx.x / JOIN;
     if (last.parts == 1 || t >= tiles - last.full) return;
     const int at = last.full + t, u = at / args.tiles_n;
-    const Found f = find_unit<256>(g, u, lane);
-    const int mine = (f.g.n + 255) / 256, in = (mine + args.group_m - 1) / args.group_m;
+    const Found f = find_unit<BM>(g, u, lane);
+    const int mine = (f.g.n + BM - 1) / BM, in = (mine + args.group_m - 1) / args.group_m;
     int tm, tn;
     raster(at - (u - f.unit) * args.tiles_n, mine, args.tiles_n, (mine + in - 1) / in, tm, tn);
-    const float* part = g.part + (size_t)t * last.parts * 65536;
+    // four parts' loads of all of a wave's accumulators under way at once: one by one their latencies
+    // are most of this kernel
+    constexpr int NM = DUAL ? 2 : 1, UP = UNITS * 256;              // UP: to the up projection's accumulators
+    const float* part = g.part + (size_t)t * last.parts * BM * BN;
+    auto own = [&](int i) { return ((blockIdx.x % JOIN) * 4 + wave) * EACH + i; };
+    auto load = [&](int k, int i, int h) __attribute__((always_inline)) {
+        const int q = own(i), w = q / UNITS, j = q % UNITS;
+        return *(const floatx4*)(part + (size_t)k * BM * BN + ((w * G::TN * G::TM + j) * 64 + lane) * 4 + h * UP);
+    };
+    floatx4 s[EACH][NM];
+#pragma unroll
+    for (int i = 0; i < EACH; ++i)
+#pragma unroll
+        for (int h = 0; h < NM; ++h) s[i][h] = load(0, i, h);
+    for (int k0 = 1; k0 < last.parts; k0 += 4) {
+        floatx4 v[4][EACH][NM];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int i = 0; i < EACH; ++i)
+#pragma unroll
+                for (int h = 0; h < NM; ++h) v[u][i][h] = load(k0 + u < last.parts ? k0 + u : last.parts - 1, i, h);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (k0 + u < last.parts)
+#pragma unroll
+                for (int i = 0; i < EACH; ++i)
+#pragma unroll
+                    for (int h = 0; h < NM; ++h) s[i][h] += v[u][i][h];
+    }
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
-        const int q = ((blockIdx.x % kJoin) * 4 + wave) * EACH + i, w = q / UNITS, j = q % UNITS;
-        const int m = tm * 256 + w / G::WAVES_N * WM + j % G::TM * 16 + (lane & 15);
+        const int q = own(i), w = q / UNITS, j = q % UNITS;
+        const int m = tm * BM + w / G::WAVES_N * WM + j % G::TM * 16 + (lane & 15);
         const int n = tn * G::BNS + w % G::WAVES_N * G::WNS + j / G::TM * 16 + 4 * (lane >> 4);
-        if (m >= f.g.n || n >= args.N) continue;
-        const float* p = part + ((w * G::TN * G::TM + j) * 64 + lane) * 4;
-        floatx4 s0 = *(const floatx4*)p, s1 = s0;
-        constexpr int UP = DUAL ? UNITS * 256 : 0;                  // the up projection's accumulators
-        if (DUAL) s1 = *(const floatx4*)(p + UP);
-        for (int k = 1; k < last.parts; ++k) {
-            s0 += *(const floatx4*)(p + (size_t)k * 65536);
-            if (DUAL) s1 += *(const floatx4*)(p + (size_t)k * 65536 + UP);
-        }
-        finish4<ET, DUAL>(s0, s1, 0, n, args.N - n < 4 ? args.N - n : 4, (size_t)(f.g.first + m) * args.N + n, args);
+        if (m < f.g.n && n < args.N)
+            finish4<ET, DUAL>(s[i][0], s[i][NM - 1], 0, n, args.N - n < 4 ? args.N - n : 4, (size_t)(f.g.first + m) * args.N + n, args);
     }
 }
 

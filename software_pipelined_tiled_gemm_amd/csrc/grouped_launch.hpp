@@ -31,8 +31,8 @@ constexpr int group_tile_n(int tile, int mats) { return kTileN[tile == kTileThin
 template <int ET, int P, bool REG, bool GATHER>
 void launch_grouped(int tile, const ProductArgs& a, const GroupArgs& g, int per, dim3 grid, hipStream_t st);
 
-// The sums of the last round's parts (tile Big)
-constexpr int64_t kPartBytes = (int64_t)kRound * 256 * 256 * 4;
+// The sums of the last round's parts
+constexpr int64_t part_bytes(int tile) { return (int64_t)kRound * kGroupTileM[tile] * group_tile_n(tile, 1) * 4; }
 
 // dX and dW in one launch (tiles Mid and Small); P: kRowsSumNK, kRowsSumKN, kRowsNK or kRowsKN
 template <int ET, int P, bool REG>

@@ -830,7 +830,6 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, int tm, int tn
     // ---- epilogue ----
     const int m_base = m0 + wm * WM, n_base = n0 + wn * WNS;
     if constexpr (LOCAL) {
-        static_assert(KG == 1, "one accumulator a wave");
         if (args.part) {
             float* to = args.part + (size_t)wave * TN * TM * 256 + lane * 4;
             if (!(SKIP && idle))

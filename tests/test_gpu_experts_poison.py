@@ -21,6 +21,9 @@ CASES = {
     "tall": ([600, 1000, 0, 515], 2050, 1024, None),
     "big": ([1024, 1300, 700, 1111], 2048, 2304, 1500),
     "parts": ([1300, 1100, 0, 900], 2304, 4160, None),
+    "long": ([30, 1, 0, 64], 136, 5000, 70),                        # few tiles, split along the sum
+    "longer": ([9, 100, 33], 6000, 72, None),                       # the input gradient's
+    "odd and long": ([9, 100, 33], 77, 4001, None),
     "short": ([40, 1, 64, 65, 100, 129, 256] * 6, 2048, 2048, None),   # gradients: reductions of one to four k-tiles
 }
 
