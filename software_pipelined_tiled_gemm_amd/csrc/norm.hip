@@ -433,8 +433,15 @@ gemm_status gemm_norm_create(gemm_norm_handle* out, int64_t rows, int64_t K, gem
     if (p->waves) {
         p->ept = K <= 64 * 8 * p->waves ? 8 : 16;
         const int64_t teams = p->waves == 1 ? (rows + 3) / 4 : rows;
-        p->wgs = std::min<int64_t>(teams, p->waves == 16 ? 512 : 2048);
-        p->back_wgs = std::min<int64_t>(teams, p->waves == 16 ? 256 : 512);
+        // about as many as the CUs hold at once: each takes the next row as it ends one (8192 x 4096,
+        // forward: 27.0 us with 1024, 29.7 with 2048, 38.6 with a workgroup a row; 2048 x 16384: 29.7
+        // with 256, 33.5 with 512; 16384 x 1536, 8 values a thread: 22.7 with 2048, 26.7 with 1024)
+        p->wgs = std::min<int64_t>(teams, (p->waves == 16 ? 512 : 2048) / (p->ept == 16 ? 2 : 1));
+        // each writes its sums of the parameters' gradients; up to 1024 of short rows, if it has eight of
+        // them or more (both passes of 16384 x 1536: 60.2 us with 1024, 70.4 with 512; of 8192 x 4096,
+        // 16 values a thread, 77.5 and 73.9)
+        const int64_t most = p->ept == 16 ? 512 : std::max<int64_t>(512, std::min<int64_t>(1024, teams / 8));
+        p->back_wgs = std::min<int64_t>(teams, p->waves == 16 ? 256 : most);
     }
     *out = p;
     return GEMM_OK;
