@@ -127,6 +127,7 @@ struct Choice {
     int tile;     // -1: no class has few enough workgroups for a launch
     double us;    // estimated
     bool split;   // the last round's tiles (a grid of less than a round: all of them) in parts
+    int parts;    // of the rows, for the matrices' gradients
 };
 
 // A launch has less than 2^32 threads, a workgroup up to 512.
@@ -148,26 +149,29 @@ double rows_wgs(const RowsShape& s, int t) {
 // groups, 1 to 2048 rows, matrices of 32 to 2048 columns and reductions of 1024 to 12288) the best
 // class with parts takes 0.27 to 1 of the time of the best without (5 columns of 736, 9728:
 // 13 and 37 us), and the choice 4.6% more than the best on average.
+// The matrices' gradients likewise (12432 rows of one group, 144 x 776, both gradients: 33 us, 77
+// in one piece).
 constexpr double kJoinUs[spg::kGroupTiles] = {0, 0, 0, 4.5, 4.0, 0, 3.5};   // the parts' launch, write and read; 0: not split
-double split_us(const RowsShape& s, const Cost& c, int t, double wgs) {
-    if (kJoinUs[t] == 0) return 1e30;
+double split_us(const Cost& c, int t, double wgs, double all, double bytes, double& parts) {
     const int bm = spg::kGroupTileM[t], bn = spg::group_tile_n(t, 1);
-    const double parts = std::min((double)spg::most_parts(bm, bn), std::floor(spg::kRound / wgs));
-    if (parts < 2.0) return 1e30;
-    const double kt = std::ceil((double)s.kt / parts);
-    if ((double)s.kt - kt < spg::split_gain(bm, bn)) return 1e30;
-    return kJoinUs[t] + cost_us(c, std::min(1.0, wgs * parts / spg::kRound), kt, s.bytes);
+    parts = std::min((double)spg::most_parts(bm, bn), std::floor(spg::kRound / wgs));
+    if (kJoinUs[t] == 0 || parts < 2.0) return 1e30;
+    const double kt = std::ceil(all / parts);
+    if (all - kt < spg::split_gain(bm, bn)) return 1e30;
+    return kJoinUs[t] + cost_us(c, std::min(1.0, wgs * parts / spg::kRound), kt, bytes);
 }
 
 Choice choose_rows(const RowsShape& s, bool reg) {
-    Choice best{-1, 1e30, false};
+    Choice best{-1, 1e30, false, 1};
     for (int t = 0; t < spg::kGroupTiles; ++t) {
         const Cost& c = kRows[reg][s.mats == 2][t];
         if (c.bw == 0 || most_wgs(s.rows, s.live, s.N, t, s.mats) > kMostWgs) continue;
-        const double wgs = rows_wgs(s, t), us = cost_us(c, wgs / slots(t, reg), (double)s.kt, s.bytes), parts = split_us(s, c, t, wgs);
+        double n;
+        const double wgs = rows_wgs(s, t), us = cost_us(c, wgs / slots(t, reg), (double)s.kt, s.bytes);
+        const double parts = split_us(c, t, wgs, (double)s.kt, s.bytes, n);
         const bool last = t == spg::kTileBig && s.kt >= 2 * spg::split_gain(256, 256) && wgs <= 12.0 * spg::kRound;
-        if (us < best.us) best = Choice{t, us, last};
-        if (parts < best.us) best = Choice{t, parts, true};
+        if (us < best.us) best = Choice{t, us, last, 1};
+        if (parts < best.us) best = Choice{t, parts, true, 1};
     }
     return best;
 }
@@ -189,12 +193,15 @@ double weights_wgs(const WeightsShape& s, int t) {
 bool too_many(const WeightsShape& s, int t) { return weights_wgs(s, t) + 8.0 * s.groups > (double)kMostWgs; }
 
 Choice choose_weights(const WeightsShape& s, bool reg) {
-    Choice best{-1, 1e30, false};
+    Choice best{-1, 1e30, false, 1};
     for (int t = 0; t < spg::kTiles; ++t) {
         const Cost& c = kWeights[reg][t];
         if (c.bw == 0 || too_many(s, t)) continue;
-        const double us = cost_us(c, weights_wgs(s, t) / slots(t, reg), s.kt, s.bytes);
-        if (us < best.us) best = Choice{t, us, false};
+        double n;
+        const double wgs = weights_wgs(s, t), us = cost_us(c, wgs / slots(t, reg), s.kt, s.bytes);
+        const double parts = split_us(c, t, wgs, s.kt, s.bytes, n);
+        if (us < best.us) best = Choice{t, us, false, 1};
+        if (parts < best.us) best = Choice{t, parts, false, (int)n};
     }
     return best;
 }
@@ -277,7 +284,7 @@ uint8_t raster_rows(int64_t rows) { return (uint8_t)(rows <= 8 ? std::max<int64_
 int64_t most_part_bytes(const Choice* c) {
     int64_t most = 0;
     for (int r = 0; r < 2; ++r)
-        if (c[r].split) most = std::max(most, spg::part_bytes(c[r].tile));
+        if (c[r].split || c[r].parts > 1) most = std::max(most, spg::part_bytes(c[r].tile));
     return most;
 }
 
@@ -378,12 +385,27 @@ int64_t weights_grid(int tile, ProductArgs& w) {
     w.tiles_m = (int32_t)ceil_div(w.M, spg::kTileM[tile]);
     w.tiles_n = (int32_t)ceil_div(w.N, spg::kTileN[tile]);
     w.group_m = raster_rows((int64_t)w.tiles_m * w.zm);
-    return up((int64_t)w.tiles_m * w.zm * w.tiles_n * w.zn, 8);
+    return up((int64_t)w.tiles_m * w.zm * w.tiles_n * w.zn * w.split, 8);
 }
 
-gemm_status run_weights(const Common& c, bool reg, int tile, ProductArgs w, const int32_t* offsets, hipStream_t st) {
-    const int64_t per = weights_grid(tile, w);
-    launch_any(spg::kGroupWeights, c.bf, reg, tile, w, group_args(c, offsets, nullptr), (int)per, dim3((unsigned)(per * c.groups)), st);
+template <int BM, int BN, int WM, int WN>
+void launch_weights_join(bool bf, const ProductArgs& w, const GroupArgs& g, hipStream_t st) {
+    const dim3 grid((unsigned)(g.groups * w.tiles_m * w.zm * w.tiles_n * w.zn * (BM * BN / 4096)));
+    if (bf) hipLaunchKernelGGL((spg::weights_join<spg::kElBF16, BM, BN, WM, WN>), grid, dim3(256), 0, st, w, g);
+    else hipLaunchKernelGGL((spg::weights_join<spg::kElF16, BM, BN, WM, WN>), grid, dim3(256), 0, st, w, g);
+}
+
+gemm_status run_weights(const Common& c, bool reg, const Choice& choice, ProductArgs w, const int32_t* offsets, void* parts,
+                        hipStream_t st) {
+    w.split = choice.parts;
+    const int64_t per = weights_grid(choice.tile, w);
+    GroupArgs g = group_args(c, offsets, nullptr);
+    g.part = (float*)parts;
+    launch_any(spg::kGroupWeights, c.bf, reg, choice.tile, w, g, (int)per, dim3((unsigned)(per * c.groups)), st);
+    const gemm_status e = launched();
+    if (e != GEMM_OK || choice.parts == 1) return e;
+    if (choice.tile == spg::kTileSmall) launch_weights_join<64, 128, 32, 64>(c.bf, w, g, st);
+    else launch_weights_join<64, 64, 32, 64>(c.bf, w, g, st);
     return launched();
 }
 
@@ -405,7 +427,7 @@ gemm_status run_gradients(int product, const Common& c, bool regx, bool regw, co
         return launched();
     }
     const gemm_status e = run_rows(product, c, regx, dx[regx], 1, x, offsets, nullptr, parts, st);
-    return e != GEMM_OK ? e : run_weights(c, regw, dw[regw].tile, w, offsets, st);
+    return e != GEMM_OK ? e : run_weights(c, regw, dw[regw], w, offsets, parts, st);
 }
 
 template <bool BF16, bool DUAL>
@@ -527,7 +549,8 @@ gemm_status gemm_grouped_create(gemm_grouped_handle* out, int64_t rows, int64_t 
         p->fwd[r] = choose_rows(fwd, r == 1);
         p->dx[r] = choose_rows(dx, r == 1);
         p->dw[r] = choose_weights(dw, r == 1);
-        p->both[r] = choose_both(dx, dw, r == 1, p->dx[r].us + p->dw[r].us);
+        // rows in parts need a launch of their own (12785 rows of 7 groups, 113 x 137: 25 us, 52 in one launch)
+        p->both[r] = p->dw[r].parts > 1 ? -1 : choose_both(dx, dw, r == 1, p->dx[r].us + p->dw[r].us);
         p->simple |= p->fwd[r].tile < 0;
         p->simple_back |= p->dx[r].tile < 0 || p->dw[r].tile < 0;
     }
@@ -538,7 +561,8 @@ gemm_status gemm_grouped_create(gemm_grouped_handle* out, int64_t rows, int64_t 
     p->ws_run = p->simple || p->stream || !p->gather ? 0 : c.gathered();
     p->part_run = section(!p->simple && !p->stream, most_part_bytes(p->fwd), p->ws_run);
     p->ws_back = p->simple_back ? 0 : c.gathered();
-    p->part_back = section(!p->simple_back && !p->stream_back, most_part_bytes(p->dx), p->ws_back);
+    // dX's and dW's one after the other
+    p->part_back = section(!p->simple_back, std::max(p->stream_back ? 0 : most_part_bytes(p->dx), most_part_bytes(p->dw)), p->ws_back);
     *out = p;
     return GEMM_OK;
 }
@@ -625,7 +649,7 @@ gemm_status gemm_grouped_backward(gemm_grouped_handle h, const void* dY, const v
     if (rows)
         e = h->stream_back ? run_stream(c, false, a, offsets, nullptr, stream)
                            : run_rows(product, c, regx, h->dx[regx], 1, a, offsets, nullptr, at(workspace, h->part_back), stream);
-    return e != GEMM_OK || !weights ? e : run_weights(c, regw, h->dw[regw].tile, w, offsets, stream);
+    return e != GEMM_OK || !weights ? e : run_weights(c, regw, h->dw[regw], w, offsets, at(workspace, h->part_back), stream);
 }
 
 gemm_status gemm_grouped_destroy(gemm_grouped_handle h) {
@@ -654,7 +678,8 @@ gemm_status gemm_experts_create(gemm_experts_handle* out, int64_t rows, int64_t 
         p->fwd[r] = choose_rows(fwd, r == 1);
         p->dx[r] = choose_rows(dx, r == 1);
         p->dw[r] = choose_weights(dw, r == 1);
-        p->both[r] = choose_both(dx, dw, r == 1, p->dx[r].us + p->dw[r].us);
+        // rows in parts need a launch of their own (12785 rows of 7 groups, 113 x 137: 25 us, 52 in one launch)
+        p->both[r] = p->dw[r].parts > 1 ? -1 : choose_both(dx, dw, r == 1, p->dx[r].us + p->dw[r].us);
         p->simple |= p->fwd[r].tile < 0;
         p->simple_back |= p->dx[r].tile < 0 || p->dw[r].tile < 0;
     }
@@ -665,7 +690,7 @@ gemm_status gemm_experts_create(gemm_experts_handle* out, int64_t rows, int64_t 
     p->part_run = section(!p->simple && !p->stream, most_part_bytes(p->fwd), p->ws_run);
     p->off_x = up(rows * p->np * 4, kAlign);
     p->ws_back = p->off_x + (p->simple_back ? 0 : c.gathered());
-    p->part_back = section(!p->simple_back, most_part_bytes(p->dx), p->ws_back);
+    p->part_back = section(!p->simple_back, std::max(most_part_bytes(p->dx), most_part_bytes(p->dw)), p->ws_back);
     *out = p;
     return GEMM_OK;
 }

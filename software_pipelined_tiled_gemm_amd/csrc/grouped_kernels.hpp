@@ -163,29 +163,18 @@ grouped_rows(ProductArgs args, GroupArgs g) {
     rows_tile<ET, B_N, DUAL, SEG, REG, BM, BN, WM, WN, S, DEEP, KG, TAIL, GATHER>(args, g, blockIdx.x, (SPG_LDS char*)lds);
 }
 
-// The parts of the last round's tiles added, and the epilogue: a workgroup for every 4096 of a
-// tile's elements, each of whose waves adds some of the accumulators of the tile's waves, 16 rows x
-// 16 columns a time.
-template <int ET, bool DUAL, bool SEG, int BM, int BN, int WM, int WN>
-__global__ void __launch_bounds__(256) grouped_join(ProductArgs args, GroupArgs g) {
+// The parts of a tile added: 4096 of its elements by each workgroup (`blk` of the tile's), each of
+// whose waves adds some of the accumulators of the tile's waves, 16 rows x 16 columns a time;
+// put(row, column, sums of four columns from there).
+template <bool DUAL, int BM, int BN, int WM, int WN, typename F>
+__device__ __forceinline__ void join_parts(const float* part, int parts, int blk, F&& put) {
     using G = ProductGeom<DUAL, BM, BN, WM, WN, 2, false, 1>;
-    constexpr int JOIN = BM * BN / 4096;
-    constexpr int UNITS = (DUAL ? G::TN / 2 : G::TN) * G::TM, EACH = G::NW * UNITS / (JOIN * 4);
+    constexpr int UNITS = (DUAL ? G::TN / 2 : G::TN) * G::TM, EACH = G::NW * UNITS / (BM * BN / 4096 * 4);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int tiles = all_units<BM>(g, lane) * args.tiles_n;
-    const LastRound last = last_round<BM, BN>(tiles, (args.K + 63) / 64 * (SEG ? 2 : 1));
-    const int t = blockIdx.x / JOIN;
-    if (last.parts == 1 || t >= tiles - last.full) return;
-    const int at = last.full + t, u = at / args.tiles_n;
-    const Found f = find_unit<BM>(g, u, lane);
-    const int mine = (f.g.n + BM - 1) / BM, in = (mine + args.group_m - 1) / args.group_m;
-    int tm, tn;
-    raster(at - (u - f.unit) * args.tiles_n, mine, args.tiles_n, (mine + in - 1) / in, tm, tn);
     // four parts' loads of all of a wave's accumulators under way at once: one by one their latencies
-    // are most of this kernel
+    // are most of the time
     constexpr int NM = DUAL ? 2 : 1, UP = UNITS * 256;              // UP: to the up projection's accumulators
-    const float* part = g.part + (size_t)t * last.parts * BM * BN;
-    auto own = [&](int i) { return ((blockIdx.x % JOIN) * 4 + wave) * EACH + i; };
+    auto own = [&](int i) { return (blk * 4 + wave) * EACH + i; };
     auto load = [&](int k, int i, int h) __attribute__((always_inline)) {
         const int q = own(i), w = q / UNITS, j = q % UNITS;
         return *(const floatx4*)(part + (size_t)k * BM * BN + ((w * G::TN * G::TM + j) * 64 + lane) * 4 + h * UP);
@@ -195,17 +184,17 @@ __global__ void __launch_bounds__(256) grouped_join(ProductArgs args, GroupArgs 
     for (int i = 0; i < EACH; ++i)
 #pragma unroll
         for (int h = 0; h < NM; ++h) s[i][h] = load(0, i, h);
-    for (int k0 = 1; k0 < last.parts; k0 += 4) {
+    for (int k0 = 1; k0 < parts; k0 += 4) {
         floatx4 v[4][EACH][NM];
 #pragma unroll
         for (int u = 0; u < 4; ++u)
 #pragma unroll
             for (int i = 0; i < EACH; ++i)
 #pragma unroll
-                for (int h = 0; h < NM; ++h) v[u][i][h] = load(k0 + u < last.parts ? k0 + u : last.parts - 1, i, h);
+                for (int h = 0; h < NM; ++h) v[u][i][h] = load(k0 + u < parts ? k0 + u : parts - 1, i, h);
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-            if (k0 + u < last.parts)
+            if (k0 + u < parts)
 #pragma unroll
                 for (int i = 0; i < EACH; ++i)
 #pragma unroll
@@ -214,26 +203,70 @@ __global__ void __launch_bounds__(256) grouped_join(ProductArgs args, GroupArgs 
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
         const int q = own(i), w = q / UNITS, j = q % UNITS;
-        const int m = tm * BM + w / G::WAVES_N * WM + j % G::TM * 16 + (lane & 15);
-        const int n = tn * G::BNS + w % G::WAVES_N * G::WNS + j / G::TM * 16 + 4 * (lane >> 4);
-        if (m < f.g.n && n < args.N)
-            finish4<ET, DUAL>(s[i][0], s[i][NM - 1], 0, n, args.N - n < 4 ? args.N - n : 4, (size_t)(f.g.first + m) * args.N + n, args);
+        put(w / G::WAVES_N * WM + j % G::TM * 16 + (lane & 15), w % G::WAVES_N * G::WNS + j / G::TM * 16 + 4 * (lane >> 4), s[i][0],
+            s[i][NM - 1]);
     }
+}
+
+// The parts of the last round's tiles added, and the epilogue.
+template <int ET, bool DUAL, bool SEG, int BM, int BN, int WM, int WN>
+__global__ void __launch_bounds__(256) grouped_join(ProductArgs args, GroupArgs g) {
+    using G = ProductGeom<DUAL, BM, BN, WM, WN, 2, false, 1>;
+    constexpr int JOIN = BM * BN / 4096;
+    const int lane = threadIdx.x & 63;
+    const int tiles = all_units<BM>(g, lane) * args.tiles_n;
+    const LastRound last = last_round<BM, BN>(tiles, (args.K + 63) / 64 * (SEG ? 2 : 1));
+    const int t = blockIdx.x / JOIN;
+    if (last.parts == 1 || t >= tiles - last.full) return;
+    const int at = last.full + t, u = at / args.tiles_n;
+    const Found f = find_unit<BM>(g, u, lane);
+    const int mine = (f.g.n + BM - 1) / BM, in = (mine + args.group_m - 1) / args.group_m;
+    int tm, tn;
+    raster(at - (u - f.unit) * args.tiles_n, mine, args.tiles_n, (mine + in - 1) / in, tm, tn);
+    join_parts<DUAL, BM, BN, WM, WN>(
+        g.part + (size_t)t * last.parts * BM * BN, last.parts, blockIdx.x % JOIN,
+        [&](int row, int col, const floatx4& s0, const floatx4& s1) __attribute__((always_inline)) {
+            const int m = tm * BM + row, n = tn * G::BNS + col;
+            if (m < f.g.n && n < args.N)
+                finish4<ET, DUAL>(s0, s1, 0, n, args.N - n < 4 ? args.N - n : 4, (size_t)(f.g.first + m) * args.N + n, args);
+        });
 }
 
 // The weights' gradients of every group: the reduction runs over the group's rows.  `per`
 // workgroups a group (a multiple of 8), so that every group's tiles are spread over all XCDs
-// whatever its rows.  A group without rows writes zeros.
+// whatever its rows.  A group without rows writes zeros.  args.split: parts that a group's rows are
+// taken in, as far as it has k-tiles for them, joined by weights_join; few small matrices and
+// many rows leave CUs idle otherwise.
+struct RowParts {
+    int parts, kt_part;
+};
+__device__ __forceinline__ RowParts row_parts(int n, int split) {
+    const int kt = (n + 63) / 64, kt_part = (kt + split - 1) / split;
+    return RowParts{kt_part > 0 ? (kt + kt_part - 1) / kt_part : 1, kt_part};
+}
+
 template <int ET, bool REG, int BM, int BN, int WM, int WN, int S, bool DEEP, int KG>
 __device__ __forceinline__ void weights_tile(ProductArgs args, const GroupArgs& g, int per, int wg, SPG_LDS char* lds) {
     using G = ProductGeom<false, BM, BN, WM, WN, S, DEEP, KG>;
     const int e = wg / per;
     const int rows = args.tiles_m * args.zm, cols = args.tiles_n * args.zn;
-    const int at = xcd_place(wg - e * per, rows * cols);
+    constexpr bool SPLIT = BM == 64;                  // the classes that the host splits
+    int at = xcd_place(wg - e * per, rows * cols * (SPLIT ? args.split : 1)), sp = 0;
     if (at < 0) return;
+    const Group gr = group_of(g, e);
+    args.part = nullptr;
+    if constexpr (SPLIT) {
+        sp = at / (rows * cols);
+        at -= sp * rows * cols;
+        const RowParts p = row_parts(gr.n, args.split);
+        if (sp >= p.parts) return;
+        if (p.parts > 1) {
+            args.part = g.part + (((size_t)e * rows * cols + at) * args.split + sp) * BM * BN;
+            args.kt_part = p.kt_part;
+        }
+    }
     int tm, tn;
     raster(at, rows, cols, args.group_m, tm, tn);
-    const Group gr = group_of(g, e);
     args.C = (char*)args.C + (size_t)e * g.b_step;
     if (args.zm == 2 || args.zn == 2) args.C1 = (char*)args.C1 + (size_t)e * g.b_step;
     if (gr.n == 0) {
@@ -256,8 +289,30 @@ __device__ __forceinline__ void weights_tile(ProductArgs args, const GroupArgs& 
     args.B[0] += (size_t)gr.first * args.ldb;
     if (args.zn == 2) args.B[1] += (size_t)gr.first * args.ldb;
     args.K = gr.n;
-    args.part = nullptr;
-    product_tile_of<ET, true, true, false, false, REG, BM, BN, WM, WN, S, DEEP, KG, false>(args, tm, tn, 0, lds);
+    product_tile_of<ET, true, true, false, false, REG, BM, BN, WM, WN, S, DEEP, KG, false, false, false, SPLIT>(args, tm, tn, sp, lds);
+}
+
+// The parts of the gradients' tiles added: a workgroup for every 4096 elements of every group's tiles.
+template <int ET, int BM, int BN, int WM, int WN>
+__global__ void __launch_bounds__(256) weights_join(ProductArgs args, GroupArgs g) {
+    constexpr int JOIN = BM * BN / 4096;
+    const int rows = args.tiles_m * args.zm, cols = args.tiles_n * args.zn;
+    const int t = blockIdx.x / JOIN, e = t / (rows * cols);
+    const RowParts p = row_parts(group_of(g, e).n, args.split);
+    if (p.parts == 1) return;
+    int tm, tn, z = 0;
+    raster(t - e * rows * cols, rows, cols, args.group_m, tm, tn);
+    if (tm >= args.tiles_m) { tm -= args.tiles_m; z = 1; }
+    if (tn >= args.tiles_n) { tn -= args.tiles_n; z = 1; }
+    args.C = (char*)args.C + (size_t)e * g.b_step;
+    if (z) args.C1 = (char*)args.C1 + (size_t)e * g.b_step;
+    join_parts<false, BM, BN, WM, WN>(
+        g.part + (size_t)t * args.split * BM * BN, p.parts, blockIdx.x % JOIN,
+        [&](int row, int col, const floatx4& s, const floatx4&) __attribute__((always_inline)) {
+            const int m = tm * BM + row, n = tn * BN + col;
+            if (m < args.M && n < args.N)
+                finish4<ET, false>(s, s, 0, n, args.N - n < 4 ? args.N - n : 4, (size_t)m * args.N + n, args, z);
+        });
 }
 
 template <int ET, bool REG, int BM, int BN, int WM, int WN, int S, bool DEEP, int KG, int WPS>

@@ -24,6 +24,8 @@ CASES = {
     "long": ([30, 1, 0, 64], 136, 5000, 70),                        # few tiles, split along the sum
     "longer": ([9, 100, 33], 6000, 72, None),                       # the input gradient's
     "odd and long": ([9, 100, 33], 77, 4001, None),
+    "rows": ([3000, 0, 1700, 5], 72, 136, 300),                     # few matrices, split along the rows
+    "odd rows": ([9000, 100], 33, 65, None),
     "short": ([40, 1, 64, 65, 100, 129, 256] * 6, 2048, 2048, None),   # gradients: reductions of one to four k-tiles
 }
 
