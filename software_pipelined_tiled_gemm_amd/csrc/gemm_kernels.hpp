@@ -148,24 +148,21 @@ __device__ __forceinline__ void dma16(const i32x4& rsrc, SPG_LDS char* lds_dst, 
 // misaligned-operand copy mode loads from a shifted window, and zeroes the elements of
 // the window that lie outside the operand's valid range in the same step.
 // Whole words are moved by selects (v_cndmask, no branches around per-lane conditions), the
-// bytes within a word by v_alignbyte.  Not with 64-bit shifts: v_lshlrev_b64 by a lane's own
-// amount, twice in a row, now and then left the first shift's result in the register (products
-// of 32-row groups by the streaming kernel, K % 8 = 6: 0.5% of the outputs wrong, others from
-// run to run; none with a wait between the two, none in this form).
+// bytes within a word by v_perm and v_alignbyte.  Every value has a name of its own: an array of
+// words here once made the compiler keep a staged k-tile (stage_regs) in scratch memory, all of it
+// (fp16 3000x5000x1001 -> fp32: 72 us, 41 as here).
+// Not with 64-bit shifts: as two v_lshlrev_b64 by a lane's own amount one after the other, some
+// products of the streaming kernel (32-row groups, K % 8 = 6) came out wrong in 0.5% of the
+// outputs, others from run to run, with the pattern of the first shift's result in place of the
+// second's.  They did not with a wait between the two, nor in this form; why is not known.
 __device__ __forceinline__ u32x4 shl128(u32x4 v, uint32_t bits) {
-    // as 256 bits, zeros below v, shifted down by 128 - bits (8 .. 128)
-    const uint32_t down = 128u - bits, bytes = down >> 3;   // alignbyte reads the low two bits
-    const bool one = down & 32u, two = down & 64u, four = down & 128u;
-    const uint32_t w[12] = {0u, 0u, 0u, 0u, v.x, v.y, v.z, v.w, 0u, 0u, 0u, 0u};
-    uint32_t a[11], b[9], c[5];
-#pragma unroll
-    for (int e = 0; e < 11; ++e) a[e] = one ? w[e + 1] : w[e];
-#pragma unroll
-    for (int e = 0; e < 9; ++e) b[e] = two ? a[e + 2] : a[e];
-#pragma unroll
-    for (int e = 0; e < 5; ++e) c[e] = four ? b[e + 4] : b[e];
-    return u32x4{__builtin_amdgcn_alignbyte(c[1], c[0], bytes), __builtin_amdgcn_alignbyte(c[2], c[1], bytes),
-                 __builtin_amdgcn_alignbyte(c[3], c[2], bytes), __builtin_amdgcn_alignbyte(c[4], c[3], bytes)};
+    const bool one = bits & 32u, two = bits & 64u;
+    const uint32_t a0 = one ? 0u : v.x, a1 = one ? v.x : v.y, a2 = one ? v.y : v.z, a3 = one ? v.z : v.w;
+    const uint32_t b0 = two ? 0u : a0, b1 = two ? 0u : a1, b2 = two ? a0 : a2, b3 = two ? a1 : a3;
+    // bytes 4 - n .. 7 - n of a word and the one below it, n = bits / 8 % 4
+    const uint32_t pick = 0x07060504u - (bits >> 3 & 3u) * 0x01010101u;
+    return u32x4{__builtin_amdgcn_perm(b0, 0u, pick), __builtin_amdgcn_perm(b1, b0, pick),
+                 __builtin_amdgcn_perm(b2, b1, pick), __builtin_amdgcn_perm(b3, b2, pick)};
 }
 
 __device__ __forceinline__ u32x4 shr128(u32x4 v, uint32_t bits) {
