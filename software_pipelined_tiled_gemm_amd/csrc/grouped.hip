@@ -32,10 +32,10 @@ gemm_status launched() {
     return e == hipSuccess ? GEMM_OK : spg::hip_fail(e);
 }
 
-// a launch has less than 2^32 threads along one axis
+// a launch has less than 2^32 threads along one axis, and one workgroup at least
 dim3 spread(int64_t wgs) {
-    const int64_t x = std::min<int64_t>(wgs, 1 << 21);
-    return dim3((unsigned)x, (unsigned)ceil_div(wgs, x));
+    const int64_t x = std::min<int64_t>(std::max<int64_t>(wgs, 1), 1 << 21);
+    return dim3((unsigned)x, (unsigned)std::max<int64_t>(ceil_div(wgs, x), 1));
 }
 
 // Rows of operands are addressed by 32-bit offsets below 2^31: 256 of them fit up to here.
@@ -632,7 +632,7 @@ gemm_status gemm_grouped_backward(gemm_grouped_handle h, const void* dY, const v
     }
     const char* x = (const char*)X;
     int64_t ldx = c.K * 2, cols = c.K;
-    if (weights && source) {
+    if (weights && source && c.rows > 0) {   // without rows a source may be given, and nothing is read
         const gemm_status e = run_gather(c, X, source, workspace, stream);
         if (e != GEMM_OK) return e;
         x = (const char*)workspace;

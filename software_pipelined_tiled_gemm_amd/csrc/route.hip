@@ -487,10 +487,10 @@ gemm_status launched() {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// a launch has less than 2^32 threads along one axis
+// a launch has less than 2^32 threads along one axis, and one workgroup at least
 dim3 spread(int64_t wgs) {
-    const int64_t x = std::min<int64_t>(wgs, 1 << 21);
-    return dim3((unsigned)x, (unsigned)ceil_div(wgs, x));
+    const int64_t x = std::min<int64_t>(std::max<int64_t>(wgs, 1), 1 << 21);
+    return dim3((unsigned)x, (unsigned)std::max<int64_t>(ceil_div(wgs, x), 1));
 }
 
 // f(element type as a constant)
