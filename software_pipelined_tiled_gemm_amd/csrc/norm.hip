@@ -5,6 +5,11 @@
 //
 // The mean is taken off before the squares are summed: the variance of a row far from zero
 // keeps its bits, which sum x^2 - mean^2 would lose.
+//
+// Rows of very large finite values (a deviation of 2^64, a sum of 2^128; not in fp16) take these sums
+// past fp32's range.  Their variance shows it, and they are taken once more as x / 2^80.  As a branch
+// of its own that costs the other rows one comparison (forward, 8192 x 4096: 27.5 us, 27.3 without;
+// 16384 x 1536: 23.4 and 23.3, against 24.8 with a factor in every row's arithmetic).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -40,6 +45,48 @@ struct NormArgs {
     float eps;
 };
 
+constexpr float kShrink = 0x1p-80f, kGrow = 0x1p80f, kMost = 3.4028234663852886e38f;
+
+// A row's mean and variance (of x * scale) are what they should be, or no other scale would help.
+template <int DT>
+__device__ __forceinline__ bool settled(float var, float scale) { return DT == kOutF16 || var <= kMost || scale != 1.0f; }
+
+// What (x * scale - mean) is multiplied by.  Of a scaled row eps is far below the variance's last
+// bit, except where there is none.
+__device__ __forceinline__ float rstd_of(float var, float eps, float scale) {
+    return scale == 1.0f ? 1.0f / sqrtf(var + eps) : var == 0.0f ? kGrow / sqrtf(eps) : 1.0f / sqrtf(var);
+}
+
+__device__ __forceinline__ void keep(const NormArgs& a, int64_t row, float mean, float rstd, float scale) {
+    if (scale != 1.0f) {
+        // a mean is below the largest value, its rounding may not be
+        const float m = mean * kGrow;
+        mean = __builtin_isinf(m) && !__builtin_isinf(mean) ? __builtin_copysignf(kMost, m) : m;
+        rstd *= scale;
+    }
+    a.mean[row] = mean;
+    a.rstd[row] = rstd;
+}
+
+// n of a kept row.  x - mean alone may pass fp32's range where both are near its end: such rows are
+// taken by halves.
+template <int DT>
+struct Kept {
+    float mean, rstd;
+    bool halves;
+    __device__ __forceinline__ Kept(float m, float r) : mean(m), rstd(r), halves(DT != kOutF16 && r < 0x1p-100f) {
+        if (halves) {
+            mean *= 0.5f;
+            rstd *= 2.0f;
+        }
+        // -mean rstd, n of the zeros past a row's end, has to be finite; where it is not, the row is
+        // one value throughout (any other deviation is 2^-24 of the mean at least): n is 0
+        if (DT != kOutF16 && rstd <= kMost && __builtin_fabsf(mean) * rstd > kMost) rstd = 0.0f;
+    }
+    // x, or its half
+    __device__ __forceinline__ float n(float x) const { return (x - mean) * rstd; }
+};
+
 // Rows of up to 64 * W * EPT values: a team of W waves takes a row, EPT values a thread, all of it
 // in registers between the sums; a workgroup of four teams (W = 1) or one takes every
 // gridDim.x-th row and has the next one's loads in flight while it sums.  weight and bias are
@@ -68,6 +115,15 @@ struct Team {
         else ((B*)(row + (uint32_t)(k * Vec<DT>::EB)))->v = pack_vec<DT>(x);
     }
     __device__ __forceinline__ float operator[](int j) const { return elem<DT>(v[j / E], j % E); }
+    __device__ __forceinline__ void halve() {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float h[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) h[e] = 0.5f * elem<DT>(v[i], e);
+            v[i] = pack_vec<DT>(h);
+        }
+    }
 };
 
 template <int PT, typename T>
@@ -125,31 +181,36 @@ __global__ void __launch_bounds__((Team<DT, W, EPT, TAIL>::NT)) norm_run(NormArg
     for (; row < a.rows; row += step) {
         x = next;
         next.load(a.X + (row + step) * pitch, K, row + step < a.rows);
-        float s[1] = {0.0f};
+        // one row of x, or of x / 2^80; false: its sums pass fp32's range
+        auto pass = [&](auto scaled) __attribute__((always_inline)) {
+            constexpr float F = decltype(scaled)::value ? kShrink : 1.0f;
+            float s[1] = {0.0f};
 #pragma unroll
-        for (int j = 0; j < EPT; ++j) s[0] += x[j];
-        team_sums<W, 1>(s, lds, turn);
-        const float mean = s[0] / (float)K;
-        s[0] = 0.0f;
+            for (int j = 0; j < EPT; ++j) s[0] += x[j] * F;
+            team_sums<W, 1>(s, lds, turn);
+            const float mean = s[0] / (float)K;
+            s[0] = 0.0f;
 #pragma unroll
-        for (int j = 0; j < EPT; ++j) {
-            const float c = x[j] - mean;
-            s[0] += T::at(j / T::E) + j % T::E < K ? c * c : 0.0f;
-        }
-        team_sums<W, 1>(s, lds, turn);
-        const float rstd = 1.0f / sqrtf(s[0] / (float)K + a.eps);
-        if (a.mean && (threadIdx.x & (W * 64 - 1)) == 0) {
-            a.mean[row] = mean;
-            a.rstd[row] = rstd;
-        }
+            for (int j = 0; j < EPT; ++j) {
+                const float c = x[j] * F - mean;
+                s[0] += T::at(j / T::E) + j % T::E < K ? c * c : 0.0f;
+            }
+            team_sums<W, 1>(s, lds, turn);
+            const float var = s[0] / (float)K;
+            if (!settled<DT>(var, F)) return false;
+            const float rstd = rstd_of(var, a.eps, F);
+            if (a.mean && (threadIdx.x & (W * 64 - 1)) == 0) keep(a, row, mean, rstd, F);
 #pragma unroll
-        for (int i = 0; i < T::V; ++i) {
-            float y[T::E];
+            for (int i = 0; i < T::V; ++i) {
+                float y[T::E];
 #pragma unroll
-            for (int e = 0; e < T::E; ++e)
-                y[e] = __builtin_fmaf((x[i * T::E + e] - mean) * rstd, w[i * T::E + e], b[i * T::E + e]);
-            if (T::at(i) < K) T::store(a.Y + row * pitch, T::at(i), K, y);
-        }
+                for (int e = 0; e < T::E; ++e)
+                    y[e] = __builtin_fmaf((x[i * T::E + e] * F - mean) * rstd, w[i * T::E + e], b[i * T::E + e]);
+                if (T::at(i) < K) T::store(a.Y + row * pitch, T::at(i), K, y);
+            }
+            return true;
+        };
+        if (__builtin_expect(!pass(std::false_type{}), 0)) pass(std::true_type{});
     }
 }
 
@@ -167,7 +228,15 @@ __global__ void __launch_bounds__((Team<DT, W, EPT, TAIL>::NT)) norm_back(NormAr
     // the widest teams have no registers left for the next row's loads
     constexpr bool AHEAD = W < 16 || EPT < 16;
     T x, dy, nx, ndy;
+    // a row's statistics are under way before its values: waiting for a load waits for those before it
+    // (8192 x 4096, both launches: 44.6 us, 46.4 with the next row's values in front of them)
+    float nm = 0.0f, nr = 0.0f;
+    auto statistics = [&](int64_t r, bool in) __attribute__((always_inline)) {
+        nm = in ? a.mean[r] : 0.0f;
+        nr = in ? a.rstd[r] : 0.0f;
+    };
     if constexpr (AHEAD) {
+        statistics(row, row < a.rows);
         nx.load(a.X + row * pitch, K, row < a.rows);
         ndy.load(a.dY + row * pitch, K, row < a.rows);
     }
@@ -176,21 +245,25 @@ __global__ void __launch_bounds__((Team<DT, W, EPT, TAIL>::NT)) norm_back(NormAr
 #pragma unroll
     for (int j = 0; j < EPT; ++j) dw[j] = db[j] = 0.0f;
     for (; row < a.rows; row += step) {
+        if constexpr (!AHEAD) statistics(row, true);
+        const float mean = nm, rstd = nr;
         if constexpr (AHEAD) {
+            const bool more = row + step < a.rows;
+            statistics(row + step, more);
             x = nx;
             dy = ndy;
-            const bool more = row + step < a.rows;
             nx.load(a.X + (row + step) * pitch, K, more);
             ndy.load(a.dY + (row + step) * pitch, K, more);
         } else {
             x.load(a.X + row * pitch, K, true);
             dy.load(a.dY + row * pitch, K, true);
         }
-        const float mean = a.mean[row], rstd = a.rstd[row];
+        const Kept<DT> of(mean, rstd);
+        if (__builtin_expect(of.halves, 0)) x.halve();
         float s[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < EPT; ++j) {
-            const float d = dy[j], n = (x[j] - mean) * rstd, g = d * w[j];
+            const float d = dy[j], n = of.n(x[j]), g = d * w[j];
             dw[j] = __builtin_fmaf(d, n, dw[j]);
             db[j] += d;
             s[0] += g;
@@ -204,8 +277,7 @@ __global__ void __launch_bounds__((Team<DT, W, EPT, TAIL>::NT)) norm_back(NormAr
 #pragma unroll
             for (int e = 0; e < T::E; ++e) {
                 const int j = i * T::E + e;
-                const float n = (x[j] - mean) * rstd;
-                o[e] = rstd * (dy[j] * w[j] - ms - n * mt);
+                o[e] = rstd * (dy[j] * w[j] - ms - of.n(x[j]) * mt);
             }
             if (T::at(i) < K) T::store(a.dX + row * pitch, T::at(i), K, o);
         }
@@ -281,30 +353,34 @@ __global__ void __launch_bounds__(kThreads) norm_rows(NormArgs a) {
     const int64_t row = (int64_t)blockIdx.y * gridDim.x + blockIdx.x, K = a.K;
     if (row >= a.rows) return;
     const char* x = a.X + row * K * Vec<DT>::EB;
-    float s = 0.0f;
-    for (int64_t k = threadIdx.x * E; k < K; k += kThreads * E) {
-        const u32x4 v = load_short<DT>(x, k, K);
-        for (int e = 0; e < E; ++e) s += elem<DT>(v, e);
-    }
-    const float mean = group_sum(s, lds) / (float)K;
-    s = 0.0f;
-    for (int64_t k = threadIdx.x * E; k < K; k += kThreads * E) {
-        const u32x4 v = load_short<DT>(x, k, K);
-        for (int e = 0; e < E; ++e) {
-            const float c = elem<DT>(v, e) - mean;
-            if (k + e < K) s += c * c;
+    auto pass = [&](auto scaled) __attribute__((always_inline)) {   // as in norm_run
+        constexpr float F = decltype(scaled)::value ? kShrink : 1.0f;
+        float s = 0.0f;
+        for (int64_t k = threadIdx.x * E; k < K; k += kThreads * E) {
+            const u32x4 v = load_short<DT>(x, k, K);
+            for (int e = 0; e < E; ++e) s += elem<DT>(v, e) * F;
         }
-    }
-    const float rstd = 1.0f / sqrtf(group_sum(s, lds) / (float)K + a.eps);
-    if (a.mean && threadIdx.x == 0) {
-        a.mean[row] = mean;
-        a.rstd[row] = rstd;
-    }
-    for (int64_t k = threadIdx.x; k < K; k += kThreads) {
-        const float n = (load1<DT>(x, k) - mean) * rstd;
-        const float w = a.weight ? load1<PT>(a.weight, k) : 1.0f, b = a.bias ? load1<PT>(a.bias, k) : 0.0f;
-        store1<DT>(a.Y + row * K * Vec<DT>::EB, k, __builtin_fmaf(n, w, b));
-    }
+        const float mean = group_sum(s, lds) / (float)K;
+        s = 0.0f;
+        for (int64_t k = threadIdx.x * E; k < K; k += kThreads * E) {
+            const u32x4 v = load_short<DT>(x, k, K);
+            for (int e = 0; e < E; ++e) {
+                const float c = elem<DT>(v, e) * F - mean;
+                if (k + e < K) s += c * c;
+            }
+        }
+        const float var = group_sum(s, lds) / (float)K;
+        if (!settled<DT>(var, F)) return false;
+        const float rstd = rstd_of(var, a.eps, F);
+        if (a.mean && threadIdx.x == 0) keep(a, row, mean, rstd, F);
+        for (int64_t k = threadIdx.x; k < K; k += kThreads) {
+            const float n = (load1<DT>(x, k) * F - mean) * rstd;
+            const float w = a.weight ? load1<PT>(a.weight, k) : 1.0f, b = a.bias ? load1<PT>(a.bias, k) : 0.0f;
+            store1<DT>(a.Y + row * K * Vec<DT>::EB, k, __builtin_fmaf(n, w, b));
+        }
+        return true;
+    };
+    if (__builtin_expect(!pass(std::false_type{}), 0)) pass(std::true_type{});
 }
 
 template <int DT, int PT>
@@ -312,10 +388,12 @@ __global__ void __launch_bounds__(kThreads) norm_rows_back(NormArgs a) {
     __shared__ float lds[kThreads / 64];
     const int64_t row = (int64_t)blockIdx.y * gridDim.x + blockIdx.x, K = a.K, o = row * K * Vec<DT>::EB;
     if (row >= a.rows) return;
-    const float mean = a.mean[row], rstd = a.rstd[row];
+    const float rstd = a.rstd[row];
+    const Kept<DT> of(a.mean[row], rstd);
+    const float part = of.halves ? 0.5f : 1.0f;
     float s = 0.0f, t = 0.0f;
     for (int64_t k = threadIdx.x; k < K; k += kThreads) {
-        const float n = (load1<DT>(a.X + o, k) - mean) * rstd;
+        const float n = of.n(load1<DT>(a.X + o, k) * part);
         const float g = load1<DT>(a.dY + o, k) * (a.weight ? load1<PT>(a.weight, k) : 1.0f);
         s += g;
         t += g * n;
@@ -323,7 +401,7 @@ __global__ void __launch_bounds__(kThreads) norm_rows_back(NormArgs a) {
     s = group_sum(s, lds) / (float)K;
     t = group_sum(t, lds) / (float)K;
     for (int64_t k = threadIdx.x; k < K; k += kThreads) {
-        const float n = (load1<DT>(a.X + o, k) - mean) * rstd;
+        const float n = of.n(load1<DT>(a.X + o, k) * part);
         const float g = load1<DT>(a.dY + o, k) * (a.weight ? load1<PT>(a.weight, k) : 1.0f);
         store1<DT>(a.dX + o, k, rstd * (g - s - n * t));
     }
@@ -339,7 +417,8 @@ __global__ void __launch_bounds__(kThreads) norm_columns(NormArgs a) {
     if (k < a.K)
         for (int64_t r = wave; r < a.rows; r += kThreads / 64) {
             const float dy = load1<DT>(a.dY, r * a.K + k);
-            w += dy * ((load1<DT>(a.X, r * a.K + k) - a.mean[r]) * a.rstd[r]);
+            const Kept<DT> of(a.mean[r], a.rstd[r]);
+            w += dy * of.n(load1<DT>(a.X, r * a.K + k) * (of.halves ? 0.5f : 1.0f));
             b += dy;
         }
     lds[wave][0][lane] = w;
