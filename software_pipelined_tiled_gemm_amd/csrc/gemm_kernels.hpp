@@ -148,7 +148,8 @@ __device__ __forceinline__ void dma16(const i32x4& rsrc, SPG_LDS char* lds_dst, 
 // misaligned-operand copy mode loads from a shifted window, and zeroes the elements of
 // the window that lie outside the operand's valid range in the same step.
 // Whole words are moved by selects (v_cndmask, no branches around per-lane conditions), the
-// bytes within a word by v_perm and v_alignbyte.  Every value has a name of its own: an array of
+// bytes within a word by v_perm and v_alignbyte (shr first, the register-staged gradients of 511 x
+// 1365 x 500 take 29.2 us so, 29.6 words first).  Every value has a name of its own: an array of
 // words here once made the compiler keep a staged k-tile (stage_regs) in scratch memory, all of it
 // (fp16 3000x5000x1001 -> fp32: 72 us, 41 as here).
 // Not with 64-bit shifts: as two v_lshlrev_b64 by a lane's own amount one after the other, some
@@ -168,10 +169,10 @@ __device__ __forceinline__ u32x4 shl128(u32x4 v, uint32_t bits) {
 __device__ __forceinline__ u32x4 shr128(u32x4 v, uint32_t bits) {
     const uint32_t bytes = bits >> 3;
     const bool one = bits & 32u, two = bits & 64u;
-    const uint32_t a0 = one ? v.y : v.x, a1 = one ? v.z : v.y, a2 = one ? v.w : v.z, a3 = one ? 0u : v.w;
-    const uint32_t b0 = two ? a2 : a0, b1 = two ? a3 : a1, b2 = two ? 0u : a2, b3 = two ? 0u : a3;
-    return u32x4{__builtin_amdgcn_alignbyte(b1, b0, bytes), __builtin_amdgcn_alignbyte(b2, b1, bytes),
-                 __builtin_amdgcn_alignbyte(b3, b2, bytes), __builtin_amdgcn_alignbyte(0u, b3, bytes)};
+    const uint32_t a0 = __builtin_amdgcn_alignbyte(v.y, v.x, bytes), a1 = __builtin_amdgcn_alignbyte(v.z, v.y, bytes);
+    const uint32_t a2 = __builtin_amdgcn_alignbyte(v.w, v.z, bytes), a3 = __builtin_amdgcn_alignbyte(0u, v.w, bytes);
+    const uint32_t b0 = one ? a1 : a0, b1 = one ? a2 : a1, b2 = one ? a3 : a2, b3 = one ? 0u : a3;
+    return u32x4{two ? b2 : b0, two ? b3 : b1, two ? 0u : b2, two ? 0u : b3};
 }
 
 // Wait until at most N vector-memory instructions of this wave are outstanding.

@@ -584,15 +584,27 @@ __device__ __forceinline__ void product_tile_of(ProductArgs args, int tm, int tn
         // only the last k-tile and the last column tile have chunks to realign: a 128-bit
         // shift by a lane's own amount is about 20 instructions, and doing it for every
         // chunk took longer than the multiplications of the small tiles
+        auto put = [&](auto jc, const u32x4& v) __attribute__((always_inline)) { *(SPG_LDS u32x4*)(lds_dst(s, jc) + lane * 16) = v; };
+        // realigned where they are staged, so that every chunk is stored as it comes in: with stores of
+        // their own on both ways the compiler waits for all of them first (300 x 2731 x 1001, gated:
+        // 12.6 us, 12.3 so).  Not for rows by group (1620 in 64 groups, 10560 columns of 49, gated: 119 us
+        // so, 94 with both ways): of short reductions the k-tile that is realigned is all there is
+        if constexpr (!SKIP) {
+            if (lb != 128 || cut)
+                static_for<0, L>([&](auto jc) {
+                    constexpr int j = decltype(jc)::value;
+                    staged[p][j] = shr128(staged[p][j], src_shift(jc, j < A_OPS ? la : lb));
+                });
+            static_for<0, L>([&](auto jc) { put(jc, staged[p][decltype(jc)::value]); });
+            return;
+        }
         if (lb == 128 && !cut) {
-            static_for<0, L>([&](auto jc) {
-                *(SPG_LDS u32x4*)(lds_dst(s, jc) + lane * 16) = staged[p][decltype(jc)::value];
-            });
+            static_for<0, L>([&](auto jc) { put(jc, staged[p][decltype(jc)::value]); });
             return;
         }
         static_for<0, L>([&](auto jc) {
             constexpr int j = decltype(jc)::value;
-            *(SPG_LDS u32x4*)(lds_dst(s, jc) + lane * 16) = shr128(staged[p][j], src_shift(jc, j < A_OPS ? la : lb));
+            put(jc, shr128(staged[p][j], src_shift(jc, j < A_OPS ? la : lb)));
         });
     };
 
