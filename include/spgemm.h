@@ -325,8 +325,8 @@ gemm_status gemm_quantize_rows(const void* X, gemm_dtype dtype, int64_t rows, in
  * waits for them).  Groups may be empty, and rows may be left over in front of the first
  * group and behind the last: no call writes them, and what they hold changes nothing.  Offsets
  * outside 0 .. rows count as the nearest of the two, and a group that would end before it
- * starts is empty; where groups overlap, their rows' results are not specified, but nothing
- * outside the operands is touched. */
+ * starts is empty; where groups overlap no row's result is specified (a matrix's gradient is its
+ * own group's all the same), and nothing outside the operands is touched. */
 
 typedef struct gemm_norm_plan* gemm_norm_handle;
 typedef struct gemm_route_plan* gemm_route_handle;
@@ -339,7 +339,8 @@ typedef struct gemm_combine_plan* gemm_combine_handle;
  *     Y = (X - mean) * rstd * weight + bias
  * X, Y [rows,K] of dtype (fp16, bf16, fp32); weight, bias [K] of param_dtype (dtype or fp32),
  * either NULL for 1 and 0.  Statistics in fp32, the mean subtracted before the squares are
- * summed; each result rounded once.  A row with an infinity or a NaN gives NaN.
+ * summed; each result rounded once.  Rows of finite values of any size keep to the formula (an rstd
+ * below 2^-126 has fewer bits); a row with an infinity or a NaN gives NaN.
  * Errors: INVALID_ARG (out NULL, negative size, unknown types, eps negative or not finite),
  * UNSUPPORTED (a size above 2^30 - 513). */
 gemm_status gemm_norm_create(gemm_norm_handle* out, int64_t rows, int64_t K, gemm_dtype dtype, gemm_dtype param_dtype,
