@@ -93,8 +93,9 @@ double row_tiles(const RowsShape& s, int BM) {
 // idle (a k-tile's copies have to come in), `busy` and `tile` (a workgroup's start and store) one
 // that fills them, and the matrices' reading (writing, for their gradients) at bw bytes a
 // microsecond the rest.  Fitted to every class at 2500 drawn shapes (1 to 256 groups, 1 to 8192
-// rows, matrices of 48 to 12288 x 40 to 4096); of the classes' measured times the choice takes
-// 2.0% more than the best on average, 14% more at 5% of the shapes.
+// rows, matrices of 48 to 12288 x 40 to 4096).  Against the best of all classes, parts and the
+// streaming kernel at 2500 other shapes, three in ten of them with few tiles and long reductions,
+// the choice takes 4.2% more on average and 22% more at 5% of the shapes; for the gradients, 1.9% and 10%.
 struct Cost {
     double alone, busy, tile, base, bw;   // bw 0: the class is not chosen
 };
@@ -148,7 +149,7 @@ double rows_wgs(const RowsShape& s, int t) {
 // last round, too: past 12 rounds one is less than 8% of the call.  At 400 drawn shapes (1 to 32
 // groups, 1 to 2048 rows, matrices of 32 to 2048 columns and reductions of 1024 to 12288) the best
 // class with parts takes 0.27 to 1 of the time of the best without (5 columns of 736, 9728:
-// 13 and 37 us), and the choice 4.6% more than the best on average.
+// 13 and 37 us).
 // The matrices' gradients likewise (12432 rows of one group, 144 x 776, both gradients: 33 us, 77
 // in one piece).
 constexpr double kJoinUs[spg::kGroupTiles] = {0, 0, 0, 4.5, 4.0, 0, 3.5};   // the parts' launch, write and read; 0: not split
@@ -492,8 +493,7 @@ gemm_status simple_weights(const Common& c, const void* D, int64_t ldd, const vo
 // matrices keep its workgroups busy enough to go on up to 4096 (single rows, 12288 x 4096: 70 us
 // against 81; of 2000 to 3500 reductions the same time).  A workgroup reads its columns one
 // chunk after the other, and where there are few of them and much to read, tiles in parts are
-// faster (72 rows of 5 groups, two matrices 96 x 12024: 86 us against 16).  Over 1300 shapes
-// this choice and that of the tiles take 4.0% more than the best.
+// faster (72 rows of 5 groups, two matrices 96 x 12024: 86 us against 16).
 bool streams(const Common& c, int64_t N, int64_t K, int mats, bool along) {
     if (!along || c.rows > 16 * c.live()) return false;
     const int64_t columns = ceil_div(N, 16);

@@ -225,7 +225,9 @@ __global__ void __launch_bounds__((Team<DT, W, EPT, TAIL>::NT)) norm_back(NormAr
     const int64_t step = (int64_t)gridDim.x * T::TEAMS, pitch = a.K * Vec<DT>::EB;
     int64_t row = (int64_t)blockIdx.x * T::TEAMS + team;
     int turn = 0;
-    // the widest teams have no registers left for the next row's loads
+    // the widest teams have no registers left for the next row's loads, and with rows that end inside
+    // a vector not for all of their own: of fp16 and fp32 they keep 28 to 56 bytes a lane in scratch
+    // (2048 x 16383 fp16: 70 us, bf16, which keeps none, 67; 16384 columns 55)
     constexpr bool AHEAD = W < 16 || EPT < 16;
     T x, dy, nx, ndy;
     // a row's statistics are under way before its values: waiting for a load waits for those before it
